@@ -78,7 +78,9 @@ enum {
                                   token's sequence id outside [0, B); entry masked */
   DSA_DEV_ERR_TIMEOUT = 4,     /* a bounded wait inside a kernel gave up; the outputs of
                                   that call are not valid */
-  DSA_DEV_ERR_SLOT_RANGE = 8   /* writer slot >= pool_rows; the row was not written */
+  DSA_DEV_ERR_SLOT_RANGE = 8,  /* writer slot >= pool_rows; the row was not written */
+  DSA_DEV_ERR_LENGTH = 16,     /* a request length, token count or query offset out of range */
+  DSA_DEV_ERR_NO_PAGES = 32    /* the free-page stack cannot serve (or hold) the call's pages */
 };
 
 /* Human-readable name of a status code (static string). */
@@ -300,6 +302,157 @@ int dsa_sparse_attn_decode_noalloc(const void* q_bf16_dev, int T, int H, int D,
                                    const int32_t* token_seq_dev, const int32_t* topk_dev, int K,
                                    float sm_scale, void* o_bf16_dev, float* lse_dev,
                                    int32_t* err_flag_dev, void* stream);
+
+/* ------------------------------------------- page tables and slot maps */
+
+/* Largest number of requests of one page-table call. */
+#define DSA_MAX_REQUESTS 16384
+
+/* Hands pages to a step's requests and builds the step's slot map, on the
+ * GPU, from lengths that only the GPU need know.  Request b holds
+ * seq_lens[b] tokens, ceil(seq_lens[b] / page_size) pages of its page-table
+ * row, and gets new_lens[b] tokens.  Pages come off the top of a stack of
+ * free physical pages, request by request and page by page: the k-th page of
+ * the call (k = 0, 1, ...) is free_pages[free_count - 1 - k].  With
+ * cu_q[b] = new_lens[0] + ... + new_lens[b - 1], token t of request b
+ * (cu_q[b] <= t < cu_q[b + 1]) gets
+ *   positions[t] = seq_lens[b] + t - cu_q[b],   token_seq[t] = b,
+ *   slots[t]     = page_table[b][positions[t] / page_size] * page_size
+ *                  + positions[t] % page_size;
+ * the rows [cu_q[B], T) of the three are padding: position 0, sequence -1,
+ * slot -1 (the writers skip it).  kv_lens[b] = seq_lens[b] + new_lens[b].
+ * All or nothing: when a length is negative, a request outgrows its row
+ * (max_pages * page_size tokens), cu_q[B] exceeds T or free_count is outside
+ * [0, free_cap] (DSA_DEV_ERR_LENGTH), or the stack holds too few pages
+ * (DSA_DEV_ERR_NO_PAGES), no page is handed out: page_table stays as it was,
+ * free_count_out = free_count, every token row is padding, cu_q is 0
+ * throughout and kv_lens = seq_lens.  A page id below 0 (in the stack or in
+ * the row entry of a partly filled page) sets DSA_DEV_ERR_PAGE_RANGE and
+ * gives its tokens slot -1.
+ *   seq_lens_dev, new_lens_dev  [B] int32; B >= 1, at most DSA_MAX_REQUESTS.
+ *   page_table_dev      [B, max_pages] int32; new pages are stored, other
+ *                       entries are left as they are.
+ *   free_pages_dev      [free_cap] int32, read.
+ *   free_count_dev      int32, read; free_count_out_dev int32, written; they
+ *                       may be one address (the update of a captured step).
+ *   slots_dev           [T] int64;  positions_dev, token_seq_dev [T] int32.
+ *   cu_q_dev            [B + 1] int32.
+ *   kv_lens_dev         [B] int32; may be seq_lens_dev.
+ * Buffers named otherwise do not overlap. */
+int dsa_pages_extend(const int32_t* seq_lens_dev, const int32_t* new_lens_dev, int B,
+                     int32_t* page_table_dev, int max_pages, int page_size,
+                     const int32_t* free_pages_dev, int free_cap, const int32_t* free_count_dev,
+                     int32_t* free_count_out_dev, int T, int64_t* slots_dev, int32_t* positions_dev,
+                     int32_t* token_seq_dev, int32_t* cu_q_dev, int32_t* kv_lens_dev,
+                     int32_t* err_flag_dev, void* stream);
+
+/* Returns the pages of finished requests to the stack, request by request and
+ * page by page: free_pages[free_count + k] = the call's k-th page.
+ * free_count_out = free_count + pages returned; seq_lens_out[b] = 0 for a
+ * finished request, seq_lens[b] for the others; the page table is read only
+ * (its rows are stale for a request of length 0).  A page belongs to one
+ * request: pages that requests share are not counted.  All or nothing: a
+ * length outside [0, max_pages * page_size] or free_count outside
+ * [0, free_cap] (DSA_DEV_ERR_LENGTH), a page id below 0
+ * (DSA_DEV_ERR_PAGE_RANGE) or a stack without room (DSA_DEV_ERR_NO_PAGES)
+ * leaves free_pages as it was and copies free_count and seq_lens.
+ *   finished_dev   [B] bytes, non-zero = finished.
+ *   free_pages_dev [free_cap] int32, written above free_count.
+ *   free_count_out_dev may be free_count_dev, seq_lens_out_dev seq_lens_dev. */
+int dsa_pages_release(const uint8_t* finished_dev, const int32_t* seq_lens_dev, int B,
+                      const int32_t* page_table_dev, int max_pages, int page_size,
+                      int32_t* free_pages_dev, int free_cap, const int32_t* free_count_dev,
+                      int32_t* free_count_out_dev, int32_t* seq_lens_out_dev, int32_t* err_flag_dev,
+                      void* stream);
+
+/* ------------------------------------------------- rotary positions */
+
+/* Rotary embedding of the 64 RoPE dims, with positions of up to 8 axes (one
+ * for text; time, height and width for images and video).  Pair i turns by
+ * the angle positions[axis[i]][t] * inv_freq[i]:
+ *   (a, b) -> mscale * (a cos - b sin, b cos + a sin),
+ * where (a, b) are dims (2 i, 2 i + 1) if interleaved, else (i, i + 32).
+ * The angle is reduced exactly (64-bit fixed-point turns), so positions of
+ * any size keep full precision. */
+typedef struct {
+  double inv_freq[32]; /* radians a position step; finite */
+  int32_t axis[32];    /* in [0, n_axes) */
+  int32_t n_axes;      /* 1 to 8 */
+  int32_t interleaved; /* 0 or 1 */
+  float mscale;        /* factor on cos and sin (1 without context scaling) */
+} dsa_rope;
+
+/* One launch between the projections and the attention over 656-byte rows:
+ * the queries' RoPE part is turned and joined to the latent part, and the new
+ * tokens' rows are turned, quantised and written to the pool.
+ *   q_out[t][h]    = q_nope[t][h] (512 dims), then the turned q_pe[t][h] (64);
+ *   pool[slots[t]] = the 656-byte row dsa_kv_write_rope656 makes of kv_c[t]
+ *                    and the turned k_pe[t]; slot < 0 skips the row, slot >=
+ *                    pool_rows sets DSA_DEV_ERR_SLOT_RANGE and skips it.
+ * Turned values are rounded to BF16 once.  Strides are in elements; the last
+ * dim is contiguous.
+ *   rope           host memory, read during the call.
+ *   positions_dev  [n_axes, T] int32, row stride pos_stride (0: one row for every axis).
+ *   q_pe_dev       [T, H, 64] BF16, 4-byte aligned, even strides; NULL with
+ *                  q_out_dev NULL: no queries.
+ *   q_nope_dev     [T, H, 512] BF16, 16-byte aligned, strides multiples of 8;
+ *                  NULL leaves q_out's first 512 dims as they are.
+ *   q_out_dev      [T, H, 576] BF16, contiguous, 16-byte aligned; overlaps no input.
+ *   kv_c_dev       [T, 512] BF16, 16-byte aligned, stride a multiple of 8; NULL
+ *                  with k_pe_dev, slots_dev and pool_dev NULL: no rows.
+ *   k_pe_dev       [T, 64] BF16, 4-byte aligned, even stride.
+ *   slots_dev      [T] int64, distinct where >= 0.
+ *   pool_dev       [pool_rows, 656] bytes, 16-byte aligned.
+ * H >= 1.  T == 0 is a no-op. */
+int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t pos_stride, int T, int H,
+                    const void* q_nope_dev, int64_t q_nope_stride_t, int64_t q_nope_stride_h,
+                    const void* q_pe_dev, int64_t q_pe_stride_t, int64_t q_pe_stride_h, void* q_out_dev,
+                    const void* kv_c_dev, int64_t kv_c_stride, const void* k_pe_dev, int64_t k_pe_stride,
+                    const int64_t* slots_dev, void* pool_dev, int64_t pool_rows, int32_t* err_flag_dev,
+                    void* stream);
+
+/* ------------------------------------------- dense attention of new tokens */
+
+/* Workspace bytes of dsa_chunk_attn for T query tokens of B requests with H
+ * heads on the current device: the work list and the partial results of
+ * query groups that are spread over several SMs.  0 for a size out of range. */
+size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
+
+/* Dense causal MLA attention of each request's new tokens over everything the
+ * request holds in the paged pool (the new tokens' rows are written first).
+ * Serves prompts, chunks of prompts, drafted tokens and single tokens; batches
+ * may mix them.  Request b's queries are the rows [cu_q[b], cu_q[b + 1]), the
+ * last n_b = cu_q[b + 1] - cu_q[b] of its kv_lens[b] tokens.  Its i-th query
+ * sees the keys j <= kv_lens[b] - n_b + i (j < kv_lens[b] when causal is 0):
+ *   row_j  = page_table[b][j / page_size] * page_size + j % page_size;
+ *   s_j    = sm_scale * <q, k_j>,  LSE = log(sum_j exp(s_j)),
+ *   O      = sum_j exp(s_j - LSE) * v_j,
+ * with k_j, v_j the dequantised row as in dsa_sparse_attn_decode (over
+ * 656-byte rows 576-wide keys, 512-wide values).  A query that sees no key
+ * (n_b > kv_lens[b]) gets O = 0 and LSE = -inf.  Rows of q outside
+ * [cu_q[0], cu_q[B]) belong to no request; their O and LSE are left as they are.
+ * A key that a query does not see changes nothing in its result, whatever the
+ * row holds.
+ * Lengths are read on the GPU: a captured call serves any lengths within the
+ * sizes it was captured with.  A key whose page-table entry is negative or
+ * lies beyond the pool is masked (DSA_DEV_ERR_PAGE_RANGE).  A request whose
+ * [cu_q[b], cu_q[b + 1]) is not an ascending range within [0, T] is skipped, a
+ * kv_lens[b] below 0 counts as 0 and one above max_pages * page_size as that
+ * (DSA_DEV_ERR_LENGTH).  Ranges of requests do not overlap.
+ *   q_bf16_dev      [T, H, 512] BF16, [T, H, 576] over 656-byte rows; 16-byte aligned.
+ *   H               1 to 1024.
+ *   page_table_dev  [B, max_pages] int32.
+ *   cu_q_dev        [B + 1] int32;  kv_lens_dev [B] int32; B <= DSA_MAX_REQUESTS.
+ *   o_bf16_dev      [T, H, 512] BF16 out, 16-byte aligned;  lse_dev [T, H] float out.
+ *   workspace_dev   ws_bytes >= dsa_chunk_attn_workspace_bytes(T, H, B, layout),
+ *                   256-byte aligned, written before it is read; calls that may
+ *                   overlap on the GPU need a workspace each.
+ * T == 0 is a no-op. */
+int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool_dev, int64_t pool_rows,
+                   int layout, int kv_row_dim, const int32_t* page_table_dev, int B, int max_pages,
+                   int page_size, const int32_t* cu_q_dev, const int32_t* kv_lens_dev, int causal,
+                   float sm_scale, void* o_bf16_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes,
+                   int32_t* err_flag_dev, void* stream);
 
 #if defined(__GNUC__)
 #pragma GCC visibility pop

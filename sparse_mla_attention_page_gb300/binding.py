@@ -26,6 +26,8 @@ DSA_DEV_ERR_INDEX_RANGE = 1
 DSA_DEV_ERR_PAGE_RANGE = 2
 DSA_DEV_ERR_TIMEOUT = 4
 DSA_DEV_ERR_SLOT_RANGE = 8
+DSA_DEV_ERR_LENGTH = 16
+DSA_DEV_ERR_NO_PAGES = 32
 
 _lock = threading.Lock()
 _lib = None
@@ -36,7 +38,14 @@ EXPORTS = (
     "dsa_quantize_q8", "dsa_sparse_attn_workspace_bytes", "dsa_sparse_attn_decode",
     "dsa_sparse_attn_prefill_q8", "dsa_gather_dequant_workspace_bytes", "dsa_gather_dequant",
     "dsa_sparse_attn_decode_noalloc", "dsa_set_wait_limit_ns",
+    "dsa_pages_extend", "dsa_pages_release", "dsa_rope_qkv656", "dsa_chunk_attn_workspace_bytes", "dsa_chunk_attn",
 )
+
+
+class DsaRope(ctypes.Structure):
+    """dsa_rope of include/dsa.h; ``rope_spec`` fills one."""
+    _fields_ = [("inv_freq", ctypes.c_double * 32), ("axis", ctypes.c_int32 * 32), ("n_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float)]
 
 
 class DsaError(RuntimeError):
@@ -91,6 +100,18 @@ def lib() -> ctypes.CDLL:
             L.dsa_sparse_attn_decode_noalloc.argtypes = [
                 vp, i32, i32, i32, vp, i64, i32, i32, vp, i32, i32, i32, vp, vp, i32,
                 c.c_float, vp, vp, vp, vp]
+            L.dsa_pages_extend.restype = i32
+            L.dsa_pages_extend.argtypes = [vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+            L.dsa_pages_release.restype = i32
+            L.dsa_pages_release.argtypes = [vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+            L.dsa_rope_qkv656.restype = i32
+            L.dsa_rope_qkv656.argtypes = [c.POINTER(DsaRope), vp, i64, i32, i32, vp, i64, i64, vp, i64, i64, vp,
+                                          vp, i64, vp, i64, vp, vp, i64, vp, vp]
+            L.dsa_chunk_attn_workspace_bytes.restype = c.c_size_t
+            L.dsa_chunk_attn_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.dsa_chunk_attn.restype = i32
+            L.dsa_chunk_attn.argtypes = [vp, i32, i32, i32, vp, i64, i32, i32, vp, i32, i32, i32, vp, vp, i32,
+                                         c.c_float, vp, vp, vp, c.c_size_t, vp, vp]
             _lib = L
     return _lib
 
@@ -312,3 +333,135 @@ def dsa_sparse_attn_decode_noalloc(q_bf16, pool, layout, topk, sm_scale, o, lse,
         _ptr(page_table), B, max_pages, page_size, _ptr(token_seq), _ptr(topk), topk.shape[1],
         float(sm_scale), _ptr(o), _ptr(lse), _ptr(err_flag), _stream(stream))
     _check(st, "dsa_sparse_attn_decode_noalloc")
+
+
+# ------------------------------------------------ dense serving operators
+
+def _arg(t, name: str, dtype: torch.dtype, shape=None, device=None, optional=False, strided=False):
+    """Address of a CUDA tensor of the given type and shape (None entries: any size),
+    on the current device; contiguous unless ``strided`` (then its last dim is)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's device is cuda:{device}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if strided:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dim")
+    elif not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call_device(stream):
+    """(the current device, the stream's address on it)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return torch.cuda.current_device(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def dsa_pages_extend(seq_lens, new_lens, page_table, page_size, free_pages, free_count, free_count_out, slots,
+                     positions, token_seq, cu_q, kv_lens, err_flag=None, stream=None) -> None:
+    """Pages for new_lens [B] more tokens of requests that hold seq_lens [B], off the stack
+    free_pages[:free_count], into page_table [B, max_pages]; and the step's token rows: slots (int64),
+    positions and token_seq [T], cu_q [B + 1] and kv_lens [B] (see include/dsa.h).  free_count_out may be
+    free_count, kv_lens may be seq_lens."""
+    dev, s = _call_device(stream)
+    i32 = torch.int32
+    B, T = seq_lens.shape[0], slots.shape[0]
+    p = [_arg(seq_lens, "seq_lens", i32, (None,), dev), _arg(new_lens, "new_lens", i32, (B,), dev), B,
+         _arg(page_table, "page_table", i32, (B, None), dev), page_table.shape[1], page_size,
+         _arg(free_pages, "free_pages", i32, (None,), dev), free_pages.shape[0],
+         _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev), T,
+         _arg(slots, "slots", torch.int64, (T,), dev), _arg(positions, "positions", i32, (T,), dev),
+         _arg(token_seq, "token_seq", i32, (T,), dev), _arg(cu_q, "cu_q", i32, (B + 1,), dev),
+         _arg(kv_lens, "kv_lens", i32, (B,), dev), _arg(err_flag, "err_flag", i32, None, dev, True)]
+    _check(lib().dsa_pages_extend(*p, s), "dsa_pages_extend")
+
+
+def dsa_pages_release(finished, seq_lens, page_table, page_size, free_pages, free_count, free_count_out, seq_lens_out,
+                      err_flag=None, stream=None) -> None:
+    """Pushes the pages of the finished requests (bool [B]) onto the stack free_pages[:free_count] (see
+    include/dsa.h).  free_count_out may be free_count, seq_lens_out may be seq_lens."""
+    dev, s = _call_device(stream)
+    i32 = torch.int32
+    B = seq_lens.shape[0]
+    p = [_arg(finished, "finished", torch.bool, (B,), dev), _arg(seq_lens, "seq_lens", i32, (None,), dev), B,
+         _arg(page_table, "page_table", i32, (B, None), dev), page_table.shape[1], page_size,
+         _arg(free_pages, "free_pages", i32, (None,), dev), free_pages.shape[0],
+         _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev),
+         _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev), _arg(err_flag, "err_flag", i32, None, dev, True)]
+    _check(lib().dsa_pages_release(*p, s), "dsa_pages_release")
+
+
+def rope_spec(theta=10000.0, sections=(32,), interleaved=False, inv_freq=None, axis=None, mscale=1.0) -> DsaRope:
+    """The rotary embedding of the 64 RoPE dims: pair i turns by positions[axis[i]] * inv_freq[i] radians.
+    ``sections`` gives the first sections[0] pairs axis 0, the next sections[1] axis 1, ...; ``axis`` (32
+    entries) sets any other assignment.  ``inv_freq`` (32 entries) replaces theta^(-i / 32)."""
+    if axis is None:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    axis = [int(a) for a in axis]
+    inv_freq = [float(theta) ** (-i / 32.0) for i in range(32)] if inv_freq is None else [float(f) for f in inv_freq]
+    if len(axis) != 32 or len(inv_freq) != 32:
+        raise ValueError("a rotary spec has 32 pairs: sections sum to 32, axis and inv_freq have 32 entries")
+    return DsaRope((ctypes.c_double * 32)(*inv_freq), (ctypes.c_int32 * 32)(*axis), max(max(axis) + 1, len(sections)),
+                   int(bool(interleaved)), mscale)
+
+
+def dsa_rope_qkv656(q_nope, q_pe, q_out, kv_c, k_pe, slots, pool, positions, rope, err_flag=None, stream=None) -> None:
+    """q_out [T, H, 576] <- q_nope [T, H, 512] and the turned q_pe [T, H, 64]; pool [rows, 656] <- the rows of
+    kv_c [T, 512] and the turned k_pe [T, 64] at ``slots``; positions int32 [axes, T] (see include/dsa.h).
+    q_nope None leaves q_out's latent part; q_pe and q_out None, or kv_c, k_pe, slots and pool None, leave that
+    side out."""
+    dev, s = _call_device(stream)
+    bf = torch.bfloat16
+    side = kv_c if q_pe is None else q_pe
+    if side is None:
+        raise ValueError("neither queries nor rows given")
+    T, H = side.shape[0], 1 if q_pe is None else q_pe.shape[1]
+    pos = _arg(positions, "positions", torch.int32, (rope.n_axes, T), dev, strided=True)
+    qn = _arg(q_nope, "q_nope", bf, (T, H, 512), dev, True, True)
+    qp = _arg(q_pe, "q_pe", bf, (T, H, 64), dev, True, True)
+    qo = _arg(q_out, "q_out", bf, (T, H, 576), dev, True)
+    kc = _arg(kv_c, "kv_c", bf, (T, 512), dev, True, True)
+    kp = _arg(k_pe, "k_pe", bf, (T, 64), dev, True, True)
+    sl = _arg(slots, "slots", torch.int64, (T,), dev, True)
+    po = _arg(pool, "pool", torch.uint8, (None, 656), dev, True)
+    st = (lambda t, d: 0 if t is None or t.shape[d] == 1 else t.stride(d))
+    _check(lib().dsa_rope_qkv656(ctypes.byref(rope), pos, st(positions, 0), T, H, qn, st(q_nope, 0),
+                                 st(q_nope, 1), qp, st(q_pe, 0), st(q_pe, 1), qo, kc, st(kv_c, 0), kp, st(k_pe, 0),
+                                 sl, po, 0 if pool is None else pool.shape[0],
+                                 _arg(err_flag, "err_flag", torch.int32, None, dev, True), s), "dsa_rope_qkv656")
+
+
+def dsa_chunk_attn_workspace_bytes(T: int, H: int, B: int, layout) -> int:
+    return int(lib().dsa_chunk_attn_workspace_bytes(T, H, B, LAYOUTS.get(layout, layout)))
+
+
+def chunk_workspace_for(T: int, H: int, B: int, layout, device=None) -> torch.Tensor:
+    """A device workspace for dsa_chunk_attn of up to T tokens of B requests."""
+    return torch.empty(dsa_chunk_attn_workspace_bytes(T, H, B, layout), dtype=torch.uint8, device=device or "cuda")
+
+
+def dsa_chunk_attn(q_bf16, pool, layout, page_table, page_size, cu_q, kv_lens, sm_scale, o, lse, workspace,
+                   causal=True, err_flag=None, stream=None) -> None:
+    """Dense attention of each request's new tokens, q [T, H, 512 or 576] rows cu_q[b]:cu_q[b + 1], over its
+    kv_lens[b] rows of the paged pool (see include/dsa.h)."""
+    dev, s = _call_device(stream)
+    lay = LAYOUTS.get(layout, layout)
+    qp = _arg(q_bf16, "q_bf16", torch.bfloat16, (None, None, 576 if lay == DSA_KV_ROPE656 else 512), dev)
+    T, H, D = q_bf16.shape
+    i32 = torch.int32
+    pp = _arg(pool, "pool", torch.uint8, (None, None), dev)
+    tp = _arg(page_table, "page_table", i32, (None, None), dev)
+    B, max_pages = page_table.shape
+    _check(lib().dsa_chunk_attn(qp, T, H, D, pp, pool.shape[0], lay, _kv_row_dim(pool, lay), tp, B, max_pages,
+                                page_size, _arg(cu_q, "cu_q", i32, (B + 1,), dev),
+                                _arg(kv_lens, "kv_lens", i32, (B,), dev), int(causal), sm_scale,
+                                _arg(o, "o", torch.bfloat16, (T, H, 512), dev),
+                                _arg(lse, "lse", torch.float32, (T, H), dev),
+                                _arg(workspace, "workspace", torch.uint8, (None,), dev), workspace.shape[0],
+                                _arg(err_flag, "err_flag", i32, None, dev, True), s), "dsa_chunk_attn")

@@ -7,46 +7,10 @@
 // 1 KiB read + 512 (528) bytes written per row.
 #include "dsa_common.cuh"
 #include "kernels.h"
+#include "row_codec.cuh"
 
 namespace dsa {
 namespace {
-
-struct Row16 {
-  float v[16];  // v[0..7]: dims 8l..8l+7, v[8..15]: dims 256+8l..256+8l+7
-};
-
-__device__ __forceinline__ void load_row16(const uint16_t* __restrict__ row, int lane, Row16& r) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(row) + lane);
-  const uint4 b = __ldcs(reinterpret_cast<const uint4*>(row + 256) + lane);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    r.v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-    r.v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
-  }
-}
-
-// Four floats -> four E4M3 bytes (saturating round-to-nearest-even); a NaN
-// input gives the FN NaN code 0x7F with the input's sign bit (the cvt
-// instruction alone returns 0x7F for NaN of either sign).
-__device__ __forceinline__ uint32_t e4m3x4_keep_nan_sign(float a, float b, float c, float d) {
-  uint32_t r = e4m3x4_satrne(a, b, c, d);
-  const float v[4] = {a, b, c, d};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (v[i] != v[i]) r = (r & ~(0xFFu << (8 * i))) | ((0x7Fu | ((__float_as_uint(v[i]) >> 31) << 7)) << (8 * i));
-  return r;
-}
-
-__device__ __forceinline__ void store_row16(uint8_t* __restrict__ row, int lane, const Row16& r) {
-  uint2 lo, hi;
-  lo.x = e4m3x4_keep_nan_sign(r.v[0], r.v[1], r.v[2], r.v[3]);
-  lo.y = e4m3x4_keep_nan_sign(r.v[4], r.v[5], r.v[6], r.v[7]);
-  hi.x = e4m3x4_keep_nan_sign(r.v[8], r.v[9], r.v[10], r.v[11]);
-  hi.y = e4m3x4_keep_nan_sign(r.v[12], r.v[13], r.v[14], r.v[15]);
-  reinterpret_cast<uint2*>(row)[lane] = lo;
-  reinterpret_cast<uint2*>(row + 256)[lane] = hi;
-}
 
 // The KV writers let the next kernel in the stream, when it is launched as a
 // programmatic dependent (the attention kernels are), start its set-up at
@@ -86,8 +50,6 @@ __global__ void __launch_bounds__(256, 4) kv_write_raw_kernel(
   }
 }
 
-// Group g of 128 dims is held by 16 lanes: groups 0 and 2 by lanes 0-15
-// (first and second half of their registers), groups 1 and 3 by lanes 16-31.
 // kRope: 656-byte rows, whose input rows are 576 wide; the 64 RoPE dims are
 // stored as they are (BF16) after the scales, one 4-byte pair per lane.
 template <bool kRope>
@@ -105,34 +67,12 @@ __global__ void __launch_bounds__(256, 4) kv_write_scaled_kernel(
       if (lane == 0) set_err(err, DSA_DEV_ERR_SLOT_RANGE);
       return;
     }
-    float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      a0 = fmaxf(a0, fabsf(r.v[k]));
-      a1 = fmaxf(a1, fabsf(r.v[8 + k]));
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
-      a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
-    }
-    const float s0 = a0 == 0.f ? 0.f : __fdiv_rn(a0, 448.0f);
-    const float s1 = a1 == 0.f ? 0.f : __fdiv_rn(a1, 448.0f);
-    // copysignf: the same quotient (s > 0), and a NaN keeps its input's sign
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      r.v[k] = s0 == 0.f ? 0.f : copysignf(__fdiv_rn(r.v[k], s0), r.v[k]);
-      r.v[8 + k] = s1 == 0.f ? 0.f : copysignf(__fdiv_rn(r.v[8 + k], s1), r.v[8 + k]);
-    }
+    float s0, s1;
+    quantise_groups(r, s0, s1);
     uint8_t* row = pool + s * kRowBytes;
     store_row16(row, lane, r);
     if (kRope) reinterpret_cast<uint32_t*>(row + kScaledRow)[lane] = rope_pair;
-    const float g1 = __shfl_sync(0xffffffffu, s0, 16);
-    const float g3 = __shfl_sync(0xffffffffu, s1, 16);
-    if (lane == 0) {
-      float4 sc = make_float4(s0, g1, s1, g3);
-      *reinterpret_cast<float4*>(row + 512) = sc;
-    }
+    store_scales(row, lane, s0, s1);
   };
   // two rows per warp and pass, all loads issued before any is used
   for (int64_t i0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i0 < n_rows; i0 += 2 * nwarps) {

@@ -1,0 +1,332 @@
+"""Dense attention of new tokens over the paged pool against the formula in 64 bits."""
+import math
+import random
+
+import pytest
+import torch
+
+import dense_ref as ref
+from sparse_mla_attention_page_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+LAYOUTS = ["raw512", "scaled528", "rope656"]
+SCALE = 1 / math.sqrt(576.0)
+BF = torch.bfloat16
+
+
+def make(new, ctx, H, layout, page=64, seed=0, qamp=1.0, amp=1.0, lead=0, tail=0):
+    """Requests of new[b] tokens after ctx[b] cached ones; `lead` and `tail` query rows belong to none."""
+    g = torch.Generator().manual_seed(seed)
+    kv = [n + c for n, c in zip(new, ctx)]
+    need = [ref.pages_of(max(k, 0), page) for k in kv]
+    n_pages = sum(need) + 3
+    ids = torch.randperm(n_pages, generator=g).to(torch.int32)
+    table = torch.full((len(new), max(need + [1]) + 1), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    T = lead + sum(new) + tail
+    cu = [lead]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q = (torch.randn(T, H, ref.KEY_DIMS[layout], generator=g) * qamp).to(BF)
+    return dict(q=q, pool=ref.make_pool(n_pages * page, layout, g, amp), layout=layout, table=table, page=page,
+                cu=torch.tensor(cu, dtype=torch.int32), kv=torch.tensor(kv, dtype=torch.int32), causal=True)
+
+
+def run(w, stream=None, ws=None):
+    T, H, _ = w["q"].shape
+    d = {k: v.cuda() for k, v in w.items() if isinstance(v, torch.Tensor)}
+    o = torch.full((T, H, 512), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if ws is None:
+        ws = binding.chunk_workspace_for(T, H, w["table"].shape[0], w["layout"])
+    ws.fill_(0xFF)                                        # what it held before has no effect
+    torch.cuda.synchronize()
+    binding.dsa_chunk_attn(d["q"], d["pool"], w["layout"], d["table"], w["page"], d["cu"], d["kv"], SCALE, o, lse, ws,
+                           causal=w["causal"], err_flag=err, stream=stream)
+    torch.cuda.synchronize()
+    return o.cpu(), lse.cpu(), int(err.item())
+
+
+def check(w, err_want=0, **kw):
+    whole_o, whole_lse, err = run(w, **kw)
+    o, lse = whole_o, whole_lse
+    ro, rl, otol, ltol, rerr = ref.chunk_attn(w["q"], w["pool"], w["layout"], w["table"], w["page"], w["cu"], w["kv"],
+                                              SCALE, w["causal"])
+    assert err == err_want == rerr
+    out = torch.isnan(rl)                                  # rows of no request
+    assert (o[out] == 7.0).all() and (lse[out] == 7.0).all()
+    o, lse, ro, rl, otol, ltol = (x[~out] for x in (o, lse, ro, rl, otol, ltol))
+    none = torch.isneginf(rl)
+    assert torch.equal(torch.isneginf(lse), none) and (o[none] == 0).all()
+    d = (o.double() - ro).abs() - otol
+    assert torch.isfinite(o).all() and (d <= 0).all(), f"O off by {d.max():.3e} beyond the bound at {torch.nonzero(d > 0)[:3].tolist()}"
+    d = ((lse.double() - rl).abs() - ltol)[~none]
+    assert d.numel() == 0 or (d <= 0).all(), f"LSE off by {d.max():.3e} beyond the bound"
+    return whole_o, whole_lse
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("H", [1, 8, 16, 20, 32, 64, 128])
+def test_single_tokens(layout, H):
+    """Decode: one token a request, contexts around the tile's 128 keys and none at all."""
+    check(make([1] * 9, [0, 1, 63, 126, 127, 128, 129, 255, 700], H, layout, seed=H))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("page", [1, 3, 16, 48, 64, 256, 1000])
+def test_page_sizes(layout, page):
+    check(make([1, 5, 40], [300, 77, 130], 8, layout, page=page, seed=page))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("new,ctx", [([2], [0]), ([130], [0]), ([7, 1, 33, 0, 64], [0, 500, 10, 20, 129]), ([200], [301])])
+@pytest.mark.parametrize("H", [3, 16])
+def test_chunks(layout, new, ctx, H):
+    """Prompts, chunks and single tokens in one batch; a request without new tokens."""
+    check(make(new, ctx, H, layout, seed=sum(new) + H))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_all_heads_of_a_chunk(layout):
+    check(make([9, 2], [400, 130], 128, layout, seed=2))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("H", [16, 128])
+def test_long_context_few_rows(layout, H):
+    """One request spread over every SM."""
+    check(make([1], [40000], H, layout, seed=3))
+    check(make([3, 1], [20011, 9], H, layout, seed=4))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_more_work_than_sms(layout):
+    """Many groups of query rows of unequal length: ranges begin and end inside requests."""
+    r = random.Random(5)
+    check(make([r.randint(1, 90) for _ in range(24)], [r.randint(0, 400) for _ in range(24)], 16, layout, seed=5))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_not_causal(layout):
+    w = make([5, 130, 1], [60, 3, 300], 8, layout, seed=6)
+    w["causal"] = False
+    check(w)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("qamp,amp", [(40.0, 1.0), (1e-3, 1.0), (1.0, 20.0), (0.05, 100.0), (1.0, 1e-3)])
+def test_amplitudes(layout, qamp, amp):
+    """Peaked and flat softmax, large and small rows."""
+    if layout == "raw512" and amp < 0.01:
+        amp = 0.05
+    check(make([1, 20], [900, 150], 16, layout, seed=7, qamp=qamp, amp=amp))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_rising_scores(layout):
+    """Keys whose scores rise along the sequence: the running maximum moves in every tile."""
+    w = make([1, 3], [1500, 1300], 16, layout, seed=8)
+    w["q"][:] = w["q"][:1, :1]
+    base = w["q"][0, 0, :512].float()
+    rows = torch.arange(w["kv"][0].item())
+    slot = w["table"][0].long()[rows // 64] * 64 + rows % 64
+    x = base[None] * (rows[:, None] / 500.0)
+    if layout == "raw512":
+        w["pool"][slot] = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        x = x.view(-1, 4, 128)
+        s = x.abs().amax(-1, keepdim=True) / 448.0
+        w["pool"][slot, :512] = torch.where(s > 0, x / s, torch.zeros(())).to(torch.float8_e4m3fn).view(torch.uint8).view(-1, 512)
+        w["pool"][slot, 512:528] = s.reshape(-1, 4).contiguous().view(torch.uint8)
+    check(w)
+
+
+@pytest.mark.parametrize("layout", ["scaled528", "rope656"])
+def test_zero_and_uneven_scales(layout):
+    """All-zero rows, zero groups, groups of very different scales."""
+    w = make([2, 40], [300, 200], 16, layout, seed=9)
+    s = w["pool"][:, 512:528].contiguous().view(torch.float32)
+    g = torch.Generator().manual_seed(1)
+    s *= 2.0 ** torch.randint(-30, 4, s.shape, generator=g).float()
+    s[::5] = 0
+    s[::3, 1] = 0
+    w["pool"][:, 512:528] = s.view(torch.uint8)
+    check(w)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_rows_of_no_request_are_left(layout):
+    check(make([3, 1, 17], [40, 200, 0], 8, layout, seed=10, lead=4, tail=9))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_queries_before_the_first_key(layout):
+    """More new tokens than the request holds: the first see nothing."""
+    w = make([10, 3, 1], [0, 0, 200], 8, layout, seed=11)
+    w["kv"][0], w["kv"][1] = 4, 0
+    check(w)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_bad_pages_are_masked(layout):
+    w = make([1, 30, 1], [200, 100, 64], 16, layout, seed=12)
+    w["table"][0, 1] = -1
+    w["table"][1, 0] = 10 ** 6
+    w["table"][2, 0] = 2 ** 31 - 1
+    w["table"][2, 1] = -5
+    check(w, err_want=2)
+
+
+@pytest.mark.parametrize("layout", ["raw512", "rope656"])
+def test_bad_lengths(layout):
+    w = make([2, 3, 4], [100, 100, 100], 8, layout, seed=13, tail=2)
+    w["kv"][1] = -4
+    check(w, err_want=16)
+    w["kv"][1] = 10 ** 9
+    o, lse, err = run(w)
+    assert err & 16 and torch.isfinite(lse[:2]).all() and torch.isfinite(lse[5:9]).all()
+    w["kv"][1] = 103
+    w["cu"] = torch.tensor([0, 2, 1, 40], dtype=torch.int32)      # descending, then beyond T
+    check(w, err_want=16)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_hidden_rows_may_hold_anything(layout):
+    """NaN and infinities in rows that a query does not see: rows past the end of the last page, later tokens of
+    the same chunk, pages of nobody."""
+    w = make([1, 6, 70], [70, 190, 0], 16, layout, seed=14)
+    want_o, want_l = check(w)
+    used = torch.zeros(w["pool"].shape[0], dtype=torch.bool)
+    for b in range(3):
+        j = torch.arange(int(w["kv"][b]))
+        used[w["table"][b].long()[j // 64] * 64 + j % 64] = True
+    w["pool"][~used] = 0xFF
+    o, lse, _ = run(w)
+    assert torch.equal(o, want_o) and torch.equal(lse, want_l)
+    # the last two tokens of request 2 hold NaN bytes (and NaN scales and RoPE dims); the one before an infinite scale
+    slots = [int(w["table"][2, p // 64]) * 64 + p % 64 for p in (67, 68, 69)]
+    if layout != "raw512":
+        w["pool"][slots[0], 512:528] = torch.full((4,), math.inf).view(torch.uint8)
+    w["pool"][slots[1:]] = 0x7F
+    o, lse, _ = run(w)
+    last = 7 + (67 if layout != "raw512" else 68)
+    ok = [t for t in range(last)]
+    assert torch.equal(o[ok], want_o[ok]) and torch.equal(lse[ok], want_l[ok])
+    assert torch.isnan(o[last:]).all() and torch.isnan(lse[last:]).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_nan_and_inf_queries_stay_in_their_rows(layout):
+    w = make([1, 40], [300, 100], 16, layout, seed=15)
+    want_o, want_l = check(w)
+    w["q"][0, 3, 5] = float("nan")
+    w["q"][20, 9, 100] = float("inf")
+    w["q"][30, 0, -1] = float("nan")
+    o, lse, _ = run(w)
+    for t, h in ((0, 3), (20, 9), (30, 0)):
+        assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h])
+        o[t, h], lse[t, h] = want_o[t, h], want_l[t, h]
+    assert torch.equal(o, want_o) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_deterministic_and_batch_independent(layout):
+    """The same call gives the same bits; zero queries average the rows."""
+    w = make([1, 30, 5], [500, 10, 900], 16, layout, seed=16)
+    a, b = run(w), run(w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    w["q"].zero_()
+    o, lse = check(w)
+    seen = torch.cat([torch.arange(int(w["kv"][i]) - int(w["cu"][i + 1] - w["cu"][i]), int(w["kv"][i])) + 1 for i in range(3)])
+    assert torch.allclose(lse.double(), seen.double().log()[:, None].expand(-1, 16), rtol=2e-6, atol=2e-6)
+
+
+def test_shared_pages():
+    """Two requests whose first pages are the same (a shared prefix)."""
+    w = make([4, 9], [200, 260], 16, "rope656", seed=17)
+    w["table"][1, :3] = w["table"][0, :3]
+    check(w)
+
+
+def test_far_rows_of_a_large_pool():
+    """Row offsets beyond 2^31 bytes."""
+    rows, layout = (2 ** 32 + 2 ** 28) // 656, "rope656"
+    rows -= rows % 64
+    w = make([1, 3], [100, 130], 16, layout, seed=18)
+    small = w["pool"]
+    n = small.shape[0] // 64
+    pool = torch.zeros(rows, 656, dtype=torch.uint8, device="cuda")
+    far = rows // 64 - n
+    pool[far * 64:] = small.cuda()
+    o1, l1, _ = run(w)
+    w2 = dict(w, pool=pool, table=torch.where(w["table"] >= 0, w["table"] + far, -1).to(torch.int32))
+    o2, l2, err = run(w2)
+    assert err == 0 and torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+def test_other_stream_and_captured_lengths():
+    """A captured call follows the lengths, offsets and pages that it finds when it is replayed."""
+    w = make([4, 60, 9], [200, 30, 500], 16, "rope656", seed=19)
+    want = run(w)
+    got = run(w, stream=torch.cuda.Stream())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    T, H = w["q"].shape[:2]
+    d = {k: v.cuda() for k, v in w.items() if isinstance(v, torch.Tensor)}
+    o = torch.zeros(T, H, 512, dtype=BF, device="cuda")
+    lse = torch.zeros(T, H, device="cuda")
+    ws = binding.chunk_workspace_for(T, H, 3, "rope656")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        binding.dsa_chunk_attn(d["q"], d["pool"], "rope656", d["table"], 64, d["cu"], d["kv"], SCALE, o, lse, ws)
+    for cu, kv in (([0, 4, 64, 73], [204, 90, 509]), ([0, 70, 71, 73], [100, 55, 300]), ([0, 0, 1, 1], [3, 90, 0])):
+        w["cu"], w["kv"] = torch.tensor(cu, dtype=torch.int32), torch.tensor(kv, dtype=torch.int32)
+        d["cu"].copy_(w["cu"])
+        d["kv"].copy_(w["kv"])
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        want = run(w)
+        assert torch.equal(o.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each."""
+    a, b = make([1, 30], [5000, 10], 16, "raw512", seed=20), make([40], [900], 16, "scaled528", seed=21)
+    wa, wb = run(a), run(b)
+    da = {k: v.cuda() for k, v in a.items() if isinstance(v, torch.Tensor)}
+    db = {k: v.cuda() for k, v in b.items() if isinstance(v, torch.Tensor)}
+    outs = []
+    for d in (da, db):
+        T, H = d["q"].shape[:2]
+        outs.append((torch.zeros(T, H, 512, dtype=BF, device="cuda"), torch.zeros(T, H, device="cuda")))
+    ws = [binding.chunk_workspace_for(31, 16, 2, "raw512"), binding.chunk_workspace_for(40, 16, 1, "scaled528")]
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, (d, lay) in enumerate(((da, "raw512"), (db, "scaled528"))):
+            binding.dsa_chunk_attn(d["q"], d["pool"], lay, d["table"], 64, d["cu"], d["kv"], SCALE, *outs[i], ws[i],
+                                   stream=s[i])
+    torch.cuda.synchronize()
+    for (o, l), want in zip(outs, (wa, wb)):
+        assert torch.equal(o.cpu(), want[0]) and torch.equal(l.cpu(), want[1])
+
+
+def test_agrees_with_the_sparse_kernel():
+    """A top-k list of every key gives the sparse decode's result."""
+    w = make([1] * 4, [127, 255, 383, 511], 16, "rope656", seed=22)
+    o, lse, _ = run(w)
+    K = 512
+    topk = torch.full((4, K), -1, dtype=torch.int32)
+    for b in range(4):
+        topk[b, :int(w["kv"][b])] = torch.arange(int(w["kv"][b]))
+    so, sl = torch.empty(4, 16, 512, dtype=BF, device="cuda"), torch.empty(4, 16, device="cuda")
+    binding.dsa_sparse_attn_decode(w["q"].cuda(), w["pool"].cuda(), "rope656", topk.cuda(), SCALE, so, sl,
+                                   binding.workspace_for(4, 16, K), page_table=w["table"].cuda(), page_size=64,
+                                   token_seq=torch.arange(4, dtype=torch.int32).cuda())
+    assert (so.cpu().float() - o.float()).abs().max() < 2.0 ** -6 * o.float().abs().max()
+    assert (sl.cpu() - lse).abs().max() < 1e-4

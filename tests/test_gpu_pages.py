@@ -1,0 +1,192 @@
+"""Page tables, slot maps and the return of pages against plain lists."""
+import random
+
+import pytest
+import torch
+
+import dense_ref as ref
+from sparse_mla_attention_page_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+def make(B, page, new_hi, ctx_hi, seed, spare=3, pad=5):
+    r = random.Random(seed)
+    new = [r.randint(0, new_hi) for _ in range(B)]
+    seq = [r.choice([0, r.randint(0, ctx_hi), page * r.randint(0, max(0, ctx_hi // page))]) for _ in range(B)]
+    width = max(ref.pages_of(s + n, page) for s, n in zip(seq, new)) + 1
+    ids = list(range(sum(ref.pages_of(s + n, page) for s, n in zip(seq, new)) + spare))
+    r.shuffle(ids)
+    table = []
+    for s in seq:
+        held = ref.pages_of(s, page)
+        table.append([ids.pop() for _ in range(held)] + [-1] * (width - held))
+    return dict(seq=seq, new=new, table=table, page=page, free=ids + [-7] * 4, count=len(ids), T=sum(new) + pad)
+
+
+def run_extend(w, in_place=False, stream=None):
+    seq, new = torch.tensor(w["seq"], **I32), torch.tensor(w["new"], **I32)
+    table, free = torch.tensor(w["table"], **I32), torch.tensor(w["free"], **I32)
+    count = torch.tensor([w["count"]], **I32)
+    T, B = w["T"], len(w["seq"])
+    out = dict(slots=torch.full((T,), 77, dtype=torch.int64, device="cuda"), positions=torch.full((T,), 77, **I32),
+               token_seq=torch.full((T,), 77, **I32), cu_q=torch.full((B + 1,), 77, **I32),
+               kv_lens=seq if in_place else torch.full((B,), 77, **I32))
+    count_out = count if in_place else torch.full((1,), 77, **I32)
+    err = torch.zeros(1, **I32)
+    torch.cuda.synchronize()
+    binding.dsa_pages_extend(seq, new, table, w["page"], free, count, count_out, err_flag=err, stream=stream, **out)
+    torch.cuda.synchronize()
+    assert free.tolist() == w["free"]
+    return {**{k: v.tolist() for k, v in out.items()}, "page_table": table.tolist(),
+            "free_count": int(count_out.item()), "err": int(err.item())}
+
+
+def check_extend(w, **kw):
+    want = ref.extend(w["seq"], w["new"], w["table"], w["page"], w["free"], w["count"], w["T"])
+    got = run_extend(w, **kw)
+    for k in want:
+        assert got[k] == want[k], k
+    return got
+
+
+@pytest.mark.parametrize("page", [1, 7, 16, 64, 256])
+@pytest.mark.parametrize("B,new_hi,ctx_hi", [(1, 1, 0), (1, 300, 5), (3, 0, 100), (64, 1, 900), (33, 200, 70), (1025, 9, 40)])
+def test_extend(B, new_hi, ctx_hi, page):
+    check_extend(make(B, page, new_hi, ctx_hi, seed=B * 1000 + page))
+
+
+def test_extend_many_tokens():
+    """More tokens than one pass of the largest cluster's threads."""
+    check_extend(make(40, 16, 4000, 100, seed=3))
+
+
+def test_extend_most_requests():
+    check_extend(make(16384, 64, 2, 3, seed=4))
+
+
+@pytest.mark.parametrize("B", [5, 300])
+def test_extend_in_place(B):
+    check_extend(make(B, 16, 40, 100, seed=5), in_place=True)
+
+
+def test_extend_other_stream():
+    s = torch.cuda.Stream()
+    check_extend(make(20, 16, 40, 100, seed=6), stream=s)
+
+
+def test_extend_exact_fit():
+    """No spare page, no padding row."""
+    w = make(17, 16, 40, 100, seed=7, spare=0, pad=0)
+    assert check_extend(w)["free_count"] == 0
+
+
+@pytest.mark.parametrize("what,bit", [("pages", 32), ("negative_seq", 16), ("negative_new", 16), ("outgrown", 16),
+                                      ("tokens", 16), ("count_negative", 16), ("count_high", 16), ("huge", 16)])
+def test_extend_refused_changes_nothing(what, bit):
+    w = make(9, 16, 40, 100, seed=8)
+    w["new"][2] = 33                                       # pages are needed, and the rows have room for them
+    w["T"] = sum(w["new"]) + 5
+    w["table"] = [row + [-1] * 3 for row in w["table"]]
+    if what == "pages":
+        w["count"] = 1
+    elif what == "negative_seq":
+        w["seq"][4] = -1
+    elif what == "negative_new":
+        w["new"][8] = -3
+    elif what == "outgrown":
+        w["seq"][1] = len(w["table"][0]) * 16 - 1
+        w["new"][1] = 2
+    elif what == "tokens":
+        w["T"] = sum(w["new"]) - 1
+    elif what == "count_negative":
+        w["count"] = -1
+    elif what == "count_high":
+        w["count"] = len(w["free"]) + 1
+    else:
+        w["seq"][3] = w["new"][3] = 2147483647
+    got = check_extend(w)
+    assert got["err"] == bit and got["page_table"] == w["table"]
+
+
+def test_extend_bad_page_ids():
+    """A negative id in the stack, and one in a partly filled page's entry."""
+    w = make(6, 16, 40, 100, seed=9)
+    w["free"][w["count"] - 1] = -4
+    w["seq"][2], w["new"][2] = 5, 3
+    w["table"][2][0] = -1
+    got = check_extend(w)
+    assert got["err"] == 2 and -1 in got["slots"][:sum(w["new"])]
+
+
+def run_release(w, finished, cap=None, in_place=False):
+    seq, table = torch.tensor(w["seq"], **I32), torch.tensor(w["table"], **I32)
+    free, count = torch.tensor(w["free"], **I32), torch.tensor([w["count"]], **I32)
+    out = seq if in_place else torch.full((len(w["seq"]),), 77, **I32)
+    count_out = count if in_place else torch.full((1,), 77, **I32)
+    err = torch.zeros(1, **I32)
+    binding.dsa_pages_release(torch.tensor(finished, device="cuda"), seq, table, w["page"], free, count, count_out, out,
+                              err_flag=err)
+    torch.cuda.synchronize()
+    assert table.tolist() == w["table"]
+    return dict(free_pages=free.tolist(), free_count=int(count_out.item()), seq_lens=out.tolist(), err=int(err.item()))
+
+
+def check_release(w, finished, **kw):
+    want = ref.release(finished, w["seq"], w["table"], w["page"], w["free"], w["count"])
+    got = run_release(w, finished, **kw)
+    assert got == want
+    return got
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,page,ctx", [(1, 16, 40), (1, 1, 5000), (7, 64, 0), (64, 64, 900), (600, 16, 300), (16384, 256, 3)])
+def test_release(B, page, ctx, in_place):
+    r = random.Random(B)
+    w = make(B, page, 0, ctx, seed=B + 1)
+    w["free"] += [-9] * sum(ref.pages_of(s, page) for s in w["seq"])
+    for share in (0.0, 0.3, 1.0):
+        check_release(w, [r.random() < share for _ in range(B)], in_place=in_place)
+
+
+@pytest.mark.parametrize("what,bit", [("room", 32), ("length", 16), ("negative", 16), ("page", 2), ("count", 16)])
+def test_release_refused_changes_nothing(what, bit):
+    w = make(9, 16, 0, 100, seed=10)
+    w["seq"][3] = max(w["seq"][3], 17)
+    w["table"][3][:2] = [900, 901]
+    w["free"] += [-9] * 200
+    if what == "room":
+        w["free"] = w["free"][:w["count"] + 1]
+    elif what == "length":
+        w["seq"][5] = len(w["table"][0]) * 16 + 1
+    elif what == "negative":
+        w["seq"][5] = -2
+    elif what == "page":
+        w["table"][3][1] = -1
+    else:
+        w["count"] = len(w["free"]) + 1
+    assert check_release(w, [True] * 9)["err"] == bit
+
+
+def test_captured_steps():
+    """A captured in-place step, replayed: lengths and the free count move on the GPU alone."""
+    w = make(6, 16, 3, 30, seed=11, spare=40)
+    B, T = 6, w["T"]
+    seq, new = torch.tensor(w["seq"], **I32), torch.tensor(w["new"], **I32)
+    table = torch.full((B, 12), -1, **I32)
+    table[:, :len(w["table"][0])] = torch.tensor(w["table"], **I32)
+    free, count = torch.tensor(w["free"], **I32), torch.tensor([w["count"]], **I32)
+    slots = torch.zeros(T, dtype=torch.int64, device="cuda")
+    pos, ts, cu = torch.zeros(T, **I32), torch.zeros(T, **I32), torch.zeros(B + 1, **I32)
+    g = torch.cuda.CUDAGraph()
+    lists = dict(seq=seq.tolist(), table=table.tolist(), count=w["count"])
+    with torch.cuda.graph(g):
+        binding.dsa_pages_extend(seq, new, table, 16, free, count, count, slots, pos, ts, cu, seq)
+    for step in range(4):
+        g.replay()
+        torch.cuda.synchronize()
+        want = ref.extend(lists["seq"], w["new"], lists["table"], 16, w["free"], lists["count"], T)
+        assert slots.tolist() == want["slots"] and table.tolist() == want["page_table"], step
+        assert seq.tolist() == want["kv_lens"] and int(count.item()) == want["free_count"]
+        lists = dict(seq=want["kv_lens"], table=want["page_table"], count=want["free_count"])
