@@ -440,7 +440,7 @@ size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
  * kv_lens[b] below 0 counts as 0 and one above max_pages * page_size as that
  * (DSA_DEV_ERR_LENGTH).  Ranges of requests do not overlap.
  *   q_bf16_dev      [T, H, 512] BF16, [T, H, 576] over 656-byte rows; 16-byte aligned.
- *   H               1 to 1024.
+ *   H               1 to 1024; T * H < 2^30.
  *   page_table_dev  [B, max_pages] int32.
  *   cu_q_dev        [B + 1] int32;  kv_lens_dev [B] int32; B <= DSA_MAX_REQUESTS.
  *   o_bf16_dev      [T, H, 512] BF16 out, 16-byte aligned;  lse_dev [T, H] float out.

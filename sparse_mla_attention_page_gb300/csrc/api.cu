@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dsa.h"
+#include "dense.h"
 #include "kernels.h"
 
 namespace dsa {
@@ -38,7 +39,7 @@ namespace {
 
 using dsa::current_device_sms;
 
-// Limit of the attention kernel's bounded waits (dsa_set_wait_limit_ns).
+// Limit of the attention kernels' bounded waits (dsa_set_wait_limit_ns).
 std::atomic<uint64_t> g_wait_ns{1000000000ull};
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -145,6 +146,8 @@ int sparse_attn(bool q8, const void* q, const float* q_scale, int T, int H, int 
 }
 
 }  // namespace
+
+uint64_t dsa::wait_limit_ns() { return g_wait_ns.load(); }
 
 extern "C" {
 

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dsa.h"
+#include "chunk.cuh"
 #include "dense.h"
 #include "kernels.h"
 
@@ -33,6 +34,30 @@ int launch_status(bool launched) {
 bool table_ok(int B, int max_pages, int page_size) {
   return B >= 1 && B <= DSA_MAX_REQUESTS && max_pages >= 1 && page_size >= 1 &&
          (int64_t)max_pages * page_size <= INT32_MAX;
+}
+
+// Where the parts of the attention's workspace begin (pointers from base on).
+size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, char* base) {
+  w.nc = dsa::chunk_columns(T, H, B);
+  w.max_units = (int64_t)T * H / w.nc + B;     // full units, and the last of each request
+  w.grid = sms;
+  size_t end = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + end;
+    end += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  w.hdr = reinterpret_cast<dsa::ChunkHeader*>(take(sizeof(dsa::ChunkHeader)));
+  w.units = reinterpret_cast<dsa::ChunkUnit*>(take((size_t)w.max_units * sizeof(dsa::ChunkUnit)));
+  w.cta_unit = reinterpret_cast<int32_t*>(take((size_t)sms * sizeof(int32_t)));
+  w.splits = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
+  w.part_lse = reinterpret_cast<float*>(take((size_t)sms * 2 * w.nc * sizeof(float)));
+  w.part_o = reinterpret_cast<float*>(take((size_t)sms * 2 * w.nc * 512 * sizeof(float)));
+  return end;
+}
+
+bool chunk_sizes_ok(int T, int H, int B) {
+  return T >= 0 && H >= 1 && H <= 1024 && (int64_t)T * H <= INT32_MAX / 2 && B >= 1 && B <= DSA_MAX_REQUESTS;
 }
 
 }  // namespace
@@ -157,8 +182,11 @@ int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t 
 }
 
 size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout) {
-  if (T < 0 || H < 1 || H > 1024 || B < 1 || B > DSA_MAX_REQUESTS || dsa_kv_row_bytes(layout) == 0) return 0;
-  return 256;
+  if (!chunk_sizes_ok(T, H, B) || dsa_kv_row_bytes(layout) == 0) return 0;
+  int sms = 0;
+  if (dsa::current_device_sms(&sms) != DSA_OK) sms = 152;
+  dsa::ChunkWork w{};
+  return lay_out_chunk(w, T, H, B, sms, nullptr);
 }
 
 int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool_dev, int64_t pool_rows,
@@ -166,7 +194,7 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
                    const int32_t* cu_q_dev, const int32_t* kv_lens_dev, int causal, float sm_scale,
                    void* o_bf16_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes, int32_t* err_flag_dev,
                    void* stream) {
-  if (T < 0 || T > INT32_MAX / 2 || pool_rows < 0) return DSA_ERR_SHAPE;
+  if (T < 0 || pool_rows < 0) return DSA_ERR_SHAPE;
   if (dsa_kv_row_bytes(layout) == 0) return DSA_ERR_LAYOUT;
   const int width = layout == DSA_KV_ROPE656 ? 576 : 512;
   if (D != width || kv_row_dim != width) return DSA_ERR_ROW_WIDTH;
@@ -175,7 +203,8 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
   if (any_null(page_table_dev, cu_q_dev, kv_lens_dev) || q_bf16_dev == nullptr || pool_dev == nullptr ||
       o_bf16_dev == nullptr || lse_dev == nullptr)
     return DSA_ERR_NULL;
-  if (!table_ok(B, max_pages, page_size) || pool_rows < 1 || pool_rows > INT32_MAX) return DSA_ERR_SHAPE;
+  if (!table_ok(B, max_pages, page_size) || !chunk_sizes_ok(T, H, B) || pool_rows < 1 || pool_rows > INT32_MAX)
+    return DSA_ERR_SHAPE;
   if (!aligned(q_bf16_dev, 16) || !aligned(pool_dev, 16) || !aligned(o_bf16_dev, 16) || !aligned(lse_dev, 4) ||
       !aligned(page_table_dev, 4) || !aligned(cu_q_dev, 4) || !aligned(kv_lens_dev, 4) || !aligned(err_flag_dev, 4))
     return DSA_ERR_ALIGN;
@@ -184,7 +213,10 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
   int sms = 0;
   const int st = dsa::current_device_sms(&sms);
   if (st != DSA_OK) return st;
-  dsa::ChunkArgs a{};
+  dsa::ChunkWork w{};
+  lay_out_chunk(w, T, H, B, sms, static_cast<char*>(workspace_dev));
+  w.wait_ns = dsa::wait_limit_ns();
+  dsa::ChunkArgs& a = w.a;
   a.q = static_cast<const uint16_t*>(q_bf16_dev);
   a.T = T;
   a.H = H;
@@ -204,7 +236,7 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
   a.lse = lse_dev;
   a.err = err_flag_dev;
   cudaGetLastError();
-  return launch_status(dsa::launch_chunk_attn(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(dsa::launch_chunk_attn(w, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

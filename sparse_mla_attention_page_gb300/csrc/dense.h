@@ -86,6 +86,13 @@ struct ChunkArgs {
   float* lse;
   int32_t* err;
 };
-bool launch_chunk_attn(const ChunkArgs& a, cudaStream_t stream);
+// Query rows of a unit of the work list: the widest that an average request
+// fills.
+int chunk_columns(int T, int H, int B);
+struct ChunkWork;      // chunk.cuh
+bool launch_chunk_attn(const ChunkWork& w, cudaStream_t stream);
+
+// Limit of every bounded wait inside the attention kernels (dsa_set_wait_limit_ns).
+uint64_t wait_limit_ns();
 
 }  // namespace dsa

@@ -16,63 +16,14 @@
 
 #include "dense.h"
 #include "dsa_common.cuh"
+#include "scan.cuh"
 
 namespace dsa {
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-
-struct Sum2 {
-  int64_t a, b;
-};
-
-// Exclusive prefix sum of v over the block's threads; *total gets the sum.
-__device__ __forceinline__ Sum2 block_scan(Sum2 v, Sum2* total) {
-  __shared__ Sum2 warp_sums[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sum2 s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int64_t ta = __shfl_up_sync(0xffffffffu, s.a, o), tb = __shfl_up_sync(0xffffffffu, s.b, o);
-    if (lane >= o) {
-      s.a += ta;
-      s.b += tb;
-    }
-  }
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    Sum2 w = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t ta = __shfl_up_sync(0xffffffffu, w.a, o), tb = __shfl_up_sync(0xffffffffu, w.b, o);
-      if (lane >= o) {
-        w.a += ta;
-        w.b += tb;
-      }
-    }
-    warp_sums[lane] = w;
-  }
-  __syncthreads();
-  const Sum2 before = warp == 0 ? Sum2{0, 0} : warp_sums[warp - 1];
-  *total = warp_sums[kWarps - 1];
-  return Sum2{before.a + s.a - v.a, before.b + s.b - v.b};
-}
-
-// The last index i in [0, n) with start[i] <= x (start rises from 0): the
-// request whose range holds x (empty ranges share a start with the next one).
-__device__ __forceinline__ int owner(const int32_t* start, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
+constexpr int kThreads = kScanThreads;
 
 __device__ __forceinline__ int64_t pages_of(int64_t tokens, int page_size) {
   return (tokens + page_size - 1) / page_size;
@@ -91,31 +42,31 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const ExtendA
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   bool bad = count < 0 || count > a.free_cap;
-  Sum2 mine{0, 0};
+  int64_t tokens = 0, pages = 0;
   for (int b = b0; b < b1; ++b) {
     const int64_t s = a.seq_lens[b], n = a.new_lens[b];
     bad |= s < 0 || n < 0 || s + n > room;
-    mine.a += n;
-    mine.b += pages_of(s + n, a.page_size) - pages_of(s, a.page_size);
+    tokens += n;
+    pages += pages_of(s + n, a.page_size) - pages_of(s, a.page_size);
   }
-  Sum2 total;
-  Sum2 at = block_scan(mine, &total);
-  bad |= total.a > a.T;
+  int64_t all_tokens, all_pages;
+  int64_t tok_at = block_scan(tokens, &all_tokens), page_at = block_scan(pages, &all_pages);
+  bad |= all_tokens > a.T;
   const bool lengths_bad = __syncthreads_or(bad) != 0;
-  const bool short_of_pages = !lengths_bad && total.b > count;
+  const bool short_of_pages = !lengths_bad && all_pages > count;
   const bool refused = lengths_bad || short_of_pages;
   if (refused && gtid == 0)
     set_err(a.err, lengths_bad ? DSA_DEV_ERR_LENGTH : DSA_DEV_ERR_NO_PAGES);
   for (int b = b0; b < b1; ++b) {
     const int64_t s = a.seq_lens[b], n = a.new_lens[b];
-    tok0[b] = refused ? 0 : (int32_t)at.a;
-    page0[b] = refused ? 0 : (int32_t)at.b;
+    tok0[b] = refused ? 0 : (int32_t)tok_at;
+    page0[b] = refused ? 0 : (int32_t)page_at;
     seq[b] = (int32_t)s;
-    at.a += n;
-    at.b += pages_of(s + n, a.page_size) - pages_of(s, a.page_size);
+    tok_at += n;
+    page_at += pages_of(s + n, a.page_size) - pages_of(s, a.page_size);
   }
-  const int n_tok = refused ? 0 : (int)total.a;
-  const int n_pages = refused ? 0 : (int)total.b;
+  const int n_tok = refused ? 0 : (int)all_tokens;
+  const int n_pages = refused ? 0 : (int)all_pages;
   cluster.sync();   // every CTA has read the lengths and the count: the outputs may alias them
 
   bool bad_page = false;
@@ -123,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const ExtendA
     int64_t slot = -1;
     int pos = 0, b = -1;
     if (t < n_tok) {
-      b = owner(tok0, a.B, t);
+      b = scan_owner(tok0, a.B, t);
       pos = seq[b] + (t - tok0[b]);
       const int p = pos / a.page_size;
       const int have = (int)pages_of(seq[b], a.page_size);
@@ -138,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const ExtendA
     a.token_seq[t] = b;
   }
   for (int k = gtid; k < n_pages; k += gsize) {
-    const int b = owner(page0, a.B, k);
+    const int b = scan_owner(page0, a.B, k);
     const int p = (int)pages_of(seq[b], a.page_size) + (k - page0[b]);
     const int32_t page = __ldg(a.free_pages + (count - 1 - k));
     bad_page |= page < 0;
@@ -170,28 +121,28 @@ __global__ void __launch_bounds__(kThreads, 1) pages_release_kernel(const Releas
     return a.finished[b] && s > 0 ? pages_of(s, a.page_size) : 0;
   };
   bool bad = count < 0 || count > a.free_cap;
-  Sum2 mine{0, 0};
+  int64_t pages = 0;
   for (int b = b0; b < b1; ++b) {
     const int64_t s = a.seq_lens[b];
     bad |= s < 0 || s > room;
-    mine.a += back(b);
+    pages += back(b);
   }
-  Sum2 total;
-  Sum2 at = block_scan(mine, &total);
+  int64_t all_pages;
+  int64_t at = block_scan(pages, &all_pages);
   const bool lengths_bad = __syncthreads_or(bad) != 0;
-  const bool no_room = !lengths_bad && count + total.a > a.free_cap;
+  const bool no_room = !lengths_bad && count + all_pages > a.free_cap;
   const bool refused = lengths_bad || no_room;
   if (refused && gtid == 0) set_err(a.err, lengths_bad ? DSA_DEV_ERR_LENGTH : DSA_DEV_ERR_NO_PAGES);
   for (int b = b0; b < b1; ++b) {
-    page0[b] = refused ? 0 : (int32_t)at.a;
-    at.a += back(b);
+    page0[b] = refused ? 0 : (int32_t)at;
+    at += back(b);
   }
-  const int n_pages = refused ? 0 : (int)total.a;
+  const int n_pages = refused ? 0 : (int)all_pages;
   __syncthreads();
   // every page is looked at before any is pushed
   bool bad_page = false;
   for (int k = gtid; k < n_pages; k += gsize) {
-    const int b = owner(page0, a.B, k);
+    const int b = scan_owner(page0, a.B, k);
     bad_page |= __ldg(a.page_table + (int64_t)b * a.max_pages + (k - page0[b])) < 0;
   }
   // the flag is set up in every CTA before another one may reach it
@@ -202,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_release_kernel(const Releas
   if (!refused && dropped && gtid == 0) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
   if (!dropped)
     for (int k = gtid; k < n_pages; k += gsize) {
-      const int b = owner(page0, a.B, k);
+      const int b = scan_owner(page0, a.B, k);
       a.free_pages[count + k] = __ldg(a.page_table + (int64_t)b * a.max_pages + (k - page0[b]));
     }
   for (int b = gtid; b < a.B; b += gsize) a.seq_lens_out[b] = a.finished[b] && !dropped ? 0 : a.seq_lens[b];

@@ -120,10 +120,16 @@ def chunk_attn(q, pool, layout, table, page, cu, kv_lens, sm_scale, causal=True)
     """(O, LSE, bound of O's error, bound of LSE's) in float64, CPU tensors; rows of no request NaN.
 
     The bounds count, per output: the BF16 rounding of O (2^-8 |O|); the two E4M3 terms of each softmax weight
-    (2^-4 of 2^-4 of it, and FP32 sums of exponentials: 2^-8 + 2^-12 of sum_j w_j |v_j|; E4M3's smallest step, 2^-9, at a
-    largest weight of at least 2^4: 2^-14 of sum_j |v_j| per unit of l); scores in FP32 sums of up to 576 exact
+    (2^-4 of 2^-4 of it, and FP32 sums of exponentials: 2^-8 + 2^-12 of sum_j w_j |v_j|; E4M3's smallest step: see
+    below); scores in FP32 sums of up to 576 exact
     products (2^-17 of sum_d |q_d k_jd|, and once again for the queries' two E4M3 terms), which enter O through
-    the weights and LSE directly."""
+    the weights and LSE directly.
+
+    E4M3's smallest step over rows with scales.  The operand of group g is P = 2^(s_j - M) s_jg, rounded by at most 2^-10
+    (half of 2^-9) where the step binds, and multiplies the row's byte b_jd.  M is at most max_j (s_j + log2 S_j) - 4 with
+    S_j the row's largest scale, so for the row J of that maximum 2^(s_J - M) S_J >= 2^4, and l = sum_j 2^(s_j - M) =
+    2^(s_J - M) / w_J >= 2^4 / (S_J w_J).  O is off by at most sum_j 2^-10 |b_jd| / l <= 2^-14 max_j (w_j S_j) sum_j |b_jd|.
+    (Raw rows: S = 1, b = v, max w = 1 / (l / e^max s).)"""
     T, H, _ = q.shape
     q = q.double()
     o = torch.full((T, H, 512), math.nan, dtype=torch.float64)
@@ -148,7 +154,12 @@ def chunk_attn(q, pool, layout, table, page, cu, kv_lens, sm_scale, causal=True)
         last = kv if not causal else max(0, kv)
         if not bool(ok[:last].all()):
             err |= 2
-        k, v = dequant(pool[torch.where(ok, row, 0)], layout)
+        rows = pool[torch.where(ok, row, 0)]
+        k, v = dequant(rows, layout)
+        codes = rows[:, :512].contiguous().view(torch.float8_e4m3fn).double().abs()
+        big = torch.ones(kv, dtype=torch.float64)
+        if layout != "raw512":
+            big = rows[:, 512:528].contiguous().view(torch.float32).double().abs().amax(1)
         for i in range(n):
             see = ok & (j < (kv - n + i + 1 if causal else kv))
             kk, vv = k[see], v[see]
@@ -162,8 +173,8 @@ def chunk_attn(q, pool, layout, table, page, cu, kv_lens, sm_scale, causal=True)
             o[t0 + i], lse[t0 + i] = w @ vv, z
             mag = (qi.abs() @ kk.abs().T * abs(sm_scale)).amax(-1) * 2.0 ** -16 + 2.0 ** -18
             absv = w @ vv.abs()
-            l = (z - s.amax(-1)).exp()
+            step = 2.0 ** -14 * (w * big[see]).amax(-1)[:, None] * codes[see].sum(0)
             otol[t0 + i] = (2.0 ** -8 * o[t0 + i].abs() + (2.0 ** -8 + 2.0 ** -12 + 2 * mag[:, None]) * absv
-                            + 2.0 ** -14 * vv.abs().sum(0) / l[:, None])
+                            + step)
             ltol[t0 + i] = mag + z.abs() * 2.0 ** -22
     return o, lse, otol, ltol, err
