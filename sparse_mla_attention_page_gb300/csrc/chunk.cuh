@@ -4,9 +4,12 @@
 // A unit is a group of up to NC consecutive query rows of one request (row =
 // token x head, tokens outermost) and takes the 128-key tiles up to the last
 // key that its last row sees.  The units' tiles, one after another, are the
-// global tile list; CTA c of the persistent grid owns the tiles
-// [c n / grid, (c + 1) n / grid), so a unit may be spread over CTAs.  Lengths
-// live on the GPU: a plan kernel writes the list into the workspace.
+// global tile list; CTA c of the persistent grid owns a range of it, so a unit
+// may be spread over CTAs.  The ranges are cut evenly by cost: a unit counts
+// kUnitCost tiles more than it has, for its query operand and its output
+// (prompts of up to 2047 tokens, where units have 1 to 16 tiles: cut by tiles
+// alone the CTAs took 199 to 433 us).  Lengths live on the GPU: a plan kernel
+// writes the list into the workspace.
 #pragma once
 #include <cstdint>
 
@@ -15,6 +18,7 @@
 namespace dsa {
 
 constexpr int kChunkTile = 128;      // keys of a tile
+constexpr int kUnitCost = 3;         // cost of a unit beside its tiles', in tiles
 
 struct __align__(16) ChunkUnit {
   int64_t tile0;     // first global tile
@@ -25,18 +29,27 @@ struct __align__(16) ChunkUnit {
   int32_t vis0;      // keys that the request's first token sees (may be negative); all keys when not causal
   int32_t tiles;     // at least 1
   int32_t kv;        // the request's keys
+  int32_t last;      // keys that the unit's last row sees
+  int32_t pad;
+};
+
+// Where a CTA's range begins.
+struct __align__(16) ChunkStart {
+  int64_t t0;        // first global tile (the number of tiles for CTAs without work, and behind the last one)
+  int32_t unit;
+  int32_t pad;
+  ChunkUnit u;
+};
+
+// A unit spread over CTAs c0 ..: its parts lie in the slots slot0, 2 (c0 + 1), 2 (c0 + 2), ...
+struct __align__(16) ChunkSplit {
+  int64_t row0;      // as of the unit
+  int32_t cols;
+  int32_t parts;     // 0: no unit of few parts begins in this CTA
+  int32_t slot0, next;
   int32_t pad[2];
 };
-
-// A unit spread over CTAs c0 .. c1; its parts lie in the slots slot0, 2 (c0 + 1), 2 (c0 + 2), ...
-struct ChunkSplit {
-  int32_t unit, c0, c1, slot0;
-};
-
-struct ChunkHeader {
-  int64_t n_tiles;
-  int32_t n_units, n_splits;
-};
+constexpr int kFewParts = 8;         // split units of up to so many parts are merged a thread for each 8 dims
 
 // Everything a call needs; the pointers from hdr on lie in the workspace.
 struct ChunkWork {
@@ -44,18 +57,16 @@ struct ChunkWork {
   int nc;                  // query rows of a unit
   int64_t max_units;
   int grid;                // CTAs of the attention grid
+  int box_shift;           // log2 of the rows of a TMA box; 0: rows are copied one by one
   uint64_t wait_ns;
-  ChunkHeader* hdr;
-  ChunkUnit* units;
-  int32_t* cta_unit;       // [grid] the unit of each CTA's first tile
-  ChunkSplit* splits;      // [grid]
+  ChunkUnit* units;        // [max_units + 1]
+  ChunkStart* starts;      // [grid + 1]
+  ChunkSplit* few;         // [grid] by the CTA in which the unit begins
+  ChunkSplit* many;        // [grid] units of more parts
+  int32_t* n_many;
   float* part_lse;         // [2 grid][nc]
   float* part_o;           // [2 grid][nc][512] normalised
 };
-
-__host__ __device__ __forceinline__ int64_t chunk_tile_begin(int64_t c, int64_t n_tiles, int grid) {
-  return c * n_tiles / grid;
-}
 
 // Keys that row r of a unit's request sees.
 __device__ __forceinline__ int chunk_visible(const ChunkArgs& a, const ChunkUnit& u, int col) {

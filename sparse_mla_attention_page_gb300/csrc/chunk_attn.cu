@@ -4,38 +4,53 @@
 //   s_j = sm_scale log2(e) <q, k_j>,  p_j = 2^(s_j - m),  l = sum_j p_j
 //   O = sum_j p_j v_j / l,            LSE = ln2 (m + log2 l)
 //
-// Orientation.  A unit (chunk.cuh) is NC query rows; its keys come in tiles of
-// 128.  Scores are formed transposed, S^T = K Q^T (M = 128 keys, N = query
-// columns), and so is the output, O^T += V^T P^T (M = 128 latent dims, four
-// times, N = NC): the E4M3 rows land in shared memory once and are both the
+// Orientation.  A unit (chunk.cuh) is NC = 16 or 32 query rows; its keys come in
+// tiles of 128.  Scores are formed transposed, S^T = K Q^T (M = 128 keys, N =
+// query columns), and so is the output, O^T += V^T P^T (M = 128 latent dims,
+// four times): the E4M3 rows land in shared memory once and are both the
 // K-major A operand of the first product and the MN-major A operand of the
-// second, with no conversion.  512 output dims of 64 query rows take half the
-// tensor memory, the score buffers the other half, so NC = 64 is the widest
-// unit; with 128 query rows along M instead, O alone would fill it.
+// second, with no conversion.  (With query rows along M the FP32 output of 128
+// rows alone would fill the tensor memory.)  Units of 64 columns were built
+// too: they read a tile once for twice the columns, but their operands leave
+// room for little more than one tile of rows, and they ran 4 % (4096 tokens
+// over 8192, 656-byte rows) to 8 % (prompts over raw rows) slower.
 //
-// 16-bit data on 8-bit operands.  A BF16 query splits exactly into two E4M3
-// terms (hi, and lo 16 times larger, both NC columns of one operand), times a
-// power of two for each row; scores are then exact but for their FP32 sums.
-// Softmax weights are written as two E4M3 terms that add up in the same
-// accumulator (two K ranges): 8 significant bits, as BF16 weights would have.
-// p is scaled so that the running maximum maps to 2^4 and may grow to 2^8
-// before the maximum moves, which keeps E4M3's smallest step 2^-13 or less of
-// the largest weight.
+// 16-bit data on 8-bit operands.  A BF16 query times a power of two for its row
+// splits into two E4M3 terms, q ~ hi + lo / 16, exactly where it is within
+// 2^14 of the row's largest entry; softmax weights likewise, p ~ hi + lo / 16,
+// to 8 significant bits (as BF16 weights would have).  The terms are columns of
+// their own in both products, so a tile is read once for both.  p of the key
+// that sets the running maximum is 1 and may grow to 2^8.75 before the maximum
+// moves (E4M3 ends at 448); lo then still resolves 2^-14.
 //
 // Group scales (528- and 656-byte rows): one pass of the score product for
 // each 128-dim group, multiplied by the row's scale as it is read out, and one
-// P operand for each group, p s_g, against that group's block of values.  The
-// running maximum is kept of s + log2(largest scale of the row), which bounds
-// the entries of all four.  RoPE dims are one more pass, BF16.
+// P operand for each group against that group's block of values.  With S the
+// power of two above the row's largest scale, the running maximum M is kept of
+// s + log2 S, so that one exponential serves all four groups,
+//   P_g = 2^(s + log2 S - M) (s_g / S) c_g,   l = sum 2^(s + log2 S - M) / S,
+// and c_g, a power of two for each group, lifts groups that are smaller than
+// their rows' largest throughout the segment.  (S and c_g are powers of two:
+// nothing is rounded but P itself.)  RoPE dims are one more pass, BF16, with
+// the row's power of two in the query.
 //
-// Warp roles (24 warps): 16 softmax (warp w: TMEM lane quarter w % 4 = 32 keys
-// of the tile, column quarter w / 4), one issuing thread for each product, six
-// producers that translate keys to rows and gather them with 16-byte cp.async
-// into a ring of 16 KB blocks (128 keys x 128 bytes).  A block is released as
-// soon as the product that reads it last has finished.
+// Warp roles: 16 softmax warps (warp w: TMEM lane quarter w % 4 = 32 keys of
+// the tile, column quarter w / 4), one issuing thread for each product, and
+// producers that translate keys to rows and bring them into a ring of 16 KB
+// blocks (128 keys x 128 bytes).  A block is released as soon as the product
+// that reads it last has finished.  Pages of a multiple of 16 rows come by TMA
+// (one warp, boxes of 16 to 128 rows: a page never ends inside a box); other
+// page sizes row by row with 16-byte cp.async (six warps).
+//
+// What lies in shared memory for a key that nobody sees (the rest of a page, a
+// box that was not loaded) has no effect: its weights are 0, and a row that
+// holds a NaN byte is cleared before the second product reads it.
 #include <atomic>
 #include <cstddef>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "chunk.cuh"
 #include "dsa_common.cuh"
@@ -49,77 +64,88 @@ using namespace tc;
 
 constexpr int kTile = kChunkTile;
 constexpr int kBlock = kTile * 128;          // bytes of a ring block
-constexpr float kTop = 8.0f;                 // p never exceeds 2^kTop
-constexpr float kBias = 4.0f;                // p of the key that set the maximum: 2^kBias
-constexpr float kNoMax = -1.0e30f;           // maximum of a row that has seen no key (finite: 2^(-inf - m) = 0)
+constexpr float kTop = 8.75f;                // p never exceeds 2^kTop (E4M3 ends at 448 = 2^8.8)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSmxWarps = 16, kSmxThreads = 512;
-constexpr int kQkWarp = 16, kPvWarp = 17, kProdWarp0 = 18, kProdWarps = 6, kProdThreads = 192;
-constexpr int kThreads = 768;
+constexpr int kQkWarp = 16, kPvWarp = 17, kProdWarp0 = 18;
+constexpr int kProdWarps = 6, kProdThreads = 192;    // of the row-by-row form
 constexpr int kQuads = kTile / 4;            // producer work unit: 4 rows (one warp instruction per 128-byte piece)
 constexpr int kQuadsPerWarp = (kQuads + kProdWarps - 1) / kProdWarps;
-constexpr int kLaunchRegs = 80;              // registers a thread at launch (768 threads); the softmax warps then
-constexpr int kSmxRegs = 96;                 // take 96 and the others give back to 48: 512 x 96 + 256 x 48 = 768 x 80
-constexpr int kOtherRegs = 48;
-static_assert(kSmxRegs * kSmxThreads + kOtherRegs * (kThreads - kSmxThreads) == kLaunchRegs * kThreads, "register split");
 constexpr int kMeta = 4;                     // tiles whose rows and scales are kept
+constexpr int kSegs = 6;                     // segments whose units are kept
+constexpr int kMaxSBuf = 4;                  // score buffers
+constexpr int kProdBar = 8;                  // named barriers: 1 + column quarter, producers
 constexpr int kMaxBlocks = 12;
 constexpr int kSmemLimit = 232448;
 
 struct Misc {
   uint64_t full[kMaxBlocks], empty[kMaxBlocks];
+  uint64_t rope_full, rope_empty;  // the tile's RoPE block (a buffer of its own: it is free long before the others)
   uint64_t meta_full[kMeta];       // rows (and scales) of a tile are in place
-  uint64_t s_full[2], s_free[2];
+  uint64_t s_full[kMaxSBuf], s_free[kMaxSBuf];
   uint64_t p_full[2], p_free[2];
   uint64_t q_full;                 // a segment's query operand is built
   uint64_t pv_done[2];             // all PV products of the even, the odd tiles
   uint64_t final[2];               // drain of the two issuers
+  ChunkUnit unit[kSegs];           // of each segment, published with its first tile's rows
   uint32_t tmem_base;
   int abort;
-  __align__(16) int32_t rows[kMeta][kTile];   // pool row of each key, -1: masked
-  __align__(16) float sig[2][64];  // per segment parity: log2-domain factor of each query column
-  __align__(16) int vis[2][64];    // keys that it sees
-  __align__(16) float mrun[2][64]; // its running maximum
-  float red[4][4][16];             // [column quarter][lane quarter][column]
-  float linv[64], lse[64];
+  __align__(16) int32_t rows[kMeta][kTile];   // pool row of each key (TMA: of each box's first), -1: masked
+  __align__(16) float sig[2][32];  // per segment parity: log2-domain factor of each query column
+  __align__(16) int vis[2][32];    // keys that it sees
+  __align__(16) float nmax[2][32]; // minus its running maximum
+  __align__(16) float by[32], alpha[32];   // a move of the maxima, and its factor; at a segment's end 1 / l and LSE
+  float red[4][4][8];             // [column quarter][lane quarter][column]
+  float red_sc[4][4][4];           // [column quarter][lane quarter][group]
 };
-constexpr int kMiscBytes = 5632;
+constexpr int kMiscBytes = 5120;
 static_assert(sizeof(Misc) <= kMiscBytes, "misc area");
 
-template <int NC, int kLayout>
+template <int NC, int kLayout, bool kTma>
 struct Cfg {
   static constexpr bool kScaled = kLayout != DSA_KV_RAW512;
   static constexpr bool kRope = kLayout == DSA_KV_ROPE656;
-  static constexpr int R = kLayout == DSA_KV_RAW512 ? kRawRow : kLayout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
+  [[maybe_unused]] static constexpr int R = kLayout == DSA_KV_RAW512 ? kRawRow : kLayout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
   static constexpr int CPT = NC / 4;                 // query columns of a softmax thread
+  // Registers: the launch gives every thread LAUNCH_REGS; the softmax warps
+  // then take SMX_REGS and the others give back to OTHER_REGS.
+  static constexpr int THREADS = kTma ? 640 : 768;
+  static constexpr int LAUNCH_REGS = kTma ? 96 : 80;
+  static constexpr int SMX_REGS = kTma ? 104 : 88;
+  static constexpr int OTHER_REGS = (LAUNCH_REGS * THREADS - SMX_REGS * kSmxThreads) / (THREADS - kSmxThreads);
+  static_assert(SMX_REGS * kSmxThreads + OTHER_REGS * (THREADS - kSmxThreads) == LAUNCH_REGS * THREADS &&
+                SMX_REGS % 8 == 0 && OTHER_REGS % 8 == 0, "register split");
   static constexpr int G = kScaled ? 4 : 1;          // P operands of a tile
-  static constexpr int NPASS = G + (kRope ? 1 : 0);  // score passes of a tile
-  static constexpr int NB = kRope ? 5 : 4;           // ring blocks of a tile (RoPE first)
-  static constexpr int NQ = 2 * NC;                  // columns of the query operand: hi, lo
-  static constexpr int TERMS = 2;                    // E4M3 terms of P
-  static constexpr int S_COLS = NQ;
-  static constexpr int O_COL0 = 2 * S_COLS;
-  static constexpr int TMEM_COLS = O_COL0 + 4 * NC;  // 128, 256 or 512
-  static constexpr int Q_BYTES = NQ * 512;
+  static constexpr int NPASS = G + (kRope ? 1 : 0);  // score passes of a tile (RoPE first)
+  static constexpr int NQ = 2 * NC;                  // columns of the query and P operands: hi, lo
+  // score buffers, each of the PG passes that are read out together
+  static constexpr int PG = kScaled ? 2 : 1, S_COLS = PG * NQ;
+  static constexpr int SBUF = 4 * NQ + 4 * S_COLS <= 512 ? 4 : 2;
+  static constexpr int O_COL0 = SBUF * S_COLS;
+  static constexpr int TMEM_USED = O_COL0 + 4 * NQ;
+  static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
+  static constexpr int Q_BYTES = 2 * NC * 512;
   static constexpr int QR_BYTES = kRope ? NC * 128 : 0;
-  static constexpr int P_TERM = NC * 128;            // bytes of one term
-  static constexpr int P_BYTES = TERMS * P_TERM;
+  static constexpr int NPB = NC == 32 && kScaled ? 1 : 2;    // P operands (of all groups) in flight
+  static constexpr int P_GROUP = 2 * NC * 128;
+  static constexpr int P_BYTES = G * P_GROUP;
   static constexpr int SC_BYTES = kScaled ? kMeta * kTile * 16 : 0;
-  static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES;
-  static constexpr int NPB = 2;                      // P operands in flight
+  static constexpr int ROPE_BYTES = kRope ? kBlock : 0;
+  static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES + ROPE_BYTES;
   static constexpr int NS_FIT = (kSmemLimit - FIXED - NPB * P_BYTES) / kBlock;
   static constexpr int NS = NS_FIT < kMaxBlocks ? NS_FIT : kMaxBlocks;
-  static constexpr int Q_OFF = NS * kBlock;
+  static constexpr int ROPE_OFF = NS * kBlock;
+  static constexpr int Q_OFF = ROPE_OFF + ROPE_BYTES;
   static constexpr int QR_OFF = Q_OFF + Q_BYTES;
   static constexpr int P_OFF = QR_OFF + QR_BYTES;
   static constexpr int SC_OFF = P_OFF + NPB * P_BYTES;
   static constexpr int MISC_OFF = SC_OFF + SC_BYTES;
   static constexpr int SMEM = MISC_OFF + kMiscBytes + 1024;
-  static_assert(NS > NB, "a tile's blocks and one more");
+  static_assert(NS > 4, "a tile's blocks and one more");
   // a tile's rows are replaced kMeta tiles later, when its blocks are gone from the ring
   static_assert((NS - 1) / 4 + 1 < kMeta, "rows of a tile in use");
-  static_assert(SMEM <= kSmemLimit && TMEM_COLS <= 512 && P_TERM % 1024 == 0 && QR_BYTES % 1024 == 0, "budgets");
+  static_assert(SMEM <= kSmemLimit && TMEM_USED <= 512 && P_GROUP % 1024 == 0 && QR_BYTES % 1024 == 0, "budgets");
 };
 
 // Byte offset of element (n, k) in a K-major operand of N rows whose K extent
@@ -131,9 +157,9 @@ __device__ __forceinline__ uint32_t kmajor_off(int n, int k) {
 
 // Byte offset of P column n, key k in the MN-major PV operand without swizzle:
 // core matrices of 8 keys x 16 columns.
-template <int NC>
+template <int NP>
 __device__ __forceinline__ uint32_t p_off(int n, int k) {
-  return (n >> 4) * 128 + (k >> 3) * (NC * 8) + (k & 7) * 16 + (n & 15);
+  return (n >> 4) * 128 + (k >> 3) * (NP * 8) + (k & 7) * 16 + (n & 15);
 }
 
 // Leaves in lane l the max (or sum) over the 32 lanes of v[l % N].
@@ -181,15 +207,9 @@ template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
   if constexpr (N == 4) {
     tmem_ld4(taddr, v);
-  } else if constexpr (N == 8) {
-    tmem_ld8(taddr, v);
   } else {
-    static_assert(N == 16, "columns");
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
+    static_assert(N == 8, "columns");
+    tmem_ld8(taddr, v);
   }
 }
 template <int N>
@@ -197,41 +217,55 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N]) 
   if constexpr (N == 4) {
     tmem_st4(taddr, v);
   } else {
-#pragma unroll
-    for (int c = 0; c < N; c += 8) {
-      uint32_t t8[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) t8[k] = v[c + k];
-      tmem_st8(taddr + c, t8);
-    }
+    static_assert(N == 8, "columns");
+    tmem_st8(taddr, v);
   }
 }
 
-// Two E4M3 terms of a pair of weights, p ~ hi + lo, from the FP16 value of p
-// (the residual is exact in FP16).
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi2, uint32_t& lo2) {
-  uint32_t p, t, r;
+// Two E4M3 terms of a pair of FP16 values, p ~ hi + lo / 16 (the residual is
+// exact in FP16).
+__device__ __forceinline__ void split2(uint32_t p, uint32_t& hi2, uint32_t& lo2) {
+  uint32_t t, r;
   uint16_t h;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(v1), "f"(v0));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(p));
   hi2 = h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(t) : "h"(h));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(t));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0x4C004C00u));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(r));
   lo2 = h;
 }
 
-// N bytes (4, 8 or 16) held as pairs, to shared memory.
+// N bytes (4 or 8) held as pairs, to shared memory.
 template <int N>
 __device__ __forceinline__ void st_bytes(uint32_t addr, const uint32_t (&t)[N / 2]) {
-  if constexpr (N == 16)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(t[0] | t[1] << 16), "r"(t[2] | t[3] << 16),
-                 "r"(t[4] | t[5] << 16), "r"(t[6] | t[7] << 16)
-                 : "memory");
-  else if constexpr (N == 8)
+  if constexpr (N == 8)
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(t[0] | t[1] << 16), "r"(t[2] | t[3] << 16) : "memory");
   else
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(t[0] | t[1] << 16) : "memory");
+}
+
+// Two floats in one 64-bit register: half the instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // N consecutive values of a 16-byte aligned shared array (the same for the whole warp).
@@ -247,74 +281,112 @@ __device__ __forceinline__ void ld_row(const T* p, T (&v)[N]) {
   }
 }
 
-// A CTA's walk through its tiles.  A segment is the part of a unit inside the
-// CTA's range.  The next unit's entry is fetched while the current one is
-// worked on.
-struct Walk {
-  ChunkUnit u, next;
-  int unit, tile;
-  __device__ __forceinline__ static ChunkUnit fetch(const ChunkWork& w, int i, int n_units) {
-    union {
-      ChunkUnit u;
-      int4 v[3];
-    } x;
-    const int4* src = reinterpret_cast<const int4*>(w.units + (i < n_units ? i : n_units - 1));
-#pragma unroll
-    for (int k = 0; k < 3; ++k) x.v[k] = __ldcg(src + k);
-    return x.u;
-  }
-  __device__ __forceinline__ Walk(const ChunkWork& w, int first_unit, int64_t t0, int n_units) {
-    unit = first_unit;
-    u = fetch(w, unit, n_units);
-    next = fetch(w, unit + 1, n_units);
-    tile = (int)(t0 - u.tile0);
-  }
-  __device__ __forceinline__ void advance(const ChunkWork& w, int n_units) {
-    if (++tile == u.tiles) {
-      tile = 0;
-      u = next;
-      next = fetch(w, ++unit + 1, n_units);
-    }
-  }
-  __device__ __forceinline__ bool first(int it) const { return it == 0 || tile == 0; }
-  __device__ __forceinline__ bool last(int it, int n_it) const { return it == n_it - 1 || tile == u.tiles - 1; }
-};
-
+// A CTA's part of the tile list.
 struct Range {
   int64_t t0;
-  int n_it, unit, n_units;
+  int n_it;
+};
+
+// The producers' walk through a CTA's tiles.  A segment is the part of a unit
+// inside the CTA's range.  What they need of the next unit is fetched while the
+// current one is worked on: its request and lengths by every thread, one word
+// of its entry by each of the first twelve (for the other roles).
+struct Walk {
+  int unit, tile, tiles, b, last;
+  int next_tiles, next_b, next_last;
+  int32_t word, next_word;
+  static constexpr int kWords = sizeof(ChunkUnit) / 4;
+  __device__ __forceinline__ void fetch_next(const ChunkWork& w, int ptid) {
+    const ChunkUnit* u = w.units + unit + 1;     // (behind the last unit: read, never used)
+    next_tiles = __ldcg(&u->tiles);
+    next_b = __ldcg(&u->b);
+    next_last = __ldcg(&u->last);
+    if (ptid < kWords) next_word = __ldcg(reinterpret_cast<const int32_t*>(u) + ptid);
+  }
+  __device__ __forceinline__ Walk(const ChunkWork& w, int ptid, const Range& rg) {
+    const ChunkStart* s = w.starts + blockIdx.x;
+    unit = __ldcg(&s->unit);
+    tiles = __ldcg(&s->u.tiles);
+    b = __ldcg(&s->u.b);
+    last = __ldcg(&s->u.last);
+    tile = (int)(rg.t0 - __ldcg(&s->u.tile0));
+    word = next_word = 0;
+    if (ptid < kWords) word = __ldcg(reinterpret_cast<const int32_t*>(&s->u) + ptid);
+    fetch_next(w, ptid);
+  }
+  // true when the next tile starts a segment
+  __device__ __forceinline__ bool advance(const ChunkWork& w, int ptid) {
+    if (++tile < tiles) return false;
+    tile = 0;
+    tiles = next_tiles;
+    b = next_b;
+    last = next_last;
+    word = next_word;
+    ++unit;
+    fetch_next(w, ptid);
+    return true;
+  }
+};
+
+// The other roles' position: tiles left in the segment, from the units that
+// the producers published.
+struct Segment {
+  int seg = -1, left = 0;
+  // at a tile's start; true when it is its segment's first
+  __device__ __forceinline__ bool starts() const { return left == 0; }
+  __device__ __forceinline__ int open(const Misc& ms, const int64_t t0, int it, int n_it) {
+    ++seg;
+    const ChunkUnit& u = ms.unit[seg % kSegs];
+    const int tile = it == 0 ? (int)(t0 - u.tile0) : 0;
+    left = min(u.tiles - tile, n_it - it);
+    return tile;
+  }
+};
+
+// The unit's query rows into L2, ahead of their use (one thread).
+__device__ __forceinline__ void prefetch_queries(const ChunkArgs& a, const ChunkUnit& u) {
+  const uint16_t* src = a.q + u.row0 * a.q_row;
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"((uint32_t)(u.cols * a.q_row * 2)) : "memory");
+}
+
+struct ChunkMaps {
+  CUtensorMap rows, scales;
 };
 
 // ------------------------------------------------------------------- roles
 
-template <int NC, int kLayout>
+template <int NC, int kLayout, bool kTma>
 __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const Range& rg) {
-  using C = Cfg<NC, kLayout>;
+  using C = Cfg<NC, kLayout, kTma>;
   const ChunkArgs& a = w.a;
   const int ptid = threadIdx.x - kProdWarp0 * 32, pw = ptid >> 5, lane = ptid & 31;
   const int rq = lane >> 3, ch = lane & 7;
   volatile int* abort = &ms.abort;
   const uint32_t kv0 = smem_u32(sm);
   // thread -> key ptid of each tile: its page-table entry is fetched a tile ahead
-  Walk cur(w, rg.unit, rg.t0, rg.n_units);
+  Walk cur(w, ptid, rg);
   int32_t entry = -1, off = 0;
   bool seen = false;
   auto look_up = [&]() {
     const int j = cur.tile * kTile + ptid;
-    seen = ptid < kTile && j < chunk_visible(a, cur.u, cur.u.cols - 1);
+    seen = ptid < kTile && j < cur.last;
     if (seen) {
       const int page = j / a.page_size;
       off = j - page * a.page_size;
-      entry = __ldg(a.page_table + (int64_t)cur.u.b * a.max_pages + page);
+      entry = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
     }
   };
   look_up();
-  int slot = 0, phase = 0;
+  int slot = 0, phase = 0, seg = 0;
   bool ok = true;      // false once a wait gave up: keep going through every barrier
-  for (int it = 0; it < rg.n_it; ++it) {
-    const int m = it % kMeta;
+  bool opens = true;   // the tile starts a segment
+  auto acquire = [&]() {
     ok = ok && mbar_wait(smem_u32(&ms.empty[slot]), phase ^ 1, abort, w.wait_ns);
     ok = __all_sync(0xffffffffu, ok);
+  };
+  for (int it = 0; it < rg.n_it; ++it) {
+    const int m = it % kMeta;
+    acquire();
     if (ptid < kTile) {
       int32_t row = -1;
       if (seen) {
@@ -328,35 +400,41 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
                           a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kD, row >= 0 ? 16u : 0u);
     }
     if (C::kScaled) cp_async_arrive_noinc(smem_u32(&ms.meta_full[m]));
-    cur.advance(w, rg.n_units);
+    if (opens) {
+      if (ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
+      ++seg;
+    }
+    const bool opened = opens;
+    opens = cur.advance(w, ptid);
     if (it + 1 < rg.n_it) look_up();
-    named_bar_sync(2, kProdThreads);
-    if (ptid == 0) mbar_arrive(smem_u32(&ms.meta_full[m]));
-    int32_t rows[kQuadsPerWarp];
+    named_bar_sync(kProdBar, kProdThreads);
+    if (ptid == 0) {
+      mbar_arrive(smem_u32(&ms.meta_full[m]));
+      if (opened && seg > 1) prefetch_queries(a, ms.unit[(seg - 1) % kSegs]);
+    }
+    // 128 bytes of every row, from byte `col` of it
+    auto copy = [&](uint32_t base, int col, uint32_t bar) {
 #pragma unroll
-    for (int i = 0; i < kQuadsPerWarp; ++i) {
-      const int q = pw + i * kProdWarps;
-      rows[i] = q < kQuads ? ms.rows[m][4 * q + rq] : -1;
+      for (int i = 0; i < kQuadsPerWarp; ++i) {
+        const int q = pw + i * kProdWarps;
+        if (q >= kQuads) break;
+        const int r = 4 * q + rq;
+        const int32_t pr = ms.rows[m][r];
+        const uint8_t* src = a.pool + (int64_t)(pr >= 0 ? pr : 0) * C::R + col + ch * 16;
+        cp_async_16_zfill(base + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4), src, pr >= 0 ? 16u : 0u);
+      }
+      cp_async_arrive_noinc(bar);
+    };
+    if (C::kRope) {
+      ok = ok && mbar_wait(smem_u32(&ms.rope_empty), (it & 1) ^ 1, abort, w.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) copy(smem_u32(sm + C::ROPE_OFF), kScaledRow, smem_u32(&ms.rope_full));
     }
 #pragma unroll 1
-    for (int k = 0; k < C::NB; ++k) {
-      if (k > 0) {
-        ok = ok && mbar_wait(smem_u32(&ms.empty[slot]), phase ^ 1, abort, w.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      if (ok) {
-        const uint32_t base = kv0 + slot * kBlock;
-        const int col = (C::kRope ? (k == 0 ? kScaledRow : (k - 1) * 128) : k * 128) + ch * 16;
-#pragma unroll
-        for (int i = 0; i < kQuadsPerWarp; ++i) {
-          const int q = pw + i * kProdWarps;
-          if (q >= kQuads) break;
-          const int r = 4 * q + rq;
-          const uint8_t* src = a.pool + (int64_t)(rows[i] >= 0 ? rows[i] : 0) * C::R + col;
-          cp_async_16_zfill(base + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4), src, rows[i] >= 0 ? 16u : 0u);
-        }
-        cp_async_arrive_noinc(smem_u32(&ms.full[slot]));
-      }
+    for (int k = 0; k < 4; ++k) {
+      if (k > 0) acquire();
+      if (!ok) continue;
+      copy(kv0 + slot * kBlock, k * 128, smem_u32(&ms.full[slot]));
       if (++slot == C::NS) {
         slot = 0;
         phase ^= 1;
@@ -364,6 +442,111 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
     }
   }
   cp_async_wait_all();
+}
+
+__device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// One box of the map at (x, y): x a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// One warp; lane i < 128 / box translates and loads the tile's i-th box of every
+// block.  The copies themselves set the pace (a box of 64 rows takes about 130
+// cycles to issue, 64 bytes a clock), so each block is requested as soon as the
+// product that read its slot last has finished.
+template <int NC, int kLayout, bool kTma>
+__device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm, Misc& ms, const Range& rg) {
+  using C = Cfg<NC, kLayout, kTma>;
+  const ChunkArgs& a = w.a;
+  const int lane = threadIdx.x & 31, box = 1 << w.box_shift;
+  const bool mine = lane < (kTile >> w.box_shift);
+  volatile int* abort = &ms.abort;
+  const uint32_t kv0 = smem_u32(sm) + ((uint32_t)lane << (w.box_shift + 7));
+  Walk cur(w, lane, rg);
+  int32_t entry = -1, off = 0, want = 0;     // the next tile's: page-table entry, row in the page, keys seen of the box
+  auto look_up = [&]() {
+    const int j = cur.tile * kTile + (lane << w.box_shift);
+    want = mine ? min(box, cur.last - j) : 0;
+    if (want > 0) {
+      const int page = j / a.page_size;
+      off = j - page * a.page_size;
+      entry = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
+    }
+  };
+  look_up();
+  int slot = 0, phase = 0, seg = 0, issued = 0, metas = 0;
+  bool ok = true, opens = true;
+  for (int it = 0; it < rg.n_it && ok; ++it) {
+    const int m = it % kMeta;
+    int32_t row = -1;
+    if (want > 0) {
+      const int64_t r = (int64_t)entry * a.page_size + off;
+      const bool out = entry < 0 || r >= a.pool_rows;
+      if (!out) row = (int32_t)r;
+      if (out || r + want > a.pool_rows) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
+    }
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0)) << w.box_shift;   // rows to come
+    if (C::kRope) {
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ms.rope_empty), (it & 1) ^ 1, abort, w.wait_ns));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_tx(smem_u32(&ms.rope_full), n * 128);
+      __syncwarp();
+      if (row >= 0) tma_load(kv0 + C::ROPE_OFF, &maps.rows, kScaledRow, row, smem_u32(&ms.rope_full));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ms.empty[slot]), phase ^ 1, abort, w.wait_ns));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_tx(smem_u32(&ms.full[slot]), n * 128);
+      __syncwarp();
+      if (row >= 0) tma_load(kv0 + slot * kBlock, &maps.rows, k * 128, row, smem_u32(&ms.full[slot]));
+      issued = min(issued + 1, C::NS);
+      if (++slot == C::NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+      if (k == 0) {        // (the slot is free, so the tile kMeta before is out of the way)
+        ++metas;
+        if (mine) ms.rows[m][lane] = row;
+        if (opens) {
+          if (lane < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[lane] = cur.word;
+          __syncwarp();
+          if (lane == 0 && seg > 0) prefetch_queries(a, ms.unit[seg % kSegs]);
+          ++seg;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (C::kScaled) mbar_arrive_tx(smem_u32(&ms.meta_full[m]), n * 16);
+          else mbar_arrive(smem_u32(&ms.meta_full[m]));
+        }
+        if (C::kScaled) {
+          __syncwarp();
+          if (row >= 0)
+            tma_load(smem_u32(sm + C::SC_OFF) + m * kTile * 16 + ((uint32_t)lane << (w.box_shift + 4)), &maps.scales, kD, row,
+                     smem_u32(&ms.meta_full[m]));
+        }
+        opens = cur.advance(w, lane);
+        if (it + 1 < rg.n_it) look_up();
+      }
+    }
+  }
+  // nothing is left in flight when the CTA ends, not even after a wait gave up
+  volatile int no_abort = 0;
+  for (int i = 0; i < issued; ++i) {
+    if (slot == 0) phase ^= 1;
+    slot = slot == 0 ? C::NS - 1 : slot - 1;
+    mbar_wait(smem_u32(&ms.full[slot]), phase, &no_abort, 2000000000ull);
+  }
+  if (C::kRope && metas > 0) mbar_wait(smem_u32(&ms.rope_full), (metas - 1) & 1, &no_abort, 2000000000ull);
+  if (C::kScaled)
+    for (int i = max(0, metas - kMeta); i < metas; ++i)
+      mbar_wait(smem_u32(&ms.meta_full[i % kMeta]), (i / kMeta) & 1, &no_abort, 2000000000ull);
 }
 
 // Waits (bounded) for every tcgen05 operation this thread issued, so that the
@@ -374,49 +557,62 @@ __device__ __forceinline__ void drain_mma(uint32_t bar) {
   mbar_wait(bar, 0, &no_abort, 2000000000ull);
 }
 
-template <int NC, int kLayout>
+template <int NC, int kLayout, bool kTma>
 __device__ void qk_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem, const Range& rg) {
-  using C = Cfg<NC, kLayout>;
+  using C = Cfg<NC, kLayout, kTma>;
   if ((threadIdx.x & 31) != 0) return;
   volatile int* abort = &ms.abort;
   const uint32_t kv0 = smem_u32(sm);
   constexpr uint32_t kId = idesc_e4m3(C::NQ, false), kIdRope = idesc_bf16(NC);
   const uint64_t q_desc = sdesc_sw128(smem_u32(sm + C::Q_OFF), 16, 1024);
-  Walk cur(w, rg.unit, rg.t0, rg.n_units);
-  int slot = 0, phase = 0, seg = -1, si = 0;
+  Segment sg;
+  int slot = 0, phase = 0, sb = 0, s_phase = 1;      // a fresh score buffer is free
   bool ok = true;
-  for (int it = 0; it < rg.n_it && ok; ++it, cur.advance(w, rg.n_units)) {
-    if (cur.first(it)) {
-      ++seg;
-      ok = mbar_wait(smem_u32(&ms.q_full), seg & 1, abort, w.wait_ns);
+  for (int it = 0; it < rg.n_it && ok; ++it, --sg.left) {
+    if (sg.starts()) {
+      ok = mbar_wait(smem_u32(&ms.q_full), (sg.seg + 1) & 1, abort, w.wait_ns);
+      if (!ok) break;
+      sg.open(ms, rg.t0, it, rg.n_it);
     }
-#pragma unroll 1
-    for (int k = 0; k < C::NB && ok; ++k) {
-      const int sb = si & 1;
-      const bool opens = C::kScaled || k == 0;     // first block of a score pass
-      if (opens && si >= 2) ok = mbar_wait(smem_u32(&ms.s_free[sb]), ((si >> 1) - 1) & 1, abort, w.wait_ns);
+    // pass p: its score buffer, free when its first pass begins, handed over after its last
+    auto score_buffer = [&](int p) { return p % C::PG != 0 || mbar_wait(smem_u32(&ms.s_free[sb]), s_phase, abort, w.wait_ns); };
+    auto scored = [&](int p) {
+      if (p % C::PG != C::PG - 1 && p != C::NPASS - 1) return;
+      mma_commit(smem_u32(&ms.s_full[sb]));
+      if (++sb == C::SBUF) {
+        sb = 0;
+        s_phase ^= 1;
+      }
+    };
+    if (C::kRope) {
+      ok = score_buffer(0) && mbar_wait(smem_u32(&ms.rope_full), it & 1, abort, w.wait_ns);
+      if (!ok) break;
+      if (!kTma) fence_proxy_async_smem();   // rows landed through cp.async (generic proxy)
+      tc_fence_after();
+      const uint64_t ad = sdesc_sw128(kv0 + C::ROPE_OFF, 16, 1024), bd = sdesc_sw128(smem_u32(sm + C::QR_OFF), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16(tmem + sb * C::S_COLS, desc_add(ad, kk * 32), desc_add(bd, kk * 32), kIdRope, kk > 0 ? 1u : 0u);
+      mma_commit(smem_u32(&ms.rope_empty));
+      scored(0);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool opens = C::kScaled || k == 0;       // first block of a score pass
+      const int p = C::kScaled ? k + (C::kRope ? 1 : 0) : 0;
+      if (opens) ok = score_buffer(p);
       ok = ok && mbar_wait(smem_u32(&ms.full[slot]), phase, abort, w.wait_ns);
       if (!ok) break;
-      fence_proxy_async_smem();   // rows landed through cp.async (generic proxy)
+      if (!kTma) fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t ad = sdesc_sw128(kv0 + slot * kBlock, 16, 1024);
-      const uint32_t d = tmem + sb * C::S_COLS;
-      if (C::kRope && k == 0) {
-        const uint64_t bd = sdesc_sw128(smem_u32(sm + C::QR_OFF), 16, 1024);
+      const uint64_t bd = desc_add(q_desc, k * (C::NQ * 128));
+      const uint32_t d = tmem + sb * C::S_COLS + p % C::PG * C::NQ;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_bf16(d, desc_add(ad, kk * 32), desc_add(bd, kk * 32), kIdRope, kk > 0 ? 1u : 0u);
-        mma_commit(smem_u32(&ms.empty[slot]));
-      } else {
-        const int g = C::kRope ? k - 1 : k;
-        const uint64_t bd = desc_add(q_desc, g * (C::NQ * 128));
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_e4m3(d, desc_add(ad, kk * 32), desc_add(bd, kk * 32), kId, (!opens || kk > 0) ? 1u : 0u);
+      for (int kk = 0; kk < 4; ++kk) {
+        mma_e4m3(d, desc_add(ad, kk * 32), desc_add(bd, kk * 32), kId, (!opens || kk > 0) ? 1u : 0u);
       }
-      if (C::kScaled || k == C::NB - 1) {
-        mma_commit(smem_u32(&ms.s_full[sb]));
-        ++si;
-      }
+      if (C::kScaled || k == 3) scored(p);
       if (++slot == C::NS) {
         slot = 0;
         phase ^= 1;
@@ -426,46 +622,39 @@ __device__ void qk_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem
   drain_mma(smem_u32(&ms.final[0]));
 }
 
-template <int NC, int kLayout>
+template <int NC, int kLayout, bool kTma>
 __device__ void pv_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem, const Range& rg) {
-  using C = Cfg<NC, kLayout>;
+  using C = Cfg<NC, kLayout, kTma>;
   if ((threadIdx.x & 31) != 0) return;
   volatile int* abort = &ms.abort;
   const uint32_t kv0 = smem_u32(sm);
-  constexpr uint32_t kId = idesc_e4m3(NC, true, true);
-  const uint64_t p_desc = sdesc_mn_none(smem_u32(sm + C::P_OFF), NC * 8, 128);
-  Walk cur(w, rg.unit, rg.t0, rg.n_units);
-  int slot = 0, pi = 0;
+  constexpr uint32_t kId = idesc_e4m3(C::NQ, true, true);
+  const uint64_t p_desc = sdesc_mn_none(smem_u32(sm + C::P_OFF), C::NQ * 8, 128);
+  Segment sg;
+  int slot = 0;
   bool ok = true;
   auto step = [&]() { slot = slot + 1 == C::NS ? 0 : slot + 1; };
-  for (int it = 0; it < rg.n_it && ok; ++it, cur.advance(w, rg.n_units)) {
-    const bool first = cur.first(it);
-    if (C::kRope) step();                          // the RoPE block is QK^T's alone
-#pragma unroll 1
+  for (int it = 0; it < rg.n_it && ok; ++it, --sg.left) {
+    const bool first = sg.starts();
+    const int pb = it % C::NPB;
+#pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int pb = pi % C::NPB;
-      if (C::kScaled || g == 0) {
-        ok = mbar_wait(smem_u32(&ms.p_full[pb]), (pi / C::NPB) & 1, abort, w.wait_ns);
+      if (g == 0) {
+        ok = mbar_wait(smem_u32(&ms.p_full[pb]), (it / C::NPB) & 1, abort, w.wait_ns);
         if (!ok) break;
-        fence_proxy_async_smem();   // P and the rows were written through the generic proxy
         tc_fence_after();
+        if (first) sg.open(ms, rg.t0, it, rg.n_it);
       }
       const uint64_t ad = sdesc_sw128(kv0 + slot * kBlock, 1024, 1024);
-      const uint64_t bd = desc_add(p_desc, pb * C::P_BYTES);
-      const uint32_t d = tmem + C::O_COL0 + g * NC;
+      const uint64_t bd = desc_add(p_desc, pb * C::P_BYTES + (C::kScaled ? g * C::P_GROUP : 0));
+      const uint32_t d = tmem + C::O_COL0 + g * C::NQ;
 #pragma unroll
-      for (int t = 0; t < C::TERMS; ++t)
-#pragma unroll
-        for (int js = 0; js < 4; ++js)
-          mma_e4m3(d, desc_add(ad, js * 4096), desc_add(bd, t * C::P_TERM + js * 4 * (NC * 8)), kId,
-                   (t > 0 || js > 0) ? 1u : (first ? 0u : 1u));
+      for (int js = 0; js < 4; ++js)
+        mma_e4m3(d, desc_add(ad, js * 4096), desc_add(bd, js * 4 * (C::NQ * 8)), kId, js > 0 ? 1u : (first ? 0u : 1u));
       mma_commit(smem_u32(&ms.empty[slot]));
       step();
-      if (C::kScaled || g == 3) {
-        mma_commit(smem_u32(&ms.p_free[pb]));
-        ++pi;
-      }
     }
+    if (ok) mma_commit(smem_u32(&ms.p_free[pb]));
     if (ok) mma_commit(smem_u32(&ms.pv_done[it & 1]));
   }
   drain_mma(smem_u32(&ms.final[1]));
@@ -473,9 +662,9 @@ __device__ void pv_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem
 
 // The query operand of one segment, and its columns' factors, visible keys and
 // maxima.  512 threads: column tid / TPH, dims [DPT (tid % TPH), + DPT).
-template <int NC, int kLayout>
+template <int NC, int kLayout, bool kTma>
 __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Misc& ms, const ChunkUnit& u, int par) {
-  using C = Cfg<NC, kLayout>;
+  using C = Cfg<NC, kLayout, kTma>;
   constexpr int TPH = kSmxThreads / NC, DPT = kD / TPH, NV = DPT / 8;
   const ChunkArgs& a = w.a;
   const int col = threadIdx.x / TPH, part = threadIdx.x % TPH;
@@ -485,14 +674,6 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     v[i] = live_col ? __ldg(reinterpret_cast<const uint4*>(src + part * DPT) + i) : make_uint4(0, 0, 0, 0);
-  if constexpr (C::kRope) {
-    const int rc = threadIdx.x >> 3, ch = threadIdx.x & 7;      // column, 16-byte chunk of its 64 RoPE dims
-    if (rc < NC) {
-      const uint4 x = rc < u.cols ? __ldg(reinterpret_cast<const uint4*>(a.q + (u.row0 + rc) * a.q_row + kD) + ch)
-                                  : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(sm + C::QR_OFF + (rc >> 3) * 1024 + (rc & 7) * 128 + ((ch ^ (rc & 7)) << 4)) = x;
-    }
-  }
   float amax = 0.f;
   bool nan = false;
 #pragma unroll
@@ -510,187 +691,278 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
   for (int off = TPH / 2; off >= 1; off /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   int sh = 0;
   const float base = a.sm_scale * kLog2e;
-  float sig = 0.f;
+  float sig = base;
   const bool live = amax > 0.f && amax <= 1.0e38f;
   if (live) {
     int e;
     const float f = frexpf(amax, &e);                // amax = f 2^e, f in [0.5, 1)
-    sh = f <= 0.875f ? 9 - e : 8 - e;                // largest sh with amax 2^sh <= 448
+    sh = min(f <= 0.875f ? 9 - e : 8 - e, 64);       // largest sh with amax 2^sh <= 448 (and the RoPE dims in range)
     sig = scale_pow2(base, -sh);
   } else if (amax > 0.f) {
     sig = __int_as_float(0x7FC00000);                // a row with a NaN or an infinity scores NaN
   }
   uint8_t* qb = sm + C::Q_OFF;
+  const float up = live ? __int_as_float((127 + sh) << 23) : 0.f;   // 2^sh, sh in [-120, 64]
 #pragma unroll
   for (int c = 0; c < NV / 2; ++c) {
-    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-    if (live) {
-      const uint32_t x[8] = {v[2 * c].x, v[2 * c].y, v[2 * c].z, v[2 * c].w,
-                             v[2 * c + 1].x, v[2 * c + 1].y, v[2 * c + 1].z, v[2 * c + 1].w};
+    uint32_t hi[4], lo[4];
+    const uint32_t x[8] = {v[2 * c].x, v[2 * c].y, v[2 * c].z, v[2 * c].w,
+                           v[2 * c + 1].x, v[2 * c + 1].y, v[2 * c + 1].z, v[2 * c + 1].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y[4], yh[4];
-        y[0] = scale_pow2(bf16_bits_to_f32(x[2 * i] & 0xFFFFu), sh);
-        y[1] = scale_pow2(bf16_bits_to_f32(x[2 * i] >> 16), sh);
-        y[2] = scale_pow2(bf16_bits_to_f32(x[2 * i + 1] & 0xFFFFu), sh);
-        y[3] = scale_pow2(bf16_bits_to_f32(x[2 * i + 1] >> 16), sh);
-        hi[i] = e4m3x4_satrne(y[0], y[1], y[2], y[3]);
-        e4m3x4_to_f32(hi[i], yh);
-        lo[i] = e4m3x4_satrne((y[0] - yh[0]) * 16.f, (y[1] - yh[1]) * 16.f, (y[2] - yh[2]) * 16.f, (y[3] - yh[3]) * 16.f);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h2[2], l2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {        // exact in FP16 down to steps of 2^-24
+        const uint32_t q2 = live ? x[2 * i + j] : 0u;
+        uint32_t y;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(bf16_bits_to_f32(q2 >> 16) * up), "f"(bf16_bits_to_f32(q2 & 0xFFFFu) * up));
+        split2(y, h2[j], l2[j]);
       }
+      hi[i] = h2[0] | h2[1] << 16;
+      lo[i] = l2[0] | l2[1] << 16;
     }
     const int k0 = part * DPT + 16 * c;
     *reinterpret_cast<uint4*>(qb + kmajor_off<C::NQ>(col, k0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(qb + kmajor_off<C::NQ>(NC + col, k0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
+  if constexpr (C::kRope) {                          // 64 RoPE dims: part p holds [64 p / TPH, + 64 / TPH)
+    constexpr int RD = kRopeDims / TPH;              // 2, 4 or 8 dims
+    uint32_t x[RD / 2];
+#pragma unroll
+    for (int i = 0; i < RD / 2; ++i) {
+      const uint32_t q2 = live_col ? __ldg(reinterpret_cast<const uint32_t*>(src + kD + part * RD) + i) : 0u;
+      const __nv_bfloat162 y = __floats2bfloat162_rn(scale_pow2(bf16_bits_to_f32(q2 & 0xFFFFu), sh),
+                                                     scale_pow2(bf16_bits_to_f32(q2 >> 16), sh));
+      x[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    const int byte = part * RD * 2;                  // of the column's 128
+    uint8_t* dst = sm + C::QR_OFF + (col >> 3) * 1024 + (col & 7) * 128 + (((byte >> 4) ^ (col & 7)) << 4) + (byte & 15);
+#pragma unroll
+    for (int i = 0; i < RD / 2; ++i) reinterpret_cast<uint32_t*>(dst)[i] = x[i];
+  }
   if (part == 0) {
     ms.sig[par][col] = sig;
     ms.vis[par][col] = live_col ? chunk_visible(a, u, col) : 0;
-    ms.mrun[par][col] = kNoMax;
+    ms.nmax[par][col] = 0.f;
   }
   fence_proxy_async_smem();
   warp_arrive(smem_u32(&ms.q_full));
 }
 
-template <int NC, int kLayout>
+template <int NC, int kLayout, bool kTma>
 __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem, const Range& rg) {
-  using C = Cfg<NC, kLayout>;
-  constexpr int CPT = C::CPT;
+  using C = Cfg<NC, kLayout, kTma>;
+  constexpr int CPT = C::CPT, CP2 = CPT / 2;
   const ChunkArgs& a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, cq = warp >> 2;
   const int row = 32 * quarter + lane;                   // key of the tile = TMEM lane (dim of a block, for O)
   const int c0 = cq * CPT;                               // first column
-  const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+  const int bar = 1 + cq;                                // the four warps of a column quarter
+  const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + c0;
   volatile int* abort = &ms.abort;
-  float l_part[CPT];
-  float m_lane = kNoMax;                                 // running maximum of column c0 + lane % CPT
-  int seg = -1, si = 0, pi = 0, slot0 = 0;               // slot0: ring slot of the tile's first latent block
+  uint64_t l_part[CP2];                                  // this row's share of the denominators
+  float m_lane = 0.f;                                    // running maximum of column c0 + lane % CPT (0: none yet)
+  bool has = false;                                      // it is that of a key, or the column sees none at all
+  bool pending = true;                                   // a column of the quarter still has none
+  float cg[4] = {1.f, 1.f, 1.f, 1.f};                    // c_g
+  int sb = 0, s_phase = 0;
+  int slot0 = 0;                                         // ring slot of the tile's first block
+  int tile = 0, last = 0;                                // tile of the unit, keys that anyone sees
   bool ok = true;                                        // false once a wait gave up: keep going through every barrier
-  if (C::kRope) slot0 = 1;
-  Walk cur(w, rg.unit, rg.t0, rg.n_units);
-  build_query<NC, kLayout>(w, sm, ms, cur.u, 0);
+  Segment sg;
+  ok &= mbar_wait(smem_u32(&ms.meta_full[0]), 0, abort, w.wait_ns);
+  build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[0], 0);
   for (int it = 0; it < rg.n_it; ++it) {
-    const bool first = cur.first(it), last = cur.last(it, rg.n_it);
+    const bool first = sg.starts();
     const int m = it % kMeta;
-    if (first) {
-      ++seg;
-      ok &= mbar_wait(smem_u32(&ms.q_full), seg & 1, abort, w.wait_ns);
-      m_lane = kNoMax;
-#pragma unroll
-      for (int k = 0; k < CPT; ++k) l_part[k] = 0.f;
-    }
-    const int par = seg & 1;
     ok &= mbar_wait(smem_u32(&ms.meta_full[m]), (it / kMeta) & 1, abort, w.wait_ns);
-    const int j = cur.tile * kTile + row;
-    const bool valid = ms.rows[m][row] >= 0;
-    float sc[4] = {1.f, 1.f, 1.f, 1.f}, lsc = 0.f;
+    if (first) {
+      ok &= mbar_wait(smem_u32(&ms.q_full), (sg.seg + 1) & 1, abort, w.wait_ns);
+      tile = sg.open(ms, rg.t0, it, rg.n_it);
+      last = ms.unit[sg.seg % kSegs].last;
+      m_lane = 0.f;
+      has = ms.vis[sg.seg & 1][c0 + lane % CPT] == 0;
+      pending = true;
+#pragma unroll
+      for (int k = 0; k < CP2; ++k) l_part[k] = 0;
+    }
+    --sg.left;
+    const int par = sg.seg & 1;
+    const int j = tile * kTile + row;
+    const int32_t pool_row = ms.rows[m][row >> w.box_shift];
+    const bool valid = pool_row >= 0 && j < last &&
+                       (!kTma || (int64_t)pool_row + (row & ((1 << w.box_shift) - 1)) < a.pool_rows);
+    float sc[4] = {1.f, 1.f, 1.f, 1.f};
+    float lsc = 0.f, inv = 1.f;                          // log2 S and 1 / S, S = 2^(e - 126)
+    bool odd_scale = false;
     if (C::kScaled) {
       const float4 v = *reinterpret_cast<const float4*>(sm + C::SC_OFF + (m * kTile + row) * 16);
       sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
-      const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-      lsc = fminf(fmaxf(log2f(big), -100.f), 100.f);     // rows of no magnitude add next to nothing to any output
+      const uint32_t big = max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
+                               max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
+      odd_scale = big >= 0x7F800000u;
+      const int e = min(max((int)(big >> 23), 66), 252); // S within 2^-60 .. 2^126
+      lsc = (float)(e - 126);
+      inv = __int_as_float((253 - e) << 23);
     }
-    // scores
-    float s2[CPT];
+    // scores: the passes' sums, then times the column's factor
+    uint64_t s2[CP2];
     bool poisoned = false;                               // a NaN byte in the row: every column's sum is NaN
 #pragma unroll
-    for (int pass = 0; pass < C::NPASS; ++pass) {
-      const int sb = si & 1;
-      ok &= mbar_wait(smem_u32(&ms.s_full[sb]), (si >> 1) & 1, abort, w.wait_ns);
-      ++si;
-      tc_fence_after();
-      const uint32_t base = lane_base + sb * C::S_COLS + c0;
-      if (C::kRope && pass == 0) {
-        uint32_t v[CPT];
-        tmem_ld<CPT>(base, v);
-        tmem_wait_ld();
-        const float rsig = a.sm_scale * kLog2e;
+    for (int p = 0; p < C::NPASS; ++p) {
+      if (p % C::PG == 0) {
+        ok &= mbar_wait(smem_u32(&ms.s_full[sb]), s_phase, abort, w.wait_ns);
+        tc_fence_after();
+      }
+      const bool rope = C::kRope && p == 0;
+      const bool two = !rope;
+      const int g = C::kRope ? p - 1 : p;
+      const uint32_t at = lane_base + sb * C::S_COLS + p % C::PG * C::NQ;
+      const uint64_t f2 = pack2(sc[rope ? 0 : g], sc[rope ? 0 : g]);
+      uint32_t v[CPT], lo[CPT];
+      tmem_ld<CPT>(at, v);
+      if (two) tmem_ld<CPT>(at + NC, lo);
+      tmem_wait_ld();
+      if (p % C::PG == C::PG - 1 || p == C::NPASS - 1) {
+        tc_fence_before();
+        warp_arrive(smem_u32(&ms.s_free[sb]));
+      }
+      if (!rope) poisoned |= __uint_as_float(v[0]) != __uint_as_float(v[0]);
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) s2[k] = __uint_as_float(v[k]) * rsig;
-      } else {
-        const int g = C::kRope ? pass - 1 : pass;
-        uint32_t hi[CPT], lo[CPT];
-        tmem_ld<CPT>(base, hi);
-        tmem_ld<CPT>(base + NC, lo);
-        tmem_wait_ld();
-        float sg[CPT];
-        ld_row<CPT>(&ms.sig[par][c0], sg);
-        poisoned |= __uint_as_float(hi[0]) != __uint_as_float(hi[0]);
-#pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-          const float v = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k])) * sg[k];
-          s2[k] = !C::kScaled ? v : (pass == 0) ? v * sc[g] : fmaf(v, sc[g], s2[k]);
+      for (int k = 0; k < CPT; k += 2) {
+        uint64_t t = pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+        if (two) t = fma2(pack2(__uint_as_float(lo[k]), __uint_as_float(lo[k + 1])), pack2(0.0625f, 0.0625f), t);
+        uint64_t& d = s2[k / 2];
+        if (!C::kScaled || rope) d = t;
+        else if (p == 0) d = mul2(t, f2);
+        else d = fma2(t, f2, d);
+      }
+      if (p % C::PG == C::PG - 1 || p == C::NPASS - 1) {
+        if (++sb == C::SBUF) {
+          sb = 0;
+          s_phase ^= 1;
         }
       }
-      tc_fence_before();
-      warp_arrive(smem_u32(&ms.s_free[sb]));
+    }
+    // x = s + log2 S - M
+    float x[CPT];
+    {
+      float sig[CPT], nm[CPT];
+      ld_row<CPT>(&ms.nmax[par][c0], nm);
+      ld_row<CPT>(&ms.sig[par][c0], sig);
+#pragma unroll
+      for (int k = 0; k < CPT; k += 2) {
+        uint64_t o = pack2(nm[k], nm[k + 1]);
+        if (C::kScaled) o = add2(o, pack2(lsc, lsc));
+        unpack2(fma2(s2[k / 2], pack2(sig[k], sig[k + 1]), o), x[k], x[k + 1]);
+      }
     }
     // a row with an infinite or NaN scale holds infinities of both signs and NaN: it scores NaN
-    const bool odd_scale = C::kScaled && !(fabsf(sc[0]) + fabsf(sc[1]) + fabsf(sc[2]) + fabsf(sc[3]) < INFINITY);
     if (odd_scale) {
 #pragma unroll
-      for (int k = 0; k < CPT; ++k) s2[k] = __int_as_float(0x7FC00000);
+      for (int k = 0; k < CPT; ++k) x[k] = __int_as_float(0x7FC00000);
     }
     // keys that a column does not see
-    if (!__all_sync(0xffffffffu, valid && cur.tile * kTile + kTile <= ms.vis[par][0])) {
+    if (!__all_sync(0xffffffffu, valid && tile * kTile + kTile <= ms.vis[par][0])) {
       int vis[CPT];
       ld_row<CPT>(&ms.vis[par][c0], vis);
 #pragma unroll
       for (int k = 0; k < CPT; ++k)
-        if (!valid || j >= vis[k]) s2[k] = -INFINITY;
+        if (!valid || j >= vis[k]) x[k] = -INFINITY;
     }
-    // Does a column's running maximum have to move?  One barrier ORs the
-    // threads' answers; only then are the tile's maxima formed.
-    float mr[CPT];
-    ld_row<CPT>(&ms.mrun[par][c0], mr);
-    bool grow = false;
+    // Does a column's running maximum have to move, or a c_g?  One barrier of
+    // the column quarter's warps ORs the threads' answers; only then are the
+    // tile's maxima formed.
+    float top = x[0];
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) grow |= s2[k] + lsc > mr[k] + kTop;
-    if (named_bar_red_or(1, kSmxThreads, grow)) {
+    for (int k = 1; k < CPT; ++k) top = fmaxf(top, x[k]);
+    bool grow = pending || top > kTop;
+    float rel[4];                                        // s_g / S, at most 1
+    if (C::kScaled) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        rel[g] = valid && !odd_scale ? fabsf(sc[g]) * inv : 0.f;
+        grow |= rel[g] * cg[g] > 1.f;
+      }
+    }
+    if (named_bar_red_or(bar, 128, grow)) {
       float tmp[CPT];
 #pragma unroll
-      for (int k = 0; k < CPT; ++k) tmp[k] = s2[k] + lsc;
+      for (int k = 0; k < CPT; ++k) tmp[k] = x[k];
       const float wmax = transpose_reduce<CPT, true>(tmp, lane);
       if (lane < CPT) ms.red[cq][quarter][lane] = wmax;
-      named_bar_sync(1, kSmxThreads);
+      if (C::kScaled) {
+        float t4[4] = {rel[0], rel[1], rel[2], rel[3]};
+        const float wsc = transpose_reduce<4, true>(t4, lane);
+        if (lane < 4) ms.red_sc[cq][quarter][lane] = wsc;
+      }
+      named_bar_sync(bar, 128);
       const int cl = lane % CPT;
       const float tmax = fmaxf(fmaxf(ms.red[cq][0][cl], ms.red[cq][1][cl]), fmaxf(ms.red[cq][2][cl], ms.red[cq][3][cl]));
-      float alpha_lane = 1.f;
-      const bool need = tmax > m_lane + kTop;
-      if (need) {
-        const float to = tmax - kBias;
-        alpha_lane = ex2_approx(m_lane - to);
-        m_lane = to;
-      }
-      const unsigned moved = __ballot_sync(0xffffffffu, need);
-      if (quarter == 0 && lane < CPT) ms.mrun[par][c0 + lane] = m_lane;
-      if (moved) {
+      const bool need = has ? tmax > kTop : tmax > -INFINITY;
+      const float by = need ? tmax : 0.f;        // the maximum moves by this much
+      const float alpha_lane = need ? (has ? ex2_approx(-by) : 0.f) : 1.f;   // (nothing summed before the first key)
+      has |= need;
+      m_lane += by;
+      bool moved = __any_sync(0xffffffffu, need);
+      float beta[4] = {1.f, 1.f, 1.f, 1.f};
+      if (C::kScaled) {
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) l_part[k] *= __shfl_sync(0xffffffffu, alpha_lane, k);
+        for (int g = 0; g < 4; ++g) {
+          const float mx = fmaxf(fmaxf(ms.red_sc[cq][0][g], ms.red_sc[cq][1][g]), fmaxf(ms.red_sc[cq][2][g], ms.red_sc[cq][3][g]));
+          if (pending || mx * cg[g] > 1.f) {             // c_g: the reciprocal of the power of two above mx
+            const int e = max((int)((__float_as_uint(mx) + 0x7FFFFFu) >> 23), 127 - 24);
+            const float c = __int_as_float((254 - e) << 23);
+            beta[g] = c / cg[g];
+            cg[g] = c;
+            moved = true;
+          }
+        }
+      }
+      pending = __any_sync(0xffffffffu, !has);
+      if (quarter == 0 && lane < CPT) {
+        ms.nmax[par][c0 + lane] = -m_lane;
+        ms.by[c0 + lane] = by;
+        ms.alpha[c0 + lane] = alpha_lane;
+      }
+      named_bar_sync(bar, 128);
+      if (moved) {
+        float f[CPT];
+        ld_row<CPT>(&ms.by[c0], f);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) x[k] -= f[k];
+        ld_row<CPT>(&ms.alpha[c0], f);
+#pragma unroll
+        for (int k = 0; k < CP2; ++k) l_part[k] = mul2(l_part[k], pack2(f[2 * k], f[2 * k + 1]));
         if (!first) {      // O holds this segment's earlier tiles
           ok &= mbar_wait(smem_u32(&ms.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, abort, w.wait_ns);
           tc_fence_after();
 #pragma unroll 1
-          for (int db = 0; db < 4; ++db) {
-            uint32_t v[CPT];
-            tmem_ld<CPT>(lane_base + C::O_COL0 + db * NC + c0, v);
-            tmem_wait_ld();
+          for (int g = 0; g < 4; ++g) {
+            const float bg = g == 0 ? beta[0] : g == 1 ? beta[1] : g == 2 ? beta[2] : beta[3];
 #pragma unroll
-            for (int k = 0; k < CPT; ++k)
-              v[k] = __float_as_uint(__uint_as_float(v[k]) * __shfl_sync(0xffffffffu, alpha_lane, k));
-            tmem_st<CPT>(lane_base + C::O_COL0 + db * NC + c0, v);
+            for (int t = 0; t < 2; ++t) {                // hi, lo
+              const uint32_t at = lane_base + C::O_COL0 + g * C::NQ + t * NC;
+              uint32_t v[CPT];
+              tmem_ld<CPT>(at, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < CPT; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * (f[k] * bg));
+              tmem_st<CPT>(at, v);
+            }
           }
           tmem_wait_st();
         }
       }
-      named_bar_sync(1, kSmxThreads);
-      ld_row<CPT>(&ms.mrun[par][c0], mr);
     }
+    const uint64_t inv2 = pack2(inv, inv);
+    uint32_t p2[CP2];                                    // P operands come from the FP16 values of the weights (11 significant bits)
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-      s2[k] = ex2_approx(s2[k] - mr[k]);
-      l_part[k] += s2[k];
+    for (int k = 0; k < CP2; ++k) {
+      const float p0 = ex2_approx(x[2 * k]), p1 = ex2_approx(x[2 * k + 1]);
+      l_part[k] = C::kScaled ? fma2(pack2(p0, p1), inv2, l_part[k]) : add2(l_part[k], pack2(p0, p1));
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p2[k]) : "f"(p1), "f"(p0));
     }
     if (poisoned) {
       // The row counts as NaN for the columns that see it (p is NaN already);
@@ -704,75 +976,98 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     }
     // every phase of pv_done is waited for, two tiles on, so that its parity tells the tiles apart
     if (it >= 2) ok &= mbar_wait(smem_u32(&ms.pv_done[it & 1]), ((it >> 1) - 1) & 1, abort, w.wait_ns);
-    // P operands
+    const int pb = it % C::NPB;
+    const uint32_t at = smem_u32(sm + C::P_OFF) + pb * C::P_BYTES;
 #pragma unroll
     for (int g = 0; g < C::G; ++g) {
-      const int pb = pi % C::NPB;
-      uint32_t hi2[CPT / 2], lo2[CPT / 2];
-#pragma unroll
-      for (int k = 0; k < CPT; k += 2) {
-        float v0 = s2[k], v1 = s2[k + 1];
-        if (C::kScaled) {
-          v0 *= sc[g];
-          v1 *= sc[g];
-          if (odd_scale) {                               // a weight of 0 times an infinite scale is 0
-            if (s2[k] == 0.f) v0 = 0.f;
-            if (s2[k + 1] == 0.f) v1 = 0.f;
-          }
-        }
-        split2(v0, v1, hi2[k / 2], lo2[k / 2]);
+      uint32_t hi2[CP2], lo2[CP2];
+      uint32_t f2 = 0;
+      if (C::kScaled) {
+        // a row that nobody sees may hold any scale: its weights of 0 stay 0
+        const float f = odd_scale ? 1.f : valid ? sc[g] * inv * cg[g] : 0.f;
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(f2) : "f"(f));
       }
-      if (pi >= C::NPB) ok &= mbar_wait(smem_u32(&ms.p_free[pb]), ((pi / C::NPB) - 1) & 1, abort, w.wait_ns);
-      const uint32_t at = smem_u32(sm + C::P_OFF) + pb * C::P_BYTES + p_off<NC>(c0, row);
-      st_bytes<CPT>(at, hi2);
-      st_bytes<CPT>(at + C::P_TERM, lo2);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      warp_arrive(smem_u32(&ms.p_full[pb]));
-      ++pi;
+#pragma unroll
+      for (int k = 0; k < CP2; ++k) {
+        uint32_t v = p2[k];
+        if (C::kScaled) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(f2));
+        split2(v, hi2[k], lo2[k]);
+      }
+      if (g == 0 && it >= C::NPB)
+        ok &= mbar_wait(smem_u32(&ms.p_free[pb]), ((it / C::NPB) - 1) & 1, abort, w.wait_ns);
+      st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(c0, row), hi2);
+      st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(NC + c0, row), lo2);
     }
-    slot0 += C::NB;
+    fence_proxy_async_smem();
+    tc_fence_before();
+    warp_arrive(smem_u32(&ms.p_full[pb]));
+    slot0 += 4;
     if (slot0 >= C::NS) slot0 -= C::NS;
+    ++tile;
+    if (sg.left > 0) continue;
+    const ChunkUnit& u = ms.unit[sg.seg % kSegs];
     // every score pass of this tile is done, so the query operand may be replaced
-    if (last && it + 1 < rg.n_it) build_query<NC, kLayout>(w, sm, ms, cur.next, (seg + 1) & 1);
-
-    if (last) {
-      // denominators, O, LSE
-      const float wsum = transpose_reduce<CPT, false>(l_part, lane);
-      if (lane < CPT) ms.red[cq][quarter][lane] = wsum;
-      named_bar_sync(1, kSmxThreads);
-      if (quarter == 0 && lane < CPT) {
-        const float l = (ms.red[cq][0][lane] + ms.red[cq][1][lane]) + (ms.red[cq][2][lane] + ms.red[cq][3][lane]);
-        ms.linv[c0 + lane] = l == 0.f ? 0.f : 1.f / l;
-        ms.lse[c0 + lane] = l == 0.f ? -INFINITY : (m_lane + log2f(l)) * kLn2;
-      }
-      named_bar_sync(1, kSmxThreads);
-      ok &= mbar_wait(smem_u32(&ms.pv_done[it & 1]), (it >> 1) & 1, abort, w.wait_ns);
-      tc_fence_after();
-      const ChunkUnit& u = cur.u;
-      const bool whole = u.tile0 >= rg.t0 && u.tile0 + u.tiles <= rg.t0 + rg.n_it;
-      const int64_t part = ((int64_t)blockIdx.x * 2 + (rg.t0 >= u.tile0 ? 0 : 1)) * NC;
-#pragma unroll 1
-      for (int db = 0; db < 4; ++db) {
-        uint32_t v[CPT];
-        tmem_ld<CPT>(lane_base + C::O_COL0 + db * NC + c0, v);
-        tmem_wait_ld();
-        const int d = db * 128 + row;
+    if (it + 1 < rg.n_it) {
+      ok &= mbar_wait(smem_u32(&ms.meta_full[(it + 1) % kMeta]), ((it + 1) / kMeta) & 1, abort, w.wait_ns);
+      build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[(sg.seg + 1) % kSegs], par ^ 1);
+    }
+    // the segment's end: denominators, O, LSE
+    float lsum[CPT];
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-          if (c0 + k >= u.cols) break;
-          const float li = ms.linv[c0 + k];
-          const float o = li == 0.f ? 0.f : __uint_as_float(v[k]) * li;
-          if (whole) reinterpret_cast<__nv_bfloat16*>(a.o)[(u.row0 + c0 + k) * kD + d] = __float2bfloat16_rn(o);
-          else w.part_o[(part + c0 + k) * kD + d] = o;
-        }
+    for (int k = 0; k < CP2; ++k) unpack2(l_part[k], lsum[2 * k], lsum[2 * k + 1]);
+    const float wsum = transpose_reduce<CPT, false>(lsum, lane);
+    if (lane < CPT) ms.red[cq][quarter][lane] = wsum;
+    named_bar_sync(bar, 128);
+    if (quarter == 0 && lane < CPT) {
+      const float l = (ms.red[cq][0][lane] + ms.red[cq][1][lane]) + (ms.red[cq][2][lane] + ms.red[cq][3][lane]);
+      ms.by[c0 + lane] = l == 0.f ? 0.f : 1.f / l;
+      ms.alpha[c0 + lane] = l == 0.f ? -INFINITY : (m_lane + log2f(l)) * kLn2;
+    }
+    named_bar_sync(bar, 128);
+    ok &= mbar_wait(smem_u32(&ms.pv_done[it & 1]), (it >> 1) & 1, abort, w.wait_ns);
+    tc_fence_after();
+    const bool whole = u.tile0 >= rg.t0 && u.tile0 + u.tiles <= rg.t0 + rg.n_it;
+    const int64_t part = ((int64_t)blockIdx.x * 2 + (rg.t0 >= u.tile0 ? 0 : 1)) * NC;
+    const int cols = u.cols - c0;                        // of this thread's columns
+    const int64_t row0 = u.row0;
+    float li[CPT];
+    ld_row<CPT>(&ms.by[c0], li);
+    // block db's outputs of this thread's columns, normalised
+    auto read_block = [&](int db, float (&y)[CPT]) {
+      uint32_t v[CPT], lo[CPT];
+      tmem_ld<CPT>(lane_base + C::O_COL0 + db * C::NQ, v);
+      tmem_ld<CPT>(lane_base + C::O_COL0 + db * C::NQ + NC, lo);
+      tmem_wait_ld();
+      const float unlift = C::kScaled ? __int_as_float((254 << 23) - __float_as_int(cg[db])) : 1.f;   // 1 / c_g
+#pragma unroll
+      for (int k = 0; k < CPT; ++k)
+        y[k] = li[k] == 0.f ? 0.f : fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(v[k])) * (li[k] * unlift);
+    };
+    if (whole) {
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + (row0 + c0) * kD + row;
+#pragma unroll
+      for (int db = 0; db < 4; ++db) {
+        float y[CPT];
+        read_block(db, y);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k)
+          if (k < cols) o[k * kD + db * 128] = __float2bfloat16_rn(y[k]);
       }
-      if (quarter == 0 && lane < CPT && c0 + lane < u.cols) {
-        if (whole) a.lse[u.row0 + c0 + lane] = ms.lse[c0 + lane];
-        else w.part_lse[part + c0 + lane] = ms.lse[c0 + lane];
+    } else {
+      float* o = w.part_o + (part + c0) * kD + row;
+#pragma unroll
+      for (int db = 0; db < 4; ++db) {
+        float y[CPT];
+        read_block(db, y);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k)
+          if (k < cols) o[k * kD + db * 128] = y[k];
       }
     }
-    cur.advance(w, rg.n_units);
+    if (quarter == 0 && lane < CPT && lane < cols) {
+      if (whole) a.lse[row0 + c0 + lane] = ms.alpha[c0 + lane];
+      else w.part_lse[part + c0 + lane] = ms.alpha[c0 + lane];
+    }
   }
   (void)ok;
 }
@@ -786,26 +1081,31 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <int NC, int kLayout>
-__global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkWork w) {
-  using C = Cfg<NC, kLayout>;
+template <int NC, int kLayout, bool kTma>
+__global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
+    chunk_attn_kernel(const __grid_constant__ ChunkWork w, const __grid_constant__ ChunkMaps maps) {
+  using C = Cfg<NC, kLayout, kTma>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc& ms = *reinterpret_cast<Misc*>(sm + C::MISC_OFF);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(smem_u32(&ms.full[s]), kProdThreads);
+      mbar_init(smem_u32(&ms.full[s]), kTma ? 1 : kProdThreads);
       mbar_init(smem_u32(&ms.empty[s]), 1);
     }
-    for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), 1 + (C::kScaled ? kProdThreads : 0));
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), 1 + (C::kScaled && !kTma ? kProdThreads : 0));
+    for (int s = 0; s < C::SBUF; ++s) {
       mbar_init(smem_u32(&ms.s_full[s]), 1);
       mbar_init(smem_u32(&ms.s_free[s]), kSmxWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ms.p_full[s]), kSmxWarps);
       mbar_init(smem_u32(&ms.p_free[s]), 1);
       mbar_init(smem_u32(&ms.final[s]), 1);
     }
+    mbar_init(smem_u32(&ms.rope_full), kTma ? 1 : kProdThreads);
+    mbar_init(smem_u32(&ms.rope_empty), 1);
     mbar_init(smem_u32(&ms.q_full), kSmxWarps);
     mbar_init(smem_u32(&ms.pv_done[0]), 1);
     mbar_init(smem_u32(&ms.pv_done[1]), 1);
@@ -824,25 +1124,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   grid_dependency_wait();
   grid_launch_dependents();   // the merge: its blocks wait for the whole grid
   Range rg;
-  const int64_t n_tiles = __ldcg(&w.hdr->n_tiles);
-  rg.n_units = __ldcg(&w.hdr->n_units);
-  const int grid = (int)(n_tiles < w.grid ? n_tiles : w.grid);
-  rg.t0 = 0;
-  rg.n_it = rg.unit = 0;
-  if ((int)blockIdx.x < grid) {
-    rg.t0 = chunk_tile_begin(blockIdx.x, n_tiles, grid);
-    rg.n_it = (int)(chunk_tile_begin(blockIdx.x + 1, n_tiles, grid) - rg.t0);
-    rg.unit = __ldcg(w.cta_unit + blockIdx.x);
-  }
+  rg.t0 = __ldcg(&w.starts[blockIdx.x].t0);
+  rg.n_it = (int)(__ldcg(&w.starts[blockIdx.x + 1].t0) - rg.t0);
   if (rg.n_it > 0) {          // the same for the whole CTA
     if (warp < kSmxWarps) {
-      regs_inc<kSmxRegs>();
-      softmax_role<NC, kLayout>(w, sm, ms, tmem, rg);
+      regs_inc<C::SMX_REGS>();
+      softmax_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
     } else {
-      regs_dec<kOtherRegs>();
-      if (warp == kQkWarp) qk_role<NC, kLayout>(w, sm, ms, tmem, rg);
-      else if (warp == kPvWarp) pv_role<NC, kLayout>(w, sm, ms, tmem, rg);
-      else producer_role<NC, kLayout>(w, sm, ms, rg);
+      regs_dec<C::OTHER_REGS>();
+      if (warp == kQkWarp) qk_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
+      else if (warp == kPvWarp) pv_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
+      else if constexpr (!kTma) producer_role<NC, kLayout, kTma>(w, sm, ms, rg);
+      else if (warp == kProdWarp0) tma_role<NC, kLayout, kTma>(w, maps, sm, ms, rg);
     }
   }
   tc_fence_before();
@@ -854,27 +1147,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   if (tid == 0 && ms.abort) set_err(w.a.err, DSA_DEV_ERR_TIMEOUT);
 }
 
-template <int NC, int kLayout>
-bool launch(const ChunkWork& w, cudaStream_t stream) {
-  using C = Cfg<NC, kLayout>;
+template <int NC, int kLayout, bool kTma>
+bool launch(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
+  using C = Cfg<NC, kLayout, kTma>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   cudaGetDevice(&dev);
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    if (cudaFuncSetAttribute(chunk_attn_kernel<NC, kLayout>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+    if (cudaFuncSetAttribute(chunk_attn_kernel<NC, kLayout, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
       return false;
-    // the register re-split adds up only from exactly kLaunchRegs registers a thread
+    // the register re-split adds up only from exactly LAUNCH_REGS registers a thread
     cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, chunk_attn_kernel<NC, kLayout>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+    if (cudaFuncGetAttributes(&fa, chunk_attn_kernel<NC, kLayout, kTma>) != cudaSuccess || fa.numRegs != C::LAUNCH_REGS)
       return false;
     configured.fetch_or(bit);
   }
   launch_chunk_plan(w, stream);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(w.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -882,28 +1175,70 @@ bool launch(const ChunkWork& w, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, chunk_attn_kernel<NC, kLayout>, w) != cudaSuccess) return false;
-  return launch_chunk_merge(w, stream);
+  if (cudaLaunchKernelEx(&cfg, chunk_attn_kernel<NC, kLayout, kTma>, w, maps) != cudaSuccess) return false;
+  // units of one tile are not spread over CTAs
+  return (int64_t)w.a.max_pages * w.a.page_size <= kTile || launch_chunk_merge(w, stream);
+}
+
+// The driver's tensor map encoder (the library does not link the driver).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// The pool as a matrix of bytes: boxes of `rows` rows and `width` bytes.
+bool encode_rows(CUtensorMap* map, const ChunkArgs& a, int row_bytes, int width, int rows, bool swizzle) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)a.pool_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)rows};
+  const cuuint32_t steps[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.pool), dims, strides, box, steps,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NC, int kLayout>
+bool launch_layout(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
+  return w.box_shift > 0 ? launch<NC, kLayout, true>(w, maps, stream) : launch<NC, kLayout, false>(w, maps, stream);
 }
 
 template <int NC>
-bool launch_nc(const ChunkWork& w, cudaStream_t stream) {
-  if (w.a.layout == DSA_KV_RAW512) return launch<NC, DSA_KV_RAW512>(w, stream);
-  if (w.a.layout == DSA_KV_SCALED528) return launch<NC, DSA_KV_SCALED528>(w, stream);
-  return launch<NC, DSA_KV_ROPE656>(w, stream);
+bool launch_nc(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
+  if (w.a.layout == DSA_KV_RAW512) return launch_layout<NC, DSA_KV_RAW512>(w, maps, stream);
+  if (w.a.layout == DSA_KV_SCALED528) return launch_layout<NC, DSA_KV_SCALED528>(w, maps, stream);
+  return launch_layout<NC, DSA_KV_ROPE656>(w, maps, stream);
 }
 
 }  // namespace
 
 int chunk_columns(int T, int H, int B) {
   const int64_t rows = ((int64_t)T * H + B - 1) / B;     // of an average request
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : 32;
 }
 
-bool launch_chunk_attn(const ChunkWork& w, cudaStream_t stream) {
-  if (w.nc == 16) return launch_nc<16>(w, stream);
-  if (w.nc == 32) return launch_nc<32>(w, stream);
-  return launch_nc<64>(w, stream);
+bool launch_chunk_attn(const ChunkWork& work, cudaStream_t stream) {
+  ChunkWork w = work;
+  // the largest power of two that divides the page and the tile: a box
+  const int page = w.a.page_size;
+  int shift = 0;
+  while (shift < 7 && page % (2 << shift) == 0) ++shift;
+  w.box_shift = shift >= 4 ? shift : 0;
+  ChunkMaps maps{};
+  if (w.box_shift > 0) {
+    const int row_bytes = w.a.layout == DSA_KV_RAW512 ? kRawRow : w.a.layout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
+    if (!encode_rows(&maps.rows, w.a, row_bytes, 128, 1 << w.box_shift, true)) return false;
+    if (w.a.layout != DSA_KV_RAW512 && !encode_rows(&maps.scales, w.a, row_bytes, 16, 1 << w.box_shift, false)) return false;
+  }
+  return w.nc == 16 ? launch_nc<16>(w, maps, stream) : launch_nc<32>(w, maps, stream);
 }
 
 }  // namespace dsa

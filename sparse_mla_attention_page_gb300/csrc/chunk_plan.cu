@@ -2,16 +2,18 @@
 // units that the persistent grid spread over CTAs.
 //
 // Plan: one block.  Two prefix sums (units of each request, tiles of each
-// unit), then every unit's entry is written, and with it the unit that each
-// CTA's range starts in and the list of split units.  A few hundred to a few
+// unit), then every unit's entry is written, and with it where each CTA's
+// range starts and the list of split units.  A few hundred to a few
 // thousand units: bound by its launch and three dependent passes, which the
 // attention kernel's set-up overlaps (programmatic dependent launch).
 //
 // Merge: a split unit's parts are normalised (O_c, LSE_c) of its query rows
 // over disjoint keys: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
-// One block at a time per (split unit, query row): first the weights of all
-// parts (one part per thread), then eight part lanes of 32 threads with 16
-// dims each, so that a long context's 150 parts cost a few rounds of loads.
+// Units of few parts (nearly all): a thread for each 8 dims of a row folds the
+// parts four at a time.  Units of many parts (a long context over most SMs): a
+// block for each quarter of a row's dims, first the weights of all parts (one
+// a thread), then 16 part lanes of 16 threads with four parts' loads in flight,
+// so that 150 parts cost three round trips and not forty.
 #include <cuda_bf16.h>
 
 #include "chunk.cuh"
@@ -23,8 +25,13 @@ namespace {
 
 constexpr int kPlanThreads = kScanThreads;
 constexpr int kMergeThreads = 256;
-constexpr int kPartLanes = 8;
-constexpr int kDimThreads = kMergeThreads / kPartLanes;   // 32 threads x 4 float4 = 512 dims
+constexpr int kBatch = 4;                                 // parts whose loads are issued together
+constexpr int kFewThreads = kD / 8;                       // few parts: threads of a row, 8 dims each
+constexpr int kFewRows = kMergeThreads / kFewThreads;
+constexpr int kVec = 2;                                   // many parts: float4 of a thread
+constexpr int kDimThreads = 16;                           // threads of a quarter of a row's dims
+constexpr int kLanes = kMergeThreads / kDimThreads;       // part lanes
+constexpr int kQuarter = kD / 4 / 4;                      // float4 of a quarter
 constexpr int kMaxParts = 1024;                           // CTAs of the attention grid (one per SM)
 
 struct Request {
@@ -64,29 +71,32 @@ __device__ __forceinline__ ChunkUnit unit_of(const ChunkArgs& a, const Request& 
   u.b = b;
   u.cols = (int)(rows - r0 < nc ? rows - r0 : nc);
   u.r0 = (int)r0;
-  u.vis0 = a.causal ? (int)max((int64_t)INT32_MIN / 2, (int64_t)r.kv - r.n + 1) : r.kv;
+  u.vis0 = a.causal ? r.kv - r.n + 1 : r.kv;
   u.kv = r.kv;
-  const int vis = chunk_visible(a, u, u.cols - 1);
-  u.tiles = vis <= kChunkTile ? 1 : (vis + kChunkTile - 1) / kChunkTile;
-  u.pad[0] = u.pad[1] = 0;
+  u.last = chunk_visible(a, u, u.cols - 1);
+  u.tiles = u.last <= kChunkTile ? 1 : (u.last + kChunkTile - 1) / kChunkTile;
+  u.pad = 0;
   return u;
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __grid_constant__ ChunkWork w) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int32_t first_unit[];    // [B]
-  __shared__ int n_splits;
+  __shared__ int n_many, cta_unit[kMaxParts];
   const ChunkArgs& a = w.a;
   const int tid = threadIdx.x;
-  if (tid == 0) n_splits = 0;
+  if (tid == 0) n_many = 0;
+  for (int c = tid; c < w.grid; c += kPlanThreads) w.few[c].parts = 0;
   int err = 0;
   const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   int64_t mine = 0;
+  int last_units = 0;
   for (int b = b0; b < b1; ++b) {
     const Request r = request_of(a, b);
     err |= r.err;
-    mine += units_of(a, r, w.nc);
+    last_units = units_of(a, r, w.nc);
+    mine += last_units;
   }
   int64_t total;
   int64_t at = block_scan(mine, &total);
@@ -98,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __gri
   const int n_units = (int)total;
   for (int b = b0; b < b1; ++b) {
     first_unit[b] = (int)min(at, (int64_t)INT32_MAX);
-    at += units_of(a, request_of(a, b), w.nc);
+    at += b + 1 == b1 ? last_units : units_of(a, request_of(a, b), w.nc);
   }
   __syncthreads();
 
@@ -107,7 +117,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __gri
   const int u0 = (int)min((int64_t)tid * uper, (int64_t)n_units), u1 = min(u0 + uper, n_units);
   const int first_b = u0 < u1 ? scan_owner(first_unit, a.B, u0) : 0;
   int64_t tiles = 0;
+  ChunkUnit only{};              // of a thread that has one unit (up to 1024 units): worked out once
   auto walk = [&](auto&& visit) {
+    if (u1 - u0 == 1 && tiles > 0) return visit(u0, only);
     int b = first_b;
     Request r{};
     bool have = false;
@@ -121,109 +133,191 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __gri
       visit(u, unit_of(a, r, b, u - first_unit[b], w.nc));
     }
   };
-  walk([&](int, const ChunkUnit& e) { tiles += e.tiles; });
+  walk([&](int, const ChunkUnit& e) {
+    tiles += e.tiles;
+    only = e;
+  });
   int64_t n_tiles;
   int64_t tile0 = block_scan(tiles, &n_tiles);
+  // cost: position v of the list, of length V, is tile v - v0 - kUnitCost of the
+  // unit that begins at v0, or its first; CTA c begins at floor(c V / grid)
+  const int64_t V = n_tiles + (int64_t)n_units * kUnitCost;
   const int grid = (int)(n_tiles < w.grid ? n_tiles : w.grid);
+  int64_t v0 = tile0 + (int64_t)u0 * kUnitCost;
   walk([&](int u, ChunkUnit e) {
     e.tile0 = tile0;
     w.units[u] = e;
-    // CTAs whose range starts in this unit: tile_begin(c) >= x for c >= ceil(x grid / n)
-    const int64_t end = tile0 + e.tiles;
-    const int c_lo = (int)((tile0 * grid + n_tiles - 1) / n_tiles);
-    const int c_hi = (int)((end * grid + n_tiles - 1) / n_tiles);
-    for (int c = c_lo; c < c_hi && c < grid; ++c) w.cta_unit[c] = u;
-    const int c_in = chunk_tile_begin(c_lo, n_tiles, grid) > tile0 ? c_lo : c_lo + 1;   // first that starts inside
-    if (c_in < c_hi && c_in < grid) {
-      const int c0 = c_in - 1, c1 = (c_hi < grid ? c_hi : grid) - 1;
-      w.splits[atomicAdd(&n_splits, 1)] =
-          ChunkSplit{u, c0, c1, 2 * c0 + (chunk_tile_begin(c0, n_tiles, grid) < tile0 ? 1 : 0)};
+    const int64_t body = v0 + kUnitCost, end = body + e.tiles;
+    // floor(c V / grid) >= x for c >= ceil(x grid / V)
+    const int c_lo = (int)((v0 * grid + V - 1) / V);
+    const int c_hi = min((int)((end * grid + V - 1) / V), grid);
+    for (int c = c_lo; c < c_hi; ++c) cta_unit[c] = u;
+    const int c_in = (int)(((body + 1) * grid + V - 1) / V);       // the first CTA that begins inside the unit's tiles
+    if (c_in < c_hi) {
+      const int c0 = c_in - 1, parts = c_hi - c0;
+      ChunkSplit sp;
+      sp.row0 = e.row0;
+      sp.cols = e.cols;
+      sp.parts = parts;
+      // slot 0 of a CTA holds the unit its range starts in, slot 1 its last one
+      sp.slot0 = 2 * c0 + (c0 < c_lo ? 1 : 0);
+      sp.next = 2 * (c0 + 1);
+      sp.pad[0] = sp.pad[1] = 0;
+      if (parts > kFewParts) w.many[atomicAdd(&n_many, 1)] = sp;
+      else w.few[c0] = sp;
     }
-    tile0 = end;
+    tile0 += e.tiles;
+    v0 = end;
   });
   __syncthreads();
-  if (tid == 0) *w.hdr = ChunkHeader{n_tiles, n_units, n_splits};
+  for (int c = tid; c <= w.grid; c += kPlanThreads) {
+    ChunkStart st{};
+    st.t0 = n_tiles;
+    if (c < grid) {
+      const int u = cta_unit[c];
+      st.unit = u;
+      st.u = w.units[u];
+      const int64_t in = (int64_t)c * V / grid - (st.u.tile0 + (int64_t)(u + 1) * kUnitCost);
+      st.t0 = st.u.tile0 + (in > 0 ? in : 0);
+    }
+    w.starts[c] = st;
+  }
+  if (tid == 0) *w.n_many = n_many;
 }
 
-__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkWork w) {
+__device__ __forceinline__ void fold(float4& acc, float w, const float4& v) {
+  acc.x = fmaf(w, v.x, acc.x);
+  acc.y = fmaf(w, v.y, acc.y);
+  acc.z = fmaf(w, v.z, acc.z);
+  acc.w = fmaf(w, v.w, acc.w);
+}
+
+__device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, int d4, const float4& o, float inv) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  uint2 packed;
+  packed.x = *reinterpret_cast<const uint32_t*>(&lo);
+  packed.y = *reinterpret_cast<const uint32_t*>(&hi);
+  reinterpret_cast<uint2*>(a.o + row * kD)[d4] = packed;
+}
+
+__device__ __forceinline__ ChunkSplit split_of(const ChunkSplit* s) {
+  union {
+    ChunkSplit s;
+    int4 v[2];
+  } x;
+  x.v[0] = __ldcg(reinterpret_cast<const int4*>(s));
+  x.v[1] = __ldcg(reinterpret_cast<const int4*>(s) + 1);
+  return x.s;
+}
+
+// One quarter of one row of a unit of many parts, by the whole block.
+__device__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, int dq) {
   __shared__ float wt[kMaxParts];
   __shared__ float red[kMergeThreads / 32], red2[kMergeThreads / 32];
-  __shared__ float4 acc_s[kPartLanes][kD / 4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");               // every part is written
+  __shared__ float4 acc_s[kLanes][kQuarter];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n_items = __ldcg(&w.hdr->n_splits) * w.nc;
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const int4 s4 = __ldcg(reinterpret_cast<const int4*>(w.splits) + item / w.nc);
-    const int c0 = s4.y, n_parts = s4.z - s4.y + 1, slot0 = s4.w;
-    const int col = item % w.nc;
-    const ChunkUnit& u = w.units[s4.x];
-    if (col >= __ldcg(&u.cols)) continue;
-    const int64_t row = __ldcg(&u.row0) + col;
-    auto slot = [&](int p) { return (int64_t)(p == 0 ? slot0 : 2 * (c0 + p)) * w.nc + col; };
-    // weights exp(LSE_c - max) and their sum
-    float m = -INFINITY;
-    bool nan = false;
-    for (int p = tid; p < n_parts; p += kMergeThreads) {
-      const float v = __ldcg(w.part_lse + slot(p));
-      wt[p] = v;
-      m = fmaxf(m, v);
-      nan |= v != v;
+  auto slot = [&](int p) { return (int64_t)(p == 0 ? sp.slot0 : sp.next + 2 * (p - 1)) * w.nc + col; };
+  float m = -INFINITY;
+  bool nan = false;
+  for (int p = tid; p < sp.parts; p += kMergeThreads) {
+    const float v = __ldcg(w.part_lse + slot(p));
+    wt[p] = v;
+    m = fmaxf(m, v);
+    nan |= v != v;
+  }
+  m = warp_max(m);
+  if (lane == 0) red[warp] = m;
+  nan = __syncthreads_or(nan) != 0;
+#pragma unroll
+  for (int i = 0; i < kMergeThreads / 32; ++i) m = fmaxf(m, red[i]);
+  float sum = 0.f;
+  for (int p = tid; p < sp.parts; p += kMergeThreads) {
+    wt[p] = nan ? __int_as_float(0x7FC00000) : m == -INFINITY ? 0.f : expf(wt[p] - m);
+    sum += wt[p];
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) red2[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeThreads / 32; ++i) sum += red2[i];
+  const int pl = tid / kDimThreads, dt = tid % kDimThreads;
+  float4 acc[kVec] = {};
+  for (int p0 = pl; p0 < sp.parts; p0 += kLanes * kBatch) {
+    float4 v[kBatch][kVec];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int p = p0 + q * kLanes;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        v[q][i] = p < sp.parts ? __ldcg(reinterpret_cast<const float4*>(w.part_o + slot(p) * kD) + dq * kQuarter + dt + i * kDimThreads)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    m = warp_max(m);
-    if (lane == 0) red[warp] = m;
-    nan = __syncthreads_or(nan) != 0;
 #pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) m = fmaxf(m, red[i]);
-    float sum = 0.f;
-    for (int p = tid; p < n_parts; p += kMergeThreads) {
-      const float e = nan ? wt[p] : m == -INFINITY ? 0.f : expf(wt[p] - m);
-      wt[p] = nan ? __int_as_float(0x7FC00000) : e;
-      sum += wt[p];
+    for (int q = 0; q < kBatch; ++q) {
+      const int p = p0 + q * kLanes;
+      if (p >= sp.parts) break;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) fold(acc[i], wt[p], v[q][i]);
     }
-    sum = warp_sum(sum);
-    if (lane == 0) red2[warp] = sum;
-    __syncthreads();
-    sum = 0.f;
+  }
 #pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) sum += red2[i];
-    const int pl = tid / kDimThreads, dt = tid % kDimThreads;
-    float4 acc[4] = {};
-    for (int p = pl; p < n_parts; p += kPartLanes) {
-      const float e = wt[p];
-      if (e == 0.f) continue;                                      // a part without a visible key
-      const float4* src = reinterpret_cast<const float4*>(w.part_o + slot(p) * kD) + dt;
+  for (int i = 0; i < kVec; ++i) acc_s[pl][dt + i * kDimThreads] = acc[i];
+  __syncthreads();
+  if (tid < kQuarter) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kLanes; ++i) fold(o, 1.f, acc_s[i][tid]);
+    store_row(w.a, sp.row0 + col, dq * kQuarter + tid, o, sum == 0.f ? 0.f : 1.f / sum);
+    if (tid == 0 && dq == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
+  }
+  __syncthreads();   // acc_s, wt and the sums are free for the next row
+}
+
+__global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __grid_constant__ ChunkWork w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");               // every part is written
+  const int n_many = __ldcg(w.n_many);
+  const ChunkSplit sp = split_of(w.few + blockIdx.x);              // blockIdx.y: four rows of the unit
+  const int col = blockIdx.y * kFewRows + threadIdx.x / kFewThreads, d8 = threadIdx.x % kFewThreads;
+  if (sp.parts > 0 && col < sp.cols) {
+    float m = -INFINITY, sum = 0.f;
+    float4 acc[2] = {};
+    for (int p0 = 0; p0 < sp.parts; p0 += kBatch) {
+      float ls[kBatch];
+      float4 v[kBatch][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldcg(src + i * kDimThreads);
-        acc[i].x = fmaf(e, v.x, acc[i].x);
-        acc[i].y = fmaf(e, v.y, acc[i].y);
-        acc[i].z = fmaf(e, v.z, acc[i].z);
-        acc[i].w = fmaf(e, v.w, acc[i].w);
+      for (int q = 0; q < kBatch; ++q) {
+        const int p = p0 + q;
+        const int64_t at = (int64_t)(p == 0 ? sp.slot0 : sp.next + 2 * (p - 1)) * w.nc + col;
+        const float4* src = reinterpret_cast<const float4*>(w.part_o + at * kD) + 2 * d8;
+        ls[q] = p < sp.parts ? __ldcg(w.part_lse + at) : -INFINITY;
+        v[q][0] = p < sp.parts ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[q][1] = p < sp.parts ? __ldcg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        if (ls[q] == -INFINITY) continue;                          // a part without a visible key
+        const float mn = fmaxf(m, ls[q]);
+        const float r = m == -INFINITY ? 0.f : expf(m - mn), e = expf(ls[q] - mn);
+        sum = fmaf(sum, r, e);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc[i] = make_float4(acc[i].x * r, acc[i].y * r, acc[i].z * r, acc[i].w * r);
+          fold(acc[i], e, v[q][i]);
+        }
+        m = mn;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc_s[pl][dt + i * kDimThreads] = acc[i];
-    __syncthreads();
-    if (tid < kD / 4) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kPartLanes; ++i) {
-        const float4 v = acc_s[i][tid];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      uint2 packed;
-      packed.x = *reinterpret_cast<const uint32_t*>(&lo);
-      packed.y = *reinterpret_cast<const uint32_t*>(&hi);
-      reinterpret_cast<uint2*>(w.a.o + row * kD)[tid] = packed;
-      if (tid == 0) w.a.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
-    }
-    __syncthreads();   // acc_s, wt and the sums are free for the next row
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    store_row(w.a, sp.row0 + col, 2 * d8, acc[0], inv);
+    store_row(w.a, sp.row0 + col, 2 * d8 + 1, acc[1], inv);
+    if (d8 == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
+  }
+  const int blocks = gridDim.x * gridDim.y;
+  for (int item = blockIdx.y * gridDim.x + blockIdx.x; item < n_many * w.nc * 4; item += blocks) {
+    const ChunkSplit big = split_of(w.many + item / 4 / w.nc);
+    const int c = item / 4 % w.nc;
+    if (c < big.cols) merge_many(w, big, c, item % 4);
   }
 }
 
@@ -239,7 +333,7 @@ void launch_chunk_plan(const ChunkWork& w, cudaStream_t stream) {
 bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
   if (w.grid > kMaxParts) return false;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(w.grid * 8);
+  cfg.gridDim = dim3(w.grid, w.nc / kFewRows);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

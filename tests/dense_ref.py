@@ -125,11 +125,12 @@ def chunk_attn(q, pool, layout, table, page, cu, kv_lens, sm_scale, causal=True)
     products (2^-17 of sum_d |q_d k_jd|, and once again for the queries' two E4M3 terms), which enter O through
     the weights and LSE directly.
 
-    E4M3's smallest step over rows with scales.  The operand of group g is P = 2^(s_j - M) s_jg, rounded by at most 2^-10
-    (half of 2^-9) where the step binds, and multiplies the row's byte b_jd.  M is at most max_j (s_j + log2 S_j) - 4 with
-    S_j the row's largest scale, so for the row J of that maximum 2^(s_J - M) S_J >= 2^4, and l = sum_j 2^(s_j - M) =
-    2^(s_J - M) / w_J >= 2^4 / (S_J w_J).  O is off by at most sum_j 2^-10 |b_jd| / l <= 2^-14 max_j (w_j S_j) sum_j |b_jd|.
-    (Raw rows: S = 1, b = v, max w = 1 / (l / e^max s).)"""
+    E4M3's smallest step.  With S_j the power of two above row j's largest scale (1 for raw rows), the operand of group g is
+    P = 2^(s_j + log2 S_j - M) (s_jg / S_j) c_g, c_g >= 1.  Its two terms leave at most half of lo's smallest step: 2^-10
+    where M is at most max_j (s_j + log2 S_j) - 4, or 2^-14 where lo is kept 16 times larger and M is at most that
+    maximum.  P multiplies the row's byte b_jd, and l = sum_j 2^(s_j - M) = 2^(s_J - M) / w_J for the row J of the maximum,
+    so O is off by at most (2^-14 / l) sum_j |b_jd| <= 2^-14 max_j (w_j S_j) sum_j |b_jd|, and S_j <= 2 x the largest scale:
+    2^-13 max_j (w_j max_g s_jg) sum_j |b_jd|."""
     T, H, _ = q.shape
     q = q.double()
     o = torch.full((T, H, 512), math.nan, dtype=torch.float64)
@@ -173,7 +174,7 @@ def chunk_attn(q, pool, layout, table, page, cu, kv_lens, sm_scale, causal=True)
             o[t0 + i], lse[t0 + i] = w @ vv, z
             mag = (qi.abs() @ kk.abs().T * abs(sm_scale)).amax(-1) * 2.0 ** -16 + 2.0 ** -18
             absv = w @ vv.abs()
-            step = 2.0 ** -14 * (w * big[see]).amax(-1)[:, None] * codes[see].sum(0)
+            step = 2.0 ** -13 * (w * big[see]).amax(-1)[:, None] * codes[see].sum(0)
             otol[t0 + i] = (2.0 ** -8 * o[t0 + i].abs() + (2.0 ** -8 + 2.0 ** -12 + 2 * mag[:, None]) * absv
                             + step)
             ltol[t0 + i] = mag + z.abs() * 2.0 ** -22
