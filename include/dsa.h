@@ -353,9 +353,10 @@ int dsa_pages_extend(const int32_t* seq_lens_dev, const int32_t* new_lens_dev, i
  * (its rows are stale for a request of length 0).  A page belongs to one
  * request: pages that requests share are not counted.  All or nothing: a
  * length outside [0, max_pages * page_size] or free_count outside
- * [0, free_cap] (DSA_DEV_ERR_LENGTH), a page id below 0
- * (DSA_DEV_ERR_PAGE_RANGE) or a stack without room (DSA_DEV_ERR_NO_PAGES)
- * leaves free_pages as it was and copies free_count and seq_lens.
+ * [0, free_cap] (DSA_DEV_ERR_LENGTH) or a stack without room
+ * (DSA_DEV_ERR_NO_PAGES) leaves free_pages as it was and copies free_count and
+ * seq_lens.  A page id below 0 sets DSA_DEV_ERR_PAGE_RANGE and is pushed as it
+ * is (dsa_pages_extend reports it again).
  *   finished_dev   [B] bytes, non-zero = finished.
  *   free_pages_dev [free_cap] int32, written above free_count.
  *   free_count_out_dev may be free_count_dev, seq_lens_out_dev seq_lens_dev. */

@@ -337,30 +337,54 @@ def dsa_sparse_attn_decode_noalloc(q_bf16, pool, layout, topk, sm_scale, o, lse,
 
 # ------------------------------------------------ dense serving operators
 
-def _arg(t, name: str, dtype: torch.dtype, shape=None, device=None, optional=False, strided=False):
-    """Address of a CUDA tensor of the given type and shape (None entries: any size),
-    on the current device; contiguous unless ``strided`` (then its last dim is)."""
-    if t is None and optional:
-        return None
+def _refuse(t, name, dtype, shape, device, strided):
+    """Raises what is wrong with an argument that _arg turned down."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if device is not None and t.get_device() != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's device is cuda:{device}")
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if strided:
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must be contiguous in its last dim")
-    elif not t.is_contiguous():
-        raise TypeError(f"{name} must be contiguous")
-    return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous in its last dim")
+    raise TypeError(f"{name} must be contiguous")
+
+
+def _arg(t, name: str, dtype: torch.dtype, shape, device: int):
+    """Address of a contiguous tensor of the given type and shape (None: any) on the call's device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device, False)
+
+
+def _arg_strided(t, name: str, dtype: torch.dtype, shape, device: int):
+    """The same for a tensor that is contiguous in its last dim only; None stays None."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and (t.stride(-1) == 1 or t.shape[-1] == 1)):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device, True)
+
+
+def _flag(t, device: int):
+    return None if t is None else _arg(t, "err_flag", torch.int32, None, device)
+
+
+def _dims(t, name: str, n: int):
+    """The shape of a tensor of n dims."""
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dims")
+    return t.shape
 
 
 def _call_device(stream):
     """(the current device, the stream's address on it)."""
+    dev = torch.cuda.current_device()
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return torch.cuda.current_device(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def dsa_pages_extend(seq_lens, new_lens, page_table, page_size, free_pages, free_count, free_count_out, slots,
@@ -371,15 +395,16 @@ def dsa_pages_extend(seq_lens, new_lens, page_table, page_size, free_pages, free
     free_count, kv_lens may be seq_lens."""
     dev, s = _call_device(stream)
     i32 = torch.int32
-    B, T = seq_lens.shape[0], slots.shape[0]
-    p = [_arg(seq_lens, "seq_lens", i32, (None,), dev), _arg(new_lens, "new_lens", i32, (B,), dev), B,
-         _arg(page_table, "page_table", i32, (B, None), dev), page_table.shape[1], page_size,
-         _arg(free_pages, "free_pages", i32, (None,), dev), free_pages.shape[0],
-         _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev), T,
-         _arg(slots, "slots", torch.int64, (T,), dev), _arg(positions, "positions", i32, (T,), dev),
-         _arg(token_seq, "token_seq", i32, (T,), dev), _arg(cu_q, "cu_q", i32, (B + 1,), dev),
-         _arg(kv_lens, "kv_lens", i32, (B,), dev), _arg(err_flag, "err_flag", i32, None, dev, True)]
-    _check(lib().dsa_pages_extend(*p, s), "dsa_pages_extend")
+    B, W = _dims(page_table, "page_table", 2)
+    T, = _dims(slots, "slots", 1)
+    cap, = _dims(free_pages, "free_pages", 1)
+    _check((_lib or lib()).dsa_pages_extend(
+        _arg(seq_lens, "seq_lens", i32, (B,), dev), _arg(new_lens, "new_lens", i32, (B,), dev), B,
+        _arg(page_table, "page_table", i32, None, dev), W, page_size, _arg(free_pages, "free_pages", i32, None, dev), cap,
+        _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev), T,
+        _arg(slots, "slots", torch.int64, None, dev), _arg(positions, "positions", i32, (T,), dev),
+        _arg(token_seq, "token_seq", i32, (T,), dev), _arg(cu_q, "cu_q", i32, (B + 1,), dev),
+        _arg(kv_lens, "kv_lens", i32, (B,), dev), _flag(err_flag, dev), s), "dsa_pages_extend")
 
 
 def dsa_pages_release(finished, seq_lens, page_table, page_size, free_pages, free_count, free_count_out, seq_lens_out,
@@ -388,13 +413,13 @@ def dsa_pages_release(finished, seq_lens, page_table, page_size, free_pages, fre
     include/dsa.h).  free_count_out may be free_count, seq_lens_out may be seq_lens."""
     dev, s = _call_device(stream)
     i32 = torch.int32
-    B = seq_lens.shape[0]
-    p = [_arg(finished, "finished", torch.bool, (B,), dev), _arg(seq_lens, "seq_lens", i32, (None,), dev), B,
-         _arg(page_table, "page_table", i32, (B, None), dev), page_table.shape[1], page_size,
-         _arg(free_pages, "free_pages", i32, (None,), dev), free_pages.shape[0],
-         _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev),
-         _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev), _arg(err_flag, "err_flag", i32, None, dev, True)]
-    _check(lib().dsa_pages_release(*p, s), "dsa_pages_release")
+    B, W = _dims(page_table, "page_table", 2)
+    cap, = _dims(free_pages, "free_pages", 1)
+    _check((_lib or lib()).dsa_pages_release(
+        _arg(finished, "finished", torch.bool, (B,), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev), B,
+        _arg(page_table, "page_table", i32, None, dev), W, page_size, _arg(free_pages, "free_pages", i32, None, dev), cap,
+        _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev),
+        _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev), _flag(err_flag, dev), s), "dsa_pages_release")
 
 
 def rope_spec(theta=10000.0, sections=(32,), interleaved=False, inv_freq=None, axis=None, mscale=1.0) -> DsaRope:
@@ -418,23 +443,20 @@ def dsa_rope_qkv656(q_nope, q_pe, q_out, kv_c, k_pe, slots, pool, positions, rop
     side out."""
     dev, s = _call_device(stream)
     bf = torch.bfloat16
-    side = kv_c if q_pe is None else q_pe
-    if side is None:
-        raise ValueError("neither queries nor rows given")
-    T, H = side.shape[0], 1 if q_pe is None else q_pe.shape[1]
-    pos = _arg(positions, "positions", torch.int32, (rope.n_axes, T), dev, strided=True)
-    qn = _arg(q_nope, "q_nope", bf, (T, H, 512), dev, True, True)
-    qp = _arg(q_pe, "q_pe", bf, (T, H, 64), dev, True, True)
-    qo = _arg(q_out, "q_out", bf, (T, H, 576), dev, True)
-    kc = _arg(kv_c, "kv_c", bf, (T, 512), dev, True, True)
-    kp = _arg(k_pe, "k_pe", bf, (T, 64), dev, True, True)
-    sl = _arg(slots, "slots", torch.int64, (T,), dev, True)
-    po = _arg(pool, "pool", torch.uint8, (None, 656), dev, True)
+    if q_pe is not None:
+        T, H, _ = _dims(q_pe, "q_pe", 3)
+    else:
+        (T, _), H = _dims(kv_c, "kv_c", 2), 1
     st = (lambda t, d: 0 if t is None or t.shape[d] == 1 else t.stride(d))
-    _check(lib().dsa_rope_qkv656(ctypes.byref(rope), pos, st(positions, 0), T, H, qn, st(q_nope, 0),
-                                 st(q_nope, 1), qp, st(q_pe, 0), st(q_pe, 1), qo, kc, st(kv_c, 0), kp, st(k_pe, 0),
-                                 sl, po, 0 if pool is None else pool.shape[0],
-                                 _arg(err_flag, "err_flag", torch.int32, None, dev, True), s), "dsa_rope_qkv656")
+    _check((_lib or lib()).dsa_rope_qkv656(
+        ctypes.byref(rope), _arg_strided(positions, "positions", torch.int32, (rope.n_axes, T), dev), st(positions, 0), T, H,
+        _arg_strided(q_nope, "q_nope", bf, (T, H, 512), dev), st(q_nope, 0), st(q_nope, 1),
+        _arg_strided(q_pe, "q_pe", bf, (T, H, 64), dev), st(q_pe, 0), st(q_pe, 1),
+        None if q_out is None else _arg(q_out, "q_out", bf, (T, H, 576), dev),
+        _arg_strided(kv_c, "kv_c", bf, (T, 512), dev), st(kv_c, 0), _arg_strided(k_pe, "k_pe", bf, (T, 64), dev), st(k_pe, 0),
+        None if slots is None else _arg(slots, "slots", torch.int64, (T,), dev),
+        None if pool is None else _arg(pool, "pool", torch.uint8, (_dims(pool, "pool", 2)[0], 656), dev),
+        0 if pool is None else pool.shape[0], _flag(err_flag, dev), s), "dsa_rope_qkv656")
 
 
 def dsa_chunk_attn_workspace_bytes(T: int, H: int, B: int, layout) -> int:
@@ -452,16 +474,13 @@ def dsa_chunk_attn(q_bf16, pool, layout, page_table, page_size, cu_q, kv_lens, s
     kv_lens[b] rows of the paged pool (see include/dsa.h)."""
     dev, s = _call_device(stream)
     lay = LAYOUTS.get(layout, layout)
-    qp = _arg(q_bf16, "q_bf16", torch.bfloat16, (None, None, 576 if lay == DSA_KV_ROPE656 else 512), dev)
-    T, H, D = q_bf16.shape
+    T, H, D = _dims(q_bf16, "q_bf16", 3)
+    B, W = _dims(page_table, "page_table", 2)
+    rows, _ = _dims(pool, "pool", 2)
     i32 = torch.int32
-    pp = _arg(pool, "pool", torch.uint8, (None, None), dev)
-    tp = _arg(page_table, "page_table", i32, (None, None), dev)
-    B, max_pages = page_table.shape
-    _check(lib().dsa_chunk_attn(qp, T, H, D, pp, pool.shape[0], lay, _kv_row_dim(pool, lay), tp, B, max_pages,
-                                page_size, _arg(cu_q, "cu_q", i32, (B + 1,), dev),
-                                _arg(kv_lens, "kv_lens", i32, (B,), dev), int(causal), sm_scale,
-                                _arg(o, "o", torch.bfloat16, (T, H, 512), dev),
-                                _arg(lse, "lse", torch.float32, (T, H), dev),
-                                _arg(workspace, "workspace", torch.uint8, (None,), dev), workspace.shape[0],
-                                _arg(err_flag, "err_flag", i32, None, dev, True), s), "dsa_chunk_attn")
+    _check((_lib or lib()).dsa_chunk_attn(
+        _arg(q_bf16, "q_bf16", torch.bfloat16, None, dev), T, H, D, _arg(pool, "pool", torch.uint8, None, dev), rows, lay,
+        _kv_row_dim(pool, lay), _arg(page_table, "page_table", i32, None, dev), B, W, page_size,
+        _arg(cu_q, "cu_q", i32, (B + 1,), dev), _arg(kv_lens, "kv_lens", i32, (B,), dev), int(causal), sm_scale,
+        _arg(o, "o", torch.bfloat16, (T, H, 512), dev), _arg(lse, "lse", torch.float32, (T, H), dev),
+        _arg(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _flag(err_flag, dev), s), "dsa_chunk_attn")

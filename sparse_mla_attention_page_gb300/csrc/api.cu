@@ -14,21 +14,29 @@
 
 namespace dsa {
 
-// Current device must be compute capability 10.3; returns its SM count.
+// Current device must be compute capability 10.3; returns its SM count.  A
+// device's answer does not change, so it is asked for once a process.
 int current_device_sms(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];     // 0: not asked yet, -1: another capability
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return DSA_ERR_DEVICE;
   }
-  int major = 0, minor = 0, count = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return DSA_ERR_DEVICE;
+  int count = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (count == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return DSA_ERR_DEVICE;
+    }
+    if (major != 10 || minor != 3) count = -1;
+    if (dev < kMaxDevices) known[dev].store(count, std::memory_order_relaxed);
   }
-  if (major != 10 || minor != 3) return DSA_ERR_DEVICE;
+  if (count < 0) return DSA_ERR_DEVICE;
   *sms = count;
   return DSA_OK;
 }

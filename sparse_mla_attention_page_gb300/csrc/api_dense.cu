@@ -88,7 +88,7 @@ int dsa_pages_extend(const int32_t* seq_lens_dev, const int32_t* new_lens_dev, i
                           slots_dev,      positions_dev,      token_seq_dev,     cu_q_dev,      kv_lens_dev,
                           err_flag_dev};
   cudaGetLastError();
-  return launch_status(dsa::launch_pages_extend(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(dsa::launch_pages_extend(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int dsa_pages_release(const uint8_t* finished_dev, const int32_t* seq_lens_dev, int B,
@@ -111,7 +111,7 @@ int dsa_pages_release(const uint8_t* finished_dev, const int32_t* seq_lens_dev, 
                            free_pages_dev, free_cap,     free_count_dev,
                            free_count_out_dev, seq_lens_out_dev, err_flag_dev};
   cudaGetLastError();
-  return launch_status(dsa::launch_pages_release(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(dsa::launch_pages_release(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t pos_stride, int T, int H,

@@ -29,7 +29,7 @@ struct ExtendArgs {
   int32_t* err;
 };
 // false when nothing was launched (a launch attribute could not be set).
-bool launch_pages_extend(const ExtendArgs& a, cudaStream_t stream);
+bool launch_pages_extend(const ExtendArgs& a, int sms, cudaStream_t stream);
 
 struct ReleaseArgs {
   const uint8_t* finished;
@@ -44,7 +44,7 @@ struct ReleaseArgs {
   int32_t* seq_lens_out;
   int32_t* err;
 };
-bool launch_pages_release(const ReleaseArgs& a, cudaStream_t stream);
+bool launch_pages_release(const ReleaseArgs& a, int sms, cudaStream_t stream);
 
 struct RopeArgs {
   uint64_t turn[32];      // turns a position step, as a 64-bit fraction of one turn

@@ -60,10 +60,10 @@ def release(finished, seq, table, page, free, count):
         out["err"] = 16
     elif count + len(back) > len(free):
         out["err"] = 32
-    elif any(table[b][p] < 0 for b, p in back):
-        out["err"] = 2
     if out["err"]:
         return out
+    if any(table[b][p] < 0 for b, p in back):
+        out["err"] = 2
     for k, (b, p) in enumerate(back):
         out["free_pages"][count + k] = table[b][p]
     out["free_count"] = count + len(back)

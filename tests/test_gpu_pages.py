@@ -57,9 +57,19 @@ def test_extend(B, new_hi, ctx_hi, page):
     check_extend(make(B, page, new_hi, ctx_hi, seed=B * 1000 + page))
 
 
-def test_extend_many_tokens():
-    """More tokens than one pass of the largest cluster's threads."""
-    check_extend(make(40, 16, 4000, 100, seed=3))
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("T", [16384, 16385, 300000])
+def test_extend_many_tokens(T, in_place):
+    """The largest call of one CTA, the smallest grid, and more than one pass of a full grid's threads; the padding
+    rows count as work."""
+    w = make(40, 16, 300, 100, seed=3)
+    w["T"] = T
+    check_extend(w, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_extend_a_full_grid_of_tokens(in_place):
+    check_extend(make(90, 16, 4000, 100, seed=12), in_place=in_place)
 
 
 def test_extend_most_requests():
@@ -150,7 +160,7 @@ def test_release(B, page, ctx, in_place):
         check_release(w, [r.random() < share for _ in range(B)], in_place=in_place)
 
 
-@pytest.mark.parametrize("what,bit", [("room", 32), ("length", 16), ("negative", 16), ("page", 2), ("count", 16)])
+@pytest.mark.parametrize("what,bit", [("room", 32), ("length", 16), ("negative", 16), ("count", 16)])
 def test_release_refused_changes_nothing(what, bit):
     w = make(9, 16, 0, 100, seed=10)
     w["seq"][3] = max(w["seq"][3], 17)
@@ -162,11 +172,18 @@ def test_release_refused_changes_nothing(what, bit):
         w["seq"][5] = len(w["table"][0]) * 16 + 1
     elif what == "negative":
         w["seq"][5] = -2
-    elif what == "page":
-        w["table"][3][1] = -1
     else:
         w["count"] = len(w["free"]) + 1
-    assert check_release(w, [True] * 9)["err"] == bit
+    got = check_release(w, [True] * 9)
+    assert got["err"] == bit and got["free_pages"] == w["free"] and got["seq_lens"] == w["seq"]
+
+
+def test_release_bad_page_is_pushed_and_reported():
+    w = make(9, 16, 0, 100, seed=10)
+    w["seq"][3] = max(w["seq"][3], 17)
+    w["table"][3][:2] = [900, -1]
+    w["free"] += [-9] * 200
+    assert check_release(w, [True] * 9)["err"] == 2
 
 
 def test_captured_steps():
