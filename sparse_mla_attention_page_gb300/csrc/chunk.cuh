@@ -18,7 +18,7 @@
 namespace dsa {
 
 constexpr int kChunkTile = 128;      // keys of a tile
-constexpr int kUnitCost = 3;         // cost of a unit beside its tiles', in tiles
+constexpr int kUnitCost = 2;         // cost of a unit beside its tiles', in tiles
 
 struct __align__(16) ChunkUnit {
   int64_t tile0;     // first global tile

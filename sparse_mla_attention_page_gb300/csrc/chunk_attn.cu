@@ -84,13 +84,13 @@ struct Misc {
   uint64_t rope_full, rope_empty;  // the tile's RoPE block (a buffer of its own: it is free long before the others)
   uint64_t meta_full[kMeta];       // rows (and scales) of a tile are in place
   uint64_t s_full[kMaxSBuf], s_free[kMaxSBuf];
-  uint64_t p_full[2], p_free[2];
+  uint64_t p_full[2], p_free[2];   // a tile's P is written; its PV products are done
   uint64_t q_full;                 // a segment's query operand is built
-  uint64_t pv_done[2];             // all PV products of the even, the odd tiles
   uint64_t final[2];               // drain of the two issuers
   ChunkUnit unit[kSegs];           // of each segment, published with its first tile's rows
   uint32_t tmem_base;
   int abort;
+  int clean[kMeta];                // every key of the tile has a row
   __align__(16) int32_t rows[kMeta][kTile];   // pool row of each key (TMA: of each box's first), -1: masked
   __align__(16) float sig[2][32];  // per segment parity: log2-domain factor of each query column
   __align__(16) int vis[2][32];    // keys that it sees
@@ -387,6 +387,7 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
   for (int it = 0; it < rg.n_it; ++it) {
     const int m = it % kMeta;
     acquire();
+    int32_t row_here = -1;
     if (ptid < kTile) {
       int32_t row = -1;
       if (seen) {
@@ -394,7 +395,7 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
         if (entry < 0 || r >= a.pool_rows) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
         else row = (int32_t)r;
       }
-      ms.rows[m][ptid] = row;
+      ms.rows[m][ptid] = row_here = row;
       if (C::kScaled)
         cp_async_16_zfill(smem_u32(sm + C::SC_OFF + (m * kTile + ptid) * 16),
                           a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kD, row >= 0 ? 16u : 0u);
@@ -407,8 +408,9 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
     const bool opened = opens;
     opens = cur.advance(w, ptid);
     if (it + 1 < rg.n_it) look_up();
-    named_bar_sync(kProdBar, kProdThreads);
+    const bool whole = named_bar_red_or(kProdBar, kProdThreads, ptid < kTile && row_here < 0) == 0;
     if (ptid == 0) {
+      ms.clean[m] = whole;
       mbar_arrive(smem_u32(&ms.meta_full[m]));
       if (opened && seg > 1) prefetch_queries(a, ms.unit[(seg - 1) % kSegs]);
     }
@@ -492,6 +494,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
       if (out || r + want > a.pool_rows) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
     }
     const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0)) << w.box_shift;   // rows to come
+    const bool whole = __all_sync(0xffffffffu, !mine || (want == box && row >= 0 && (int64_t)row + box <= a.pool_rows));
     if (C::kRope) {
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ms.rope_empty), (it & 1) ^ 1, abort, w.wait_ns));
       if (!ok) break;
@@ -514,6 +517,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
       if (k == 0) {        // (the slot is free, so the tile kMeta before is out of the way)
         ++metas;
         if (mine) ms.rows[m][lane] = row;
+        if (lane == 0) ms.clean[m] = whole;
         if (opens) {
           if (lane < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[lane] = cur.word;
           __syncwarp();
@@ -655,7 +659,6 @@ __device__ void pv_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem
       step();
     }
     if (ok) mma_commit(smem_u32(&ms.p_free[pb]));
-    if (ok) mma_commit(smem_u32(&ms.pv_done[it & 1]));
   }
   drain_mma(smem_u32(&ms.final[1]));
 }
@@ -769,7 +772,13 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
   int sb = 0, s_phase = 0;
   int slot0 = 0;                                         // ring slot of the tile's first block
   int tile = 0, last = 0;                                // tile of the unit, keys that anyone sees
+  int full = 0;                                          // tiles that every column sees whole
+  // rows of the pool behind which this thread's key of a box would lie outside
+  const int in_box = kTma ? row & ((1 << w.box_shift) - 1) : 0;
+  const uint32_t row_limit = (uint32_t)max((int64_t)0, a.pool_rows - in_box);
   bool ok = true;                                        // false once a wait gave up: keep going through every barrier
+  // PV of tile i; every tile's is waited for (NPB tiles on at the latest), so the parity tells them apart
+  auto pv_wait = [&](int i) { ok &= mbar_wait(smem_u32(&ms.p_free[i % C::NPB]), (i / C::NPB) & 1, abort, w.wait_ns); };
   Segment sg;
   ok &= mbar_wait(smem_u32(&ms.meta_full[0]), 0, abort, w.wait_ns);
   build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[0], 0);
@@ -781,6 +790,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       ok &= mbar_wait(smem_u32(&ms.q_full), (sg.seg + 1) & 1, abort, w.wait_ns);
       tile = sg.open(ms, rg.t0, it, rg.n_it);
       last = ms.unit[sg.seg % kSegs].last;
+      full = ms.vis[sg.seg & 1][0] / kTile;
       m_lane = 0.f;
       has = ms.vis[sg.seg & 1][c0 + lane % CPT] == 0;
       pending = true;
@@ -789,10 +799,11 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     }
     --sg.left;
     const int par = sg.seg & 1;
-    const int j = tile * kTile + row;
-    const int32_t pool_row = ms.rows[m][row >> w.box_shift];
-    const bool valid = pool_row >= 0 && j < last &&
-                       (!kTma || (int64_t)pool_row + (row & ((1 << w.box_shift) - 1)) < a.pool_rows);
+    const bool clean = ms.clean[m] != 0;
+    // this key has a row and someone sees it
+    auto row_valid = [&]() {
+      return clean || ((uint32_t)ms.rows[m][row >> w.box_shift] < row_limit && tile * kTile + row < last);
+    };
     float sc[4] = {1.f, 1.f, 1.f, 1.f};
     float lsc = 0.f, inv = 1.f;                          // log2 S and 1 / S, S = 2^(e - 126)
     bool odd_scale = false;
@@ -864,7 +875,9 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       for (int k = 0; k < CPT; ++k) x[k] = __int_as_float(0x7FC00000);
     }
     // keys that a column does not see
-    if (!__all_sync(0xffffffffu, valid && tile * kTile + kTile <= ms.vis[par][0])) {
+    if (!clean || tile >= full) {
+      const bool valid = row_valid();
+      const int j = tile * kTile + row;
       int vis[CPT];
       ld_row<CPT>(&ms.vis[par][c0], vis);
 #pragma unroll
@@ -878,13 +891,16 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
 #pragma unroll
     for (int k = 1; k < CPT; ++k) top = fmaxf(top, x[k]);
     bool grow = pending || top > kTop;
-    float rel[4];                                        // s_g / S, at most 1
-    if (C::kScaled) {
+    // P's factors s_g / S c_g, at most 1 (what lies there for a row that nobody
+    // sees, or for one that scores NaN, is cut to finite values: p is 0, or NaN)
+    float f[C::G];
+    auto factors = [&]() {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        rel[g] = valid && !odd_scale ? fabsf(sc[g]) * inv : 0.f;
-        grow |= rel[g] * cg[g] > 1.f;
-      }
+      for (int g = 0; g < C::G; ++g) f[g] = sc[g] * inv * cg[g];
+    };
+    if (C::kScaled) {
+      factors();
+      grow |= fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1 % C::G])), fmaxf(fabsf(f[2 % C::G]), fabsf(f[3 % C::G]))) > 1.f;
     }
     if (named_bar_red_or(bar, 128, grow)) {
       float tmp[CPT];
@@ -893,7 +909,10 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       const float wmax = transpose_reduce<CPT, true>(tmp, lane);
       if (lane < CPT) ms.red[cq][quarter][lane] = wmax;
       if (C::kScaled) {
-        float t4[4] = {rel[0], rel[1], rel[2], rel[3]};
+        const bool counts = !odd_scale && row_valid();
+        float t4[4];                                     // s_g / S
+#pragma unroll
+        for (int g = 0; g < 4; ++g) t4[g] = counts ? fabsf(sc[g]) * inv : 0.f;
         const float wsc = transpose_reduce<4, true>(t4, lane);
         if (lane < 4) ms.red_sc[cq][quarter][lane] = wsc;
       }
@@ -928,15 +947,16 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       }
       named_bar_sync(bar, 128);
       if (moved) {
-        float f[CPT];
-        ld_row<CPT>(&ms.by[c0], f);
+        if (C::kScaled) factors();
+        float al[CPT];
+        ld_row<CPT>(&ms.by[c0], al);
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) x[k] -= f[k];
-        ld_row<CPT>(&ms.alpha[c0], f);
+        for (int k = 0; k < CPT; ++k) x[k] -= al[k];
+        ld_row<CPT>(&ms.alpha[c0], al);
 #pragma unroll
-        for (int k = 0; k < CP2; ++k) l_part[k] = mul2(l_part[k], pack2(f[2 * k], f[2 * k + 1]));
+        for (int k = 0; k < CP2; ++k) l_part[k] = mul2(l_part[k], pack2(al[2 * k], al[2 * k + 1]));
         if (!first) {      // O holds this segment's earlier tiles
-          ok &= mbar_wait(smem_u32(&ms.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, abort, w.wait_ns);
+          pv_wait(it - 1);
           tc_fence_after();
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {
@@ -948,7 +968,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
               tmem_ld<CPT>(at, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < CPT; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * (f[k] * bg));
+              for (int k = 0; k < CPT; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * (al[k] * bg));
               tmem_st<CPT>(at, v);
             }
           }
@@ -974,8 +994,6 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = make_uint4(0, 0, 0, 0);
     }
-    // every phase of pv_done is waited for, two tiles on, so that its parity tells the tiles apart
-    if (it >= 2) ok &= mbar_wait(smem_u32(&ms.pv_done[it & 1]), ((it >> 1) - 1) & 1, abort, w.wait_ns);
     const int pb = it % C::NPB;
     const uint32_t at = smem_u32(sm + C::P_OFF) + pb * C::P_BYTES;
 #pragma unroll
@@ -983,9 +1001,8 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       uint32_t hi2[CP2], lo2[CP2];
       uint32_t f2 = 0;
       if (C::kScaled) {
-        // a row that nobody sees may hold any scale: its weights of 0 stay 0
-        const float f = odd_scale ? 1.f : valid ? sc[g] * inv * cg[g] : 0.f;
-        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(f2) : "f"(f));
+        const float fg = fminf(fmaxf(f[g], -1.f), 1.f);
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(f2) : "f"(fg));
       }
 #pragma unroll
       for (int k = 0; k < CP2; ++k) {
@@ -994,7 +1011,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
         split2(v, hi2[k], lo2[k]);
       }
       if (g == 0 && it >= C::NPB)
-        ok &= mbar_wait(smem_u32(&ms.p_free[pb]), ((it / C::NPB) - 1) & 1, abort, w.wait_ns);
+        pv_wait(it - C::NPB);
       st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(c0, row), hi2);
       st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(NC + c0, row), lo2);
     }
@@ -1024,7 +1041,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       ms.alpha[c0 + lane] = l == 0.f ? -INFINITY : (m_lane + log2f(l)) * kLn2;
     }
     named_bar_sync(bar, 128);
-    ok &= mbar_wait(smem_u32(&ms.pv_done[it & 1]), (it >> 1) & 1, abort, w.wait_ns);
+    pv_wait(it);
     tc_fence_after();
     const bool whole = u.tile0 >= rg.t0 && u.tile0 + u.tiles <= rg.t0 + rg.n_it;
     const int64_t part = ((int64_t)blockIdx.x * 2 + (rg.t0 >= u.tile0 ? 0 : 1)) * NC;
@@ -1107,8 +1124,6 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
     mbar_init(smem_u32(&ms.rope_full), kTma ? 1 : kProdThreads);
     mbar_init(smem_u32(&ms.rope_empty), 1);
     mbar_init(smem_u32(&ms.q_full), kSmxWarps);
-    mbar_init(smem_u32(&ms.pv_done[0]), 1);
-    mbar_init(smem_u32(&ms.pv_done[1]), 1);
     ms.abort = 0;
     mbar_init_fence();
   }
