@@ -695,7 +695,7 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
   int sh = 0;
   const float base = a.sm_scale * kLog2e;
   float sig = base;
-  const bool live = amax > 0.f && amax <= 1.0e38f;
+  const bool live = amax > 0.f && amax < INFINITY;
   if (live) {
     int e;
     const float f = frexpf(amax, &e);                // amax = f 2^e, f in [0.5, 1)

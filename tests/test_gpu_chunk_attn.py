@@ -158,6 +158,112 @@ def test_zero_and_uneven_scales(layout):
     check(w)
 
 
+@pytest.mark.parametrize("layout", ["scaled528", "rope656"])
+def test_groups_of_very_different_size(layout):
+    """A 128-dim group that is 2^12 times smaller than the others in every row (and one that gets larger along the
+    sequence) keeps its own precision: its bound counts the group's own rows, lifted by the power of two that all of
+    them have in common."""
+    w = make([2, 40], [900, 200], 16, layout, seed=23)
+    s = w["pool"][:, 512:528].contiguous().view(torch.float32)
+    s[:, 1] *= 2.0 ** -12
+    j = torch.arange(int(w["kv"][0]))
+    slot = w["table"][0].long()[j // 64] * 64 + j % 64
+    s[slot, 3] *= 2.0 ** -(12 - j * 12 // j.numel()).float()
+    w["pool"][:, 512:528] = s.view(torch.uint8)
+    o, _ = check(w)
+    # group 1 alone: every row's scale there is within 2^6 of every other's, so the lifted operand resolves at least
+    # 2^-14 2^6 of the group's largest row; with the two terms and the BF16 rounding, per unit of the group's RMS:
+    ro, _, _, _, _ = ref.chunk_attn(w["q"], w["pool"], layout, w["table"], 64, w["cu"], w["kv"], SCALE)
+    g, rg = o.double()[:, :, 128:256], ro[:, :, 128:256]
+    assert (g - rg).norm() <= 2.0 ** -7 * rg.norm()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_huge_and_tiny_queries(layout):
+    """Finite BF16 queries at both ends of the type's range."""
+    w = make([3], [200], 8, layout, seed=24)
+    w["q"][0] = (w["q"][0].float() * 1e-36).to(BF)
+    w["q"][1, :4] = 0
+    w["pool"][:] = w["pool"][:1]                       # equal keys: any finite score gives the same weights
+    w["q"][2, 0] = 0
+    w["q"][2, 0, 0] = torch.finfo(BF).max
+    check(w)
+
+
+@pytest.mark.parametrize("layout", ["raw512", "rope656"])
+@pytest.mark.parametrize("H", [160, 1024])
+def test_many_heads(layout, H):
+    check(make([2, 1], [30, 150], H, layout, seed=25))
+
+
+def test_thousands_of_requests():
+    """More requests, and more units, than the planning block has threads."""
+    r = random.Random(26)
+    check(make([r.randint(0, 2) for _ in range(2500)], [r.randint(0, 3) for _ in range(2500)], 3, "rope656", page=16, seed=26))
+
+
+def test_overlapping_ranges_do_no_harm():
+    """Query ranges that overlap beyond the work list's room are reported; nothing is computed, nothing breaks."""
+    w = make([30] * 40, [5] * 40, 16, "raw512", page=16, seed=27)
+    w["cu"] = torch.tensor([0, 1200] * 20 + [0], dtype=torch.int32)
+    o, lse, err = run(w)
+    assert err == 16 and (o == 7.0).all() and (lse == 7.0).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_both_row_loads_agree(layout):
+    """Pages of 16 rows and more come by TMA, others row by row: the same bits."""
+    a = make([1, 40, 3], [300, 77, 130], 16, layout, page=16, seed=28)
+    want = run(a)
+    # the same rows as pages of one row
+    table = torch.full((3, a["table"].shape[1] * 16), -1, dtype=torch.int32)
+    for b in range(3):
+        j = torch.arange(int(a["kv"][b]))
+        table[b, :j.numel()] = (a["table"][b].long()[j // 16] * 16 + j % 16).to(torch.int32)
+    got = run(dict(a, table=table, page=1))
+    assert got[2] == want[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured calls of different batches, replayed in turn on one stream with one workspace."""
+    a, b = make([1, 30], [3000, 10], 16, "rope656", seed=29), make([40, 2], [900, 50], 16, "rope656", seed=30)
+    want = [run(a), run(b)]
+    ws = binding.chunk_workspace_for(42, 16, 2, "rope656")
+    graphs, outs, keep = [], [], []
+    for w in (a, b):
+        d = {k: v.cuda() for k, v in w.items() if isinstance(v, torch.Tensor)}
+        T, H = d["q"].shape[:2]
+        o, lse = torch.zeros(T, H, 512, dtype=BF, device="cuda"), torch.zeros(T, H, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            binding.dsa_chunk_attn(d["q"], d["pool"], "rope656", d["table"], 64, d["cu"], d["kv"], SCALE, o, lse, ws)
+        graphs.append(g)
+        outs.append((o, lse))
+        keep.append(d)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, lse), (wo, wl, _) in zip(outs, want):
+        assert torch.equal(o.cpu(), wo) and torch.equal(lse.cpu(), wl)
+
+
+@pytest.mark.parametrize("page", [64, 1])
+def test_wait_that_runs_out(page):
+    """With a limit of 0 the first wait that is not complete at once gives up: the call returns, the flag says so, and
+    the next call is right."""
+    w = make([1, 40], [700, 90], 16, "rope656", page=page, seed=31)
+    want = run(w)
+    old = binding.dsa_set_wait_limit_ns(0)
+    try:
+        _, _, err = run(w)
+    finally:
+        binding.dsa_set_wait_limit_ns(old)
+    assert err & binding.DSA_DEV_ERR_TIMEOUT
+    got = run(w)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_rows_of_no_request_are_left(layout):
     check(make([3, 1, 17], [40, 200, 0], 8, layout, seed=10, lead=4, tail=9))
