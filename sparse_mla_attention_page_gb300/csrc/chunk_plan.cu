@@ -74,7 +74,7 @@ __device__ __forceinline__ ChunkUnit unit_of(const ChunkArgs& a, const Request& 
   u.vis0 = a.causal ? r.kv - r.n + 1 : r.kv;
   u.kv = r.kv;
   u.last = chunk_visible(a, u, u.cols - 1);
-  u.tiles = u.last <= kChunkTile ? 1 : (u.last + kChunkTile - 1) / kChunkTile;
+  u.tiles = u.last <= kChunkTile ? 1 : (u.last - 1) / kChunkTile + 1;
   u.pad = 0;
   return u;
 }
