@@ -48,10 +48,7 @@ size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, char* base
     return p;
   };
   w.units = reinterpret_cast<dsa::ChunkUnit*>(take((size_t)(w.max_units + 1) * sizeof(dsa::ChunkUnit)));
-  w.starts = reinterpret_cast<dsa::ChunkStart*>(take((size_t)(sms + 1) * sizeof(dsa::ChunkStart)));
-  w.few = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
-  w.many = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
-  w.n_many = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
+  w.splits = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
   w.part_lse = reinterpret_cast<float*>(take((size_t)sms * 2 * w.nc * sizeof(float)));
   w.part_o = reinterpret_cast<float*>(take((size_t)sms * 2 * w.nc * 512 * sizeof(float)));
   return end;

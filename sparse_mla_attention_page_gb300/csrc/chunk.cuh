@@ -1,5 +1,6 @@
-// Work list of the dense attention of new tokens, shared by its plan, its
-// attention kernel and the merge of split units (chunk_plan.cu, chunk_attn.cu).
+// Work list of the dense attention of new tokens, shared by the attention
+// kernel, its plan and the merge of split units (chunk_attn.cu,
+// chunk_plan.cuh, chunk_merge.cu).
 //
 // A unit is a group of up to NC consecutive query rows of one request (row =
 // token x head, tokens outermost) and takes the 128-key tiles up to the last
@@ -8,8 +9,8 @@
 // may be spread over CTAs.  The ranges are cut evenly by cost: a unit counts
 // kUnitCost tiles more than it has, for its query operand and its output
 // (prompts of up to 2047 tokens, where units have 1 to 16 tiles: cut by tiles
-// alone the CTAs took 199 to 433 us).  Lengths live on the GPU: a plan kernel
-// writes the list into the workspace.
+// alone the CTAs took 199 to 433 us).  Lengths live on the GPU: every CTA of
+// the attention kernel forms the list's prefix sums for itself.
 #pragma once
 #include <cstdint>
 
@@ -33,19 +34,11 @@ struct __align__(16) ChunkUnit {
   int32_t pad;
 };
 
-// Where a CTA's range begins.
-struct __align__(16) ChunkStart {
-  int64_t t0;        // first global tile (the number of tiles for CTAs without work, and behind the last one)
-  int32_t unit;
-  int32_t pad;
-  ChunkUnit u;
-};
-
 // A unit spread over CTAs c0 ..: its parts lie in the slots slot0, 2 (c0 + 1), 2 (c0 + 2), ...
 struct __align__(16) ChunkSplit {
   int64_t row0;      // as of the unit
   int32_t cols;
-  int32_t parts;     // 0: no unit of few parts begins in this CTA
+  int32_t parts;     // 0: no split unit begins in this CTA
   int32_t slot0, next;
   int32_t pad[2];
 };
@@ -59,11 +52,8 @@ struct ChunkWork {
   int grid;                // CTAs of the attention grid
   int box_shift;           // log2 of the rows of a TMA box; 0: rows are copied one by one
   uint64_t wait_ns;
-  ChunkUnit* units;        // [max_units + 1]
-  ChunkStart* starts;      // [grid + 1]
-  ChunkSplit* few;         // [grid] by the CTA in which the unit begins
-  ChunkSplit* many;        // [grid] units of more parts
-  int32_t* n_many;
+  ChunkUnit* units;        // [max_units + 1]; those that begin inside a CTA's range
+  ChunkSplit* splits;      // [grid] by the CTA in which the unit begins
   float* part_lse;         // [2 grid][nc]
   float* part_o;           // [2 grid][nc][512] normalised
 };
@@ -75,7 +65,6 @@ __device__ __forceinline__ int chunk_visible(const ChunkArgs& a, const ChunkUnit
   return v < 0 ? 0 : v > u.kv ? u.kv : (int)v;
 }
 
-void launch_chunk_plan(const ChunkWork& w, cudaStream_t stream);
 bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream);
 
 }  // namespace dsa

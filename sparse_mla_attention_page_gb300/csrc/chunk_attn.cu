@@ -53,6 +53,7 @@
 #include <type_traits>
 
 #include "chunk.cuh"
+#include "chunk_plan.cuh"
 #include "dsa_common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -98,6 +99,7 @@ struct Misc {
   __align__(16) float by[32], alpha[32];   // a move of the maxima, and its factor; at a segment's end 1 / l and LSE
   float red[4][4][8];             // [column quarter][lane quarter][column]
   float red_sc[4][4][4];           // [column quarter][lane quarter][group]
+  ChunkRange range;                // the CTA's part of the tile list
 };
 constexpr int kMiscBytes = 5120;
 static_assert(sizeof(Misc) <= kMiscBytes, "misc area");
@@ -106,7 +108,7 @@ template <int NC, int kLayout, bool kTma>
 struct Cfg {
   static constexpr bool kScaled = kLayout != DSA_KV_RAW512;
   static constexpr bool kRope = kLayout == DSA_KV_ROPE656;
-  [[maybe_unused]] static constexpr int R = kLayout == DSA_KV_RAW512 ? kRawRow : kLayout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
+  static constexpr int R = kLayout == DSA_KV_RAW512 ? kRawRow : kLayout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
   static constexpr int CPT = NC / 4;                 // query columns of a softmax thread
   // Registers: the launch gives every thread LAUNCH_REGS; the softmax warps
   // then take SMX_REGS and the others give back to OTHER_REGS.
@@ -143,6 +145,7 @@ struct Cfg {
   static constexpr int MISC_OFF = SC_OFF + SC_BYTES;
   static constexpr int SMEM = MISC_OFF + kMiscBytes + 1024;
   static_assert(NS > 4, "a tile's blocks and one more");
+  static_assert(NS * kBlock >= kPlanScratch, "the plan's scratch lies in the ring");
   // a tile's rows are replaced kMeta tiles later, when its blocks are gone from the ring
   static_assert((NS - 1) / 4 + 1 < kMeta, "rows of a tile in use");
   static_assert(SMEM <= kSmemLimit && TMEM_USED <= 512 && P_GROUP % 1024 == 0 && QR_BYTES % 1024 == 0, "budgets");
@@ -294,7 +297,7 @@ struct Range {
 struct Walk {
   int unit, tile, tiles, b, last;
   int next_tiles, next_b, next_last;
-  int32_t word, next_word;
+  int32_t word = 0, next_word = 0;
   static constexpr int kWords = sizeof(ChunkUnit) / 4;
   __device__ __forceinline__ void fetch_next(const ChunkWork& w, int ptid) {
     const ChunkUnit* u = w.units + unit + 1;     // (behind the last unit: read, never used)
@@ -303,15 +306,13 @@ struct Walk {
     next_last = __ldcg(&u->last);
     if (ptid < kWords) next_word = __ldcg(reinterpret_cast<const int32_t*>(u) + ptid);
   }
-  __device__ __forceinline__ Walk(const ChunkWork& w, int ptid, const Range& rg) {
-    const ChunkStart* s = w.starts + blockIdx.x;
-    unit = __ldcg(&s->unit);
-    tiles = __ldcg(&s->u.tiles);
-    b = __ldcg(&s->u.b);
-    last = __ldcg(&s->u.last);
-    tile = (int)(rg.t0 - __ldcg(&s->u.tile0));
-    word = next_word = 0;
-    if (ptid < kWords) word = __ldcg(reinterpret_cast<const int32_t*>(&s->u) + ptid);
+  __device__ __forceinline__ Walk(const ChunkWork& w, const Misc& ms, int ptid) {
+    const ChunkUnit& u = ms.unit[0];
+    unit = ms.range.unit;
+    tiles = u.tiles;
+    b = u.b;
+    last = u.last;
+    tile = (int)(ms.range.t0 - u.tile0);
     fetch_next(w, ptid);
   }
   // true when the next tile starts a segment
@@ -364,7 +365,7 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
   volatile int* abort = &ms.abort;
   const uint32_t kv0 = smem_u32(sm);
   // thread -> key ptid of each tile: its page-table entry is fetched a tile ahead
-  Walk cur(w, ptid, rg);
+  Walk cur(w, ms, ptid);
   int32_t entry = -1, off = 0;
   bool seen = false;
   auto look_up = [&]() {
@@ -401,8 +402,8 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
                           a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kD, row >= 0 ? 16u : 0u);
     }
     if (C::kScaled) cp_async_arrive_noinc(smem_u32(&ms.meta_full[m]));
-    if (opens) {
-      if (ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
+    if (opens) {       // (the first unit is the plan's)
+      if (seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
       ++seg;
     }
     const bool opened = opens;
@@ -470,7 +471,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
   const bool mine = lane < (kTile >> w.box_shift);
   volatile int* abort = &ms.abort;
   const uint32_t kv0 = smem_u32(sm) + ((uint32_t)lane << (w.box_shift + 7));
-  Walk cur(w, lane, rg);
+  Walk cur(w, ms, lane);
   int32_t entry = -1, off = 0, want = 0;     // the next tile's: page-table entry, row in the page, keys seen of the box
   auto look_up = [&]() {
     const int j = cur.tile * kTile + (lane << w.box_shift);
@@ -519,7 +520,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
         if (mine) ms.rows[m][lane] = row;
         if (lane == 0) ms.clean[m] = whole;
         if (opens) {
-          if (lane < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[lane] = cur.word;
+          if (seg > 0 && lane < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[lane] = cur.word;
           __syncwarp();
           if (lane == 0 && seg > 0) prefetch_queries(a, ms.unit[seg % kSegs]);
           ++seg;
@@ -780,7 +781,6 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
   // PV of tile i; every tile's is waited for (NPB tiles on at the latest), so the parity tells them apart
   auto pv_wait = [&](int i) { ok &= mbar_wait(smem_u32(&ms.p_free[i % C::NPB]), (i / C::NPB) & 1, abort, w.wait_ns); };
   Segment sg;
-  ok &= mbar_wait(smem_u32(&ms.meta_full[0]), 0, abort, w.wait_ns);
   build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[0], 0);
   for (int it = 0; it < rg.n_it; ++it) {
     const bool first = sg.starts();
@@ -1135,12 +1135,15 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
-  // everything above overlapped the plan, whose list is visible from here on
+  // everything above may overlap the kernel in front; what it wrote is visible from here on
   grid_dependency_wait();
+  chunk_plan<C::THREADS>(w, sm, ms.range, ms.unit[0]);
+  fence_proxy_async_smem();   // the plan's scratch becomes the ring
+  __syncthreads();
   grid_launch_dependents();   // the merge: its blocks wait for the whole grid
   Range rg;
-  rg.t0 = __ldcg(&w.starts[blockIdx.x].t0);
-  rg.n_it = (int)(__ldcg(&w.starts[blockIdx.x + 1].t0) - rg.t0);
+  rg.t0 = ms.range.t0;
+  rg.n_it = (int)(ms.range.t1 - rg.t0);
   if (rg.n_it > 0) {          // the same for the whole CTA
     if (warp < kSmxWarps) {
       regs_inc<C::SMX_REGS>();
@@ -1179,7 +1182,6 @@ bool launch(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
       return false;
     configured.fetch_or(bit);
   }
-  launch_chunk_plan(w, stream);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(w.grid);
   cfg.blockDim = dim3(C::THREADS);

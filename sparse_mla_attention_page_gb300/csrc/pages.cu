@@ -22,7 +22,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = kScanThreads;
+constexpr int kThreads = 1024;
 constexpr int kOneCta = 16 * kThreads;    // pages and tokens that one CTA takes on
 
 enum Part { kBody = 1, kFinish = 2 };     // bits: pages and tokens; lengths, offsets and the free count
@@ -33,6 +33,7 @@ __device__ __forceinline__ int64_t pages_of(int64_t tokens, int page_size) {
 
 __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const __grid_constant__ ExtendArgs a, int parts) {
   extern __shared__ int32_t sm[];
+  __shared__ int64_t sums[kThreads / 32];
   int32_t* tok0 = sm;              // first token of each request
   int32_t* page0 = sm + a.B;       // first of the call's pages of each request
   int32_t* seq = sm + 2 * a.B;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const __grid_
     pages += pages_of(s + n, a.page_size) - pages_of(s, a.page_size);
   }
   int64_t all_tokens, all_pages;
-  int64_t tok_at = block_scan(tokens, &all_tokens), page_at = block_scan(pages, &all_pages);
+  int64_t tok_at = block_scan<kThreads>(tokens, &all_tokens, sums), page_at = block_scan<kThreads>(pages, &all_pages, sums);
   bad |= all_tokens > a.T;
   const bool lengths_bad = __syncthreads_or(bad) != 0;
   const bool refused = lengths_bad || all_pages > count;
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const __grid_
 
 __global__ void __launch_bounds__(kThreads, 1) pages_release_kernel(const __grid_constant__ ReleaseArgs a, int parts) {
   extern __shared__ int32_t sm[];
+  __shared__ int64_t sums[kThreads / 32];
   int32_t* page0 = sm;             // first of the call's pages of each request
   if (parts == kFinish) asm volatile("griddepcontrol.wait;" ::: "memory");
   else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_release_kernel(const __grid
     pages += back(b);
   }
   int64_t all_pages;
-  int64_t at = block_scan(pages, &all_pages);
+  int64_t at = block_scan<kThreads>(pages, &all_pages, sums);
   const bool lengths_bad = __syncthreads_or(bad) != 0;
   const bool refused = lengths_bad || count + all_pages > a.free_cap;
   for (int b = b0; b < b1; ++b) {

@@ -1,14 +1,15 @@
-// Prefix sums over the requests of a batch, by one block of 1024 threads.
+// Prefix sums over the requests of a batch, by one block.
 #pragma once
 #include <cstdint>
 
 namespace dsa {
 
-constexpr int kScanThreads = 1024;
-
-// Exclusive prefix sum of v over the block's threads; *total gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
-  __shared__ int64_t warp_sums[kScanThreads / 32];
+// Exclusive prefix sum of v over the block's THREADS threads; *total gets the
+// sum.  warp_sums: THREADS / 32 entries of shared memory.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t* warp_sums) {
+  constexpr int kWarps = THREADS / 32;
+  static_assert(THREADS % 32 == 0 && kWarps <= 32, "one warp sums the warps");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t s = v;
 #pragma unroll
@@ -20,16 +21,16 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    int64_t x = warp_sums[lane];
+    int64_t x = lane < kWarps ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int64_t t = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += t;
     }
-    warp_sums[lane] = x;
+    if (lane < kWarps) warp_sums[lane] = x;
   }
   __syncthreads();
-  *total = warp_sums[kScanThreads / 32 - 1];
+  *total = warp_sums[kWarps - 1];
   return (warp == 0 ? 0 : warp_sums[warp - 1]) + s - v;
 }
 
