@@ -7,9 +7,7 @@
 // key that its last row sees.  The units' tiles, one after another, are the
 // global tile list; CTA c of the persistent grid owns a range of it, so a unit
 // may be spread over CTAs.  The ranges are cut evenly by cost: a unit counts
-// kUnitCost tiles more than it has, for its query operand and its output
-// (prompts of up to 2047 tokens, where units have 1 to 16 tiles: cut by tiles
-// alone the CTAs took 199 to 433 us).  Lengths live on the GPU: every CTA of
+// chunk_unit_cost more than its tiles, for its query operand and its output.  Lengths live on the GPU: every CTA of
 // the attention kernel forms the list's prefix sums for itself.
 #pragma once
 #include <cstdint>
@@ -19,7 +17,19 @@
 namespace dsa {
 
 constexpr int kChunkTile = 128;      // keys of a tile
-constexpr int kUnitCost = 2;         // cost of a unit beside its tiles', in tiles
+
+// Costs of a tile, and of a unit beside its tiles'.  Tiles of short boxes, or
+// of rows that are copied one by one, take longer (the copies set the pace),
+// so a unit counts less beside them.  Measured, five prompts of up to 2047
+// tokens and 16 heads, units of 1 to 16 tiles, us for a unit cost of 3 / 4 / 5:
+//   pages of 64   raw 237 / 213 / 196   scaled 303 / 279 / 277   rope 362 / 334 / 338
+//   pages of 16   raw 239 / 245 / 251   scaled 309 / 320 / 326   rope 357 / 367 / 375
+//   pages of 1    raw 283 / 294 / 300   scaled 336 / 348 / 357   rope 386 / 399 / 409
+// (a cost of 2: 275, 338 and 398 over pages of 16).
+constexpr int kTileCost = 2;
+constexpr int chunk_unit_cost(int layout, int box_shift) {
+  return box_shift < 5 ? 3 : layout == DSA_KV_RAW512 ? 5 : 4;
+}
 
 struct __align__(16) ChunkUnit {
   int64_t tile0;     // first global tile
@@ -51,6 +61,7 @@ struct ChunkWork {
   int64_t max_units;
   int grid;                // CTAs of the attention grid
   int box_shift;           // log2 of the rows of a TMA box; 0: rows are copied one by one
+  int unit_cost;
   uint64_t wait_ns;
   ChunkUnit* units;        // [max_units + 1]; those that begin inside a CTA's range
   ChunkSplit* splits;      // [grid] by the CTA in which the unit begins

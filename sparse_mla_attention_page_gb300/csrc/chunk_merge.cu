@@ -2,11 +2,16 @@
 //
 // A split unit's parts are normalised (O_c, LSE_c) of its query rows
 // over disjoint keys: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
-// Units of few parts (nearly all): a thread for each 8 dims of a row folds the
-// parts four at a time.  Units of many parts (a long context over most SMs): a
-// block for each quarter of a row's dims, first the weights of all parts (one
-// a thread), then 16 part lanes of 16 threads with four parts' loads in flight,
-// so that 150 parts cost three round trips and not forty.
+// Units of few parts (nearly all): a thread for each 4 dims of a row, all
+// parts' loads in flight at once.  Units of many parts (a long context over
+// most SMs): a block for each eighth of a row's dims, the weights of all parts
+// (one a thread) while the first parts' loads are in flight, 32 part lanes of
+// 8 threads.  Both are chains of a few trips to the L2 cache, so what counts is
+// that no load waits for another and that the blocks are resident at once:
+// 32.3 us for one request of 131072 scaled rows (150 parts) with 256 slices in
+// flight, 34.6 with 128 whose loads came after the weights; 81.8 us for 32
+// requests of 4096 rows and two tokens of 128 heads with four blocks of rows a
+// unit, 85 with sixteen.
 #include <cuda_bf16.h>
 
 #include "chunk.cuh"
@@ -16,13 +21,15 @@ namespace dsa {
 namespace {
 
 constexpr int kMergeThreads = 256;
-constexpr int kBatch = 4;                                 // parts whose loads are issued together
-constexpr int kFewThreads = kD / 8;                       // few parts: threads of a row, 8 dims each
+constexpr int kFewThreads = kD / 4;                       // few parts: threads of a row, 4 dims each
 constexpr int kFewRows = kMergeThreads / kFewThreads;
-constexpr int kVec = 2;                                   // many parts: float4 of a thread
-constexpr int kDimThreads = 16;                           // threads of a quarter of a row's dims
+constexpr int kFewBlocks = 4;                             // blocks of a unit (all resident: four fit an SM)
+constexpr int kSlices = 8;                                // many parts: blocks of a row
+constexpr int kSlice4 = kD / 4 / kSlices;                 // float4 of a slice
+constexpr int kVec = 2;                                   // float4 of a thread
+constexpr int kDimThreads = kSlice4 / kVec;
 constexpr int kLanes = kMergeThreads / kDimThreads;       // part lanes
-constexpr int kQuarter = kD / 4 / 4;                      // float4 of a quarter
+constexpr int kBatch = 5;                                 // parts of a lane whose loads are issued together (160 at once)
 constexpr int kMaxParts = 1024;                           // CTAs of the attention grid (one per SM)
 
 __device__ __forceinline__ void fold(float4& acc, float w, const float4& v) {
@@ -51,20 +58,33 @@ __device__ __forceinline__ ChunkSplit split_of(const ChunkSplit* s) {
   return x.s;
 }
 
-// One quarter of one row of a unit of many parts, by the whole block.
-__device__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, int dq) {
+// One slice of one row of a unit of many parts, by the whole block.
+__device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, int slice) {
   __shared__ float wt[kMaxParts];
   __shared__ float red[kMergeThreads / 32], red2[kMergeThreads / 32];
-  __shared__ float4 acc_s[kLanes][kQuarter];
+  __shared__ float4 acc_s[kLanes][kSlice4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto slot = [&](int p) { return (int64_t)(p == 0 ? sp.slot0 : sp.next + 2 * (p - 1)) * w.nc + col; };
+  const int pl = tid / kDimThreads, dt = tid % kDimThreads;
+  float4 v[kBatch][kVec];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int p = p0 + q * kLanes;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        v[q][i] = p < sp.parts ? __ldcg(reinterpret_cast<const float4*>(w.part_o + slot(p) * kD) + slice * kSlice4 + dt + i * kDimThreads)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load(pl);
   float m = -INFINITY;
   bool nan = false;
   for (int p = tid; p < sp.parts; p += kMergeThreads) {
-    const float v = __ldcg(w.part_lse + slot(p));
-    wt[p] = v;
-    m = fmaxf(m, v);
-    nan |= v != v;
+    const float x = __ldcg(w.part_lse + slot(p));
+    wt[p] = x;
+    m = fmaxf(m, x);
+    nan |= x != x;
   }
   m = warp_max(m);
   if (lane == 0) red[warp] = m;
@@ -82,18 +102,9 @@ __device__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, in
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kMergeThreads / 32; ++i) sum += red2[i];
-  const int pl = tid / kDimThreads, dt = tid % kDimThreads;
   float4 acc[kVec] = {};
   for (int p0 = pl; p0 < sp.parts; p0 += kLanes * kBatch) {
-    float4 v[kBatch][kVec];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const int p = p0 + q * kLanes;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        v[q][i] = p < sp.parts ? __ldcg(reinterpret_cast<const float4*>(w.part_o + slot(p) * kD) + dq * kQuarter + dt + i * kDimThreads)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    if (p0 != pl) load(p0);
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       const int p = p0 + q * kLanes;
@@ -105,11 +116,12 @@ __device__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, in
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc_s[pl][dt + i * kDimThreads] = acc[i];
   __syncthreads();
-  if (tid < kQuarter) {
+  if (tid < kSlice4) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
     for (int i = 0; i < kLanes; ++i) fold(o, 1.f, acc_s[i][tid]);
-    store_row(w.a, sp.row0 + col, dq * kQuarter + tid, o, sum == 0.f ? 0.f : 1.f / sum);
-    if (tid == 0 && dq == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
+    store_row(w.a, sp.row0 + col, slice * kSlice4 + tid, o, sum == 0.f ? 0.f : 1.f / sum);
+    if (tid == 0 && slice == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
   }
   __syncthreads();   // acc_s, wt and the sums are free for the next row
 }
@@ -117,58 +129,52 @@ __device__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, in
 __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __grid_constant__ ChunkWork w) {
   asm volatile("griddepcontrol.wait;" ::: "memory");               // every part is written
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the units of many parts, a bit for each CTA that one begins in
+  // The units of many parts: a bit for each CTA that one begins in, and its
+  // entry (they begin more than kFewParts CTAs apart).
   __shared__ uint32_t many[kMaxParts / 32];
+  __shared__ ChunkSplit big[kMaxParts / kFewParts];
   for (int c0 = threadIdx.x & ~31; c0 < w.grid; c0 += kMergeThreads) {
     const int c = c0 + (threadIdx.x & 31);
-    const uint32_t bits = __ballot_sync(0xffffffffu, c < w.grid && __ldcg(&w.splits[c].parts) > kFewParts);
+    ChunkSplit s{};
+    if (c < w.grid) s = split_of(w.splits + c);
+    if (s.parts > kFewParts) big[c / kFewParts] = s;
+    const uint32_t bits = __ballot_sync(0xffffffffu, s.parts > kFewParts);
     if ((threadIdx.x & 31) == 0) many[c0 / 32] = bits;
   }
-  const ChunkSplit sp = split_of(w.splits + blockIdx.x);           // blockIdx.y: four rows of the unit
-  const int col = blockIdx.y * kFewRows + threadIdx.x / kFewThreads, d8 = threadIdx.x % kFewThreads;
-  if (sp.parts > 0 && sp.parts <= kFewParts && col < sp.cols) {
-    float m = -INFINITY, sum = 0.f;
-    float4 acc[2] = {};
-    for (int p0 = 0; p0 < sp.parts; p0 += kBatch) {
-      float ls[kBatch];
-      float4 v[kBatch][2];
+  const ChunkSplit sp = split_of(w.splits + blockIdx.x);           // blockIdx.y: every fourth pair of rows
+  const int d4 = threadIdx.x % kFewThreads;
+  for (int col = blockIdx.y * kFewRows + threadIdx.x / kFewThreads; sp.parts > 0 && sp.parts <= kFewParts && col < sp.cols; col += gridDim.y * kFewRows) {
+    float ls[kFewParts];
+    float4 v[kFewParts];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const int p = p0 + q;
-        const int64_t at = (int64_t)(p == 0 ? sp.slot0 : sp.next + 2 * (p - 1)) * w.nc + col;
-        const float4* src = reinterpret_cast<const float4*>(w.part_o + at * kD) + 2 * d8;
-        ls[q] = p < sp.parts ? __ldcg(w.part_lse + at) : -INFINITY;
-        v[q][0] = p < sp.parts ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[q][1] = p < sp.parts ? __ldcg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        if (ls[q] == -INFINITY) continue;                          // a part without a visible key
-        const float mn = fmaxf(m, ls[q]);
-        const float r = m == -INFINITY ? 0.f : expf(m - mn), e = expf(ls[q] - mn);
-        sum = fmaf(sum, r, e);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          acc[i] = make_float4(acc[i].x * r, acc[i].y * r, acc[i].z * r, acc[i].w * r);
-          fold(acc[i], e, v[q][i]);
-        }
-        m = mn;
-      }
+    for (int p = 0; p < kFewParts; ++p) {
+      const int64_t at = (int64_t)(p == 0 ? sp.slot0 : sp.next + 2 * (p - 1)) * w.nc + col;
+      ls[p] = p < sp.parts ? __ldcg(w.part_lse + at) : -INFINITY;
+      v[p] = p < sp.parts ? __ldcg(reinterpret_cast<const float4*>(w.part_o + at * kD) + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    store_row(w.a, sp.row0 + col, 2 * d8, acc[0], inv);
-    store_row(w.a, sp.row0 + col, 2 * d8 + 1, acc[1], inv);
-    if (d8 == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
+    float m = ls[0], sum = 0.f;
+#pragma unroll
+    for (int p = 1; p < kFewParts; ++p) m = fmaxf(m, ls[p]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) {
+      if (ls[p] == -INFINITY) continue;                            // a part without a visible key
+      const float e = expf(ls[p] - m);                             // (NaN where one of them is: fmaxf passes it over)
+      sum += e;
+      fold(acc, e, v[p]);
+    }
+    store_row(w.a, sp.row0 + col, d4, acc, sum == 0.f ? 0.f : 1.f / sum);
+    if (d4 == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
   }
   __syncthreads();
-  // the quarter rows of those units, over all blocks
+  // the slices of those units' rows, over all blocks
   const int blocks = gridDim.x * gridDim.y;
   int item = blockIdx.y * gridDim.x + blockIdx.x;                  // from the unit's first on
   for (int i = 0; i < (w.grid + 31) / 32; ++i)
     for (uint32_t bits = many[i]; bits != 0; bits &= bits - 1) {
-      const ChunkSplit big = split_of(w.splits + 32 * i + __ffs(bits) - 1);
-      for (; item < 4 * big.cols; item += blocks) merge_many(w, big, item / 4, item % 4);
-      item -= 4 * big.cols;
+      const ChunkSplit& u = big[(32 * i + __ffs(bits) - 1) / kFewParts];
+      for (; item < kSlices * u.cols; item += blocks) merge_many(w, u, item / kSlices, item % kSlices);
+      item -= kSlices * u.cols;
     }
 }
 
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
 bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
   if (w.grid > kMaxParts) return false;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(w.grid, w.nc / kFewRows);
+  cfg.gridDim = dim3(w.grid, kFewBlocks);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -129,9 +129,9 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   });
   int64_t n_tiles;
   int64_t tile0 = block_scan<THREADS>(tiles, &n_tiles, sums);
-  // cost: position v of the list, of length V, is tile v - v0 - kUnitCost of the
-  // unit that begins at v0, or its first; CTA c begins at floor(c V / grid)
-  const int64_t V = n_tiles + (int64_t)n_units * kUnitCost;
+  // cost: position v of the list, of length V, is tile (v - body) / kTileCost of
+  // the unit whose tiles begin at body, or its first; CTA c begins at floor(c V / grid)
+  const int64_t V = n_tiles * kTileCost + (int64_t)n_units * w.unit_cost;
   const int grid = (int)(n_tiles < w.grid ? n_tiles : w.grid);
   const bool idle = cta >= grid, ends = cta + 1 >= grid;     // nothing to do; the last range
   if (tid == 0) {
@@ -141,23 +141,24 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   }
   if (idle) return;
   const int64_t va = cta * V / grid, vb = (cta + 1) * V / grid;
-  int64_t v0 = tile0 + (int64_t)u0 * kUnitCost;
+  int64_t v0 = tile0 * kTileCost + (int64_t)u0 * w.unit_cost;
   walk([&](int u, ChunkUnit e) {
     e.tile0 = tile0;
-    const int64_t body = v0 + kUnitCost, end = body + e.tiles;
+    const int64_t body = v0 + w.unit_cost, end = body + (int64_t)e.tiles * kTileCost;
+    auto tile_at = [&](int64_t v) { return v < body ? 0 : (v - body) / kTileCost; };
     if (v0 > va && v0 < vb) w.units[u] = e;
     if (va >= v0 && va < end) {
       start = e;
       mine.unit = u;
-      mine.t0 = tile0 + max(va - body, (int64_t)0);
+      mine.t0 = tile0 + tile_at(va);
     }
     if (!ends && vb >= v0 && vb < end) {
-      mine.t1 = tile0 + max(vb - body, (int64_t)0);
+      mine.t1 = tile0 + tile_at(vb);
       // Does the unit end in a later CTA, and begin in this one?  Its parts lie
       // in CTAs cta .. ceil(end grid / V) - 1: in slot 0 of a CTA whose range
       // starts with the unit, in slot 1 where another one is in front.
       ChunkSplit sp{};
-      if (vb > body && va <= body) {
+      if (tile_at(vb) > 0 && tile_at(va) == 0) {
         sp.row0 = e.row0;
         sp.cols = e.cols;
         sp.parts = (int)min((end * grid + V - 1) / V, (int64_t)grid) - cta;
