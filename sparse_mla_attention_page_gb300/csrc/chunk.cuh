@@ -18,17 +18,13 @@ namespace dsa {
 
 constexpr int kChunkTile = 128;      // keys of a tile
 
-// Costs of a tile, and of a unit beside its tiles'.  Tiles of short boxes, or
-// of rows that are copied one by one, take longer (the copies set the pace),
-// so a unit counts less beside them.  Measured, five prompts of up to 2047
-// tokens and 16 heads, units of 1 to 16 tiles, us for a unit cost of 3 / 4 / 5:
-//   pages of 64   raw 237 / 213 / 196   scaled 303 / 279 / 277   rope 362 / 334 / 338
-//   pages of 16   raw 239 / 245 / 251   scaled 309 / 320 / 326   rope 357 / 367 / 375
-//   pages of 1    raw 283 / 294 / 300   scaled 336 / 348 / 357   rope 386 / 399 / 409
-// (a cost of 2: 275, 338 and 398 over pages of 16).
+// Costs of a tile, and of a unit beside its tiles'.  us of five prompts of up to
+// 2047 tokens and 16 heads, units of 1 to 16 tiles, for a unit cost of 3 / 4 / 5:
+//   rows by TMA       raw 237 / 213 / 196   scaled 303 / 279 / 277   rope 362 / 334 / 338
+//   rows one by one   raw 248 / 236 / 242   scaled 307 / 296 / 304   rope 370 / 360 / 368
 constexpr int kTileCost = 2;
 constexpr int chunk_unit_cost(int layout, int box_shift) {
-  return box_shift < 5 ? 3 : layout == DSA_KV_RAW512 ? 5 : 4;
+  return layout == DSA_KV_RAW512 && box_shift > 0 ? 5 : 4;
 }
 
 struct __align__(16) ChunkUnit {

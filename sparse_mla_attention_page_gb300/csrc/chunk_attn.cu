@@ -38,9 +38,12 @@
 // the tile, column quarter w / 4), one issuing thread for each product, and
 // producers that translate keys to rows and bring them into a ring of 16 KB
 // blocks (128 keys x 128 bytes).  A block is released as soon as the product
-// that reads it last has finished.  Pages of a multiple of 16 rows come by TMA
-// (one warp, boxes of 16 to 128 rows: a page never ends inside a box); other
-// page sizes row by row with 16-byte cp.async (six warps).
+// that reads it last has finished.  Pages of a multiple of 32 rows come by TMA
+// (one warp, boxes of 32 to 128 rows: a page never ends inside a box); other
+// page sizes row by row with 16-byte cp.async (six warps).  us by TMA / row by
+// row, pages of 16 (boxes of 16): 1024 tokens of 16 heads over 8192, raw 434 /
+// 370, scaled 565 / 464, rope 637 / 583; 64 single tokens over up to 8192, raw
+// 47.6 / 42.8; pages of 32 (prompts of up to 2047 tokens, raw): 211 / 236.
 //
 // What lies in shared memory for a key that nobody sees (the rest of a page, a
 // box that was not loaded) has no effect: its weights are 0, and a row that
@@ -70,9 +73,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSmxWarps = 16, kSmxThreads = 512;
 constexpr int kQkWarp = 16, kPvWarp = 17, kProdWarp0 = 18;
-constexpr int kProdWarps = 6, kProdThreads = 192;    // of the row-by-row form
+constexpr int kProdWarps = 6, kProdThreads = 32 * kProdWarps;    // of the row-by-row form
 constexpr int kQuads = kTile / 4;            // producer work unit: 4 rows (one warp instruction per 128-byte piece)
-constexpr int kQuadsPerWarp = (kQuads + kProdWarps - 1) / kProdWarps;
 constexpr int kMeta = 4;                     // tiles whose rows and scales are kept
 constexpr int kSegs = 6;                     // segments whose units are kept
 constexpr int kMaxSBuf = 4;                  // score buffers
@@ -112,11 +114,11 @@ struct Cfg {
   static constexpr int CPT = NC / 4;                 // query columns of a softmax thread
   // Registers: the launch gives every thread LAUNCH_REGS; the softmax warps
   // then take SMX_REGS and the others give back to OTHER_REGS.
-  static constexpr int THREADS = kTma ? 640 : 768;
+  static constexpr int THREADS = kTma ? 640 : 32 * (kProdWarp0 + kProdWarps);
   static constexpr int LAUNCH_REGS = kTma ? 96 : 80;
   static constexpr int SMX_REGS = kTma ? 104 : 88;
-  static constexpr int OTHER_REGS = (LAUNCH_REGS * THREADS - SMX_REGS * kSmxThreads) / (THREADS - kSmxThreads);
-  static_assert(SMX_REGS * kSmxThreads + OTHER_REGS * (THREADS - kSmxThreads) == LAUNCH_REGS * THREADS &&
+  static constexpr int OTHER_REGS = (LAUNCH_REGS * THREADS - SMX_REGS * kSmxThreads) / (THREADS - kSmxThreads) / 8 * 8;
+  static_assert(SMX_REGS * kSmxThreads + OTHER_REGS * (THREADS - kSmxThreads) <= LAUNCH_REGS * THREADS &&
                 SMX_REGS % 8 == 0 && OTHER_REGS % 8 == 0, "register split");
   static constexpr int G = kScaled ? 4 : 1;          // P operands of a tile
   static constexpr int NPASS = G + (kRope ? 1 : 0);  // score passes of a tile (RoPE first)
@@ -134,6 +136,14 @@ struct Cfg {
   static constexpr int P_BYTES = G * P_GROUP;
   static constexpr int SC_BYTES = kScaled ? kMeta * kTile * 16 : 0;
   static constexpr int ROPE_BYTES = kRope ? kBlock : 0;
+  // The row-by-row producers: groups that take the blocks in turn, warps of a
+  // group, quads of rows of a warp.  A block's barrier takes an arrival from
+  // each thread of a group: three groups of two warps run raw and scaled rows
+  // 9 and 6 % faster than one of six (1024 tokens of 16 heads over 8192: 375
+  // against 412 us, 480 against 513); with the RoPE block they lose 2 to 8 %.
+  static constexpr int GROUPS = kRope ? 1 : 3;
+  static constexpr int GW = kProdWarps / GROUPS, QW = (kQuads + GW - 1) / GW;
+  static_assert(kProdWarps % GROUPS == 0 && GW % 2 == 0, "rows of a thread share their place in the swizzle");
   static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES + ROPE_BYTES;
   static constexpr int NS_FIT = (kSmemLimit - FIXED - NPB * P_BYTES) / kBlock;
   static constexpr int NS = NS_FIT < kMaxBlocks ? NS_FIT : kMaxBlocks;
@@ -364,6 +374,10 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
   const int rq = lane >> 3, ch = lane & 7;
   volatile int* abort = &ms.abort;
   const uint32_t kv0 = smem_u32(sm);
+  // this thread's rows of a block: r0, r0 + 4 GW, ...; where its 16 bytes of the first one go
+  const int group = pw / C::GW, gw = pw % C::GW, r0 = 4 * gw + rq;
+  const uint32_t dst0 = (r0 >> 3) * 1024 + (r0 & 7) * 128 + ((ch ^ (r0 & 7)) << 4);
+  int turn = 0;
   // thread -> key ptid of each tile: its page-table entry is fetched a tile ahead
   Walk cur(w, ms, ptid);
   int32_t entry = -1, off = 0;
@@ -415,16 +429,21 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
       mbar_arrive(smem_u32(&ms.meta_full[m]));
       if (opened && seg > 1) prefetch_queries(a, ms.unit[(seg - 1) % kSegs]);
     }
+    int32_t rows[C::QW];
+    auto load_rows = [&]() {
+#pragma unroll
+      for (int i = 0; i < C::QW; ++i) rows[i] = gw + i * C::GW < kQuads ? ms.rows[m][r0 + 4 * C::GW * i] : -1;
+    };
+    if (C::GROUPS == 1) load_rows();
     // 128 bytes of every row, from byte `col` of it
     auto copy = [&](uint32_t base, int col, uint32_t bar) {
+      if (C::GROUPS > 1) load_rows();
 #pragma unroll
-      for (int i = 0; i < kQuadsPerWarp; ++i) {
-        const int q = pw + i * kProdWarps;
-        if (q >= kQuads) break;
-        const int r = 4 * q + rq;
-        const int32_t pr = ms.rows[m][r];
-        const uint8_t* src = a.pool + (int64_t)(pr >= 0 ? pr : 0) * C::R + col + ch * 16;
-        cp_async_16_zfill(base + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4), src, pr >= 0 ? 16u : 0u);
+      for (int i = 0; i < C::QW; ++i) {
+        if (gw + i * C::GW >= kQuads) break;
+        const int32_t pr = rows[i];
+        const uint8_t* src = a.pool + (int64_t)(pr >= 0 ? pr : 0) * C::R + ch * 16 + col;
+        cp_async_16_zfill(base + dst0 + i * C::GW * 512, src, pr >= 0 ? 16u : 0u);
       }
       cp_async_arrive_noinc(bar);
     };
@@ -435,9 +454,11 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
     }
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
-      if (k > 0) acquire();
-      if (!ok) continue;
-      copy(kv0 + slot * kBlock, k * 128, smem_u32(&ms.full[slot]));
+      if (turn == group) {
+        if (k > 0) acquire();
+        if (ok) copy(kv0 + slot * kBlock, k * 128, smem_u32(&ms.full[slot]));
+      }
+      turn = turn + 1 == C::GROUPS ? 0 : turn + 1;
       if (++slot == C::NS) {
         slot = 0;
         phase ^= 1;
@@ -1108,7 +1129,7 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(smem_u32(&ms.full[s]), kTma ? 1 : kProdThreads);
+      mbar_init(smem_u32(&ms.full[s]), kTma ? 1 : 32 * C::GW);
       mbar_init(smem_u32(&ms.empty[s]), 1);
     }
     for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), 1 + (C::kScaled && !kTma ? kProdThreads : 0));
@@ -1121,7 +1142,7 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
       mbar_init(smem_u32(&ms.p_free[s]), 1);
       mbar_init(smem_u32(&ms.final[s]), 1);
     }
-    mbar_init(smem_u32(&ms.rope_full), kTma ? 1 : kProdThreads);
+    mbar_init(smem_u32(&ms.rope_full), kTma ? 1 : 32 * C::GW);
     mbar_init(smem_u32(&ms.rope_empty), 1);
     mbar_init(smem_u32(&ms.q_full), kSmxWarps);
     ms.abort = 0;
@@ -1244,11 +1265,12 @@ int chunk_columns(int T, int H, int B) {
 
 bool launch_chunk_attn(const ChunkWork& work, cudaStream_t stream) {
   ChunkWork w = work;
-  // the largest power of two that divides the page and the tile: a box
+  // the largest power of two that divides the page and the tile: a box (rows
+  // one by one where that is below 32, see above)
   const int page = w.a.page_size;
   int shift = 0;
   while (shift < 7 && page % (2 << shift) == 0) ++shift;
-  w.box_shift = shift >= 4 ? shift : 0;
+  w.box_shift = shift >= 5 ? shift : 0;
   w.unit_cost = chunk_unit_cost(w.a.layout, w.box_shift);
   ChunkMaps maps{};
   if (w.box_shift > 0) {

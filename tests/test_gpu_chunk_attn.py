@@ -210,16 +210,17 @@ def test_overlapping_ranges_do_no_harm():
     assert err == 16 and (o == 7.0).all() and (lse == 7.0).all()
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 96, 256])
 @pytest.mark.parametrize("layout", LAYOUTS)
-def test_both_row_loads_agree(layout):
-    """Pages of 16 rows and more come by TMA, others row by row: the same bits."""
-    a = make([1, 40, 3], [300, 77, 130], 16, layout, page=16, seed=28)
+def test_both_row_loads_agree(layout, page):
+    """Pages of a multiple of 32 rows come by TMA, others row by row: the same bits."""
+    a = make([1, 40, 3], [300, 77, 130], 16, layout, page=page, seed=28)
     want = run(a)
     # the same rows as pages of one row
-    table = torch.full((3, a["table"].shape[1] * 16), -1, dtype=torch.int32)
+    table = torch.full((3, a["table"].shape[1] * page), -1, dtype=torch.int32)
     for b in range(3):
         j = torch.arange(int(a["kv"][b]))
-        table[b, :j.numel()] = (a["table"][b].long()[j // 16] * 16 + j % 16).to(torch.int32)
+        table[b, :j.numel()] = (a["table"][b].long()[j // page] * page + j % page).to(torch.int32)
     got = run(dict(a, table=table, page=1))
     assert got[2] == want[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
@@ -274,6 +275,38 @@ def test_queries_before_the_first_key(layout):
     """More new tokens than the request holds: the first see nothing."""
     w = make([10, 3, 1], [0, 0, 200], 8, layout, seed=11)
     w["kv"][0], w["kv"][1] = 4, 0
+    check(w)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("page,rows", [(64, 5), (64, 100), (256, 300), (16, 37), (7, 30)])
+def test_pool_that_ends_inside_a_page(layout, page, rows):
+    """Keys inside the pool's last, partial page count; those behind the pool's end are masked and reported."""
+    w = make([1, 20], [rows - 1, 0], 16, layout, page=page, seed=32)
+    w["pool"] = w["pool"][:rows].contiguous()
+    ids = torch.arange(ref.pages_of(rows, page), dtype=torch.int32)
+    w["table"] = ids.repeat(2, 1).contiguous()
+    w["kv"] = torch.tensor([rows, min(rows, 20)], dtype=torch.int32)
+    check(w)
+    if rows % page:
+        w["kv"][0] = min(rows + 1, ids.numel() * page)
+        check(w, err_want=2)
+
+
+@pytest.mark.parametrize("T,B", [(17, 1), (33, 2), (31, 16), (64, 4)])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_rows_around_a_group(layout, T, B):
+    """One head: query rows around the sizes of a group, more and fewer than an average request has."""
+    r = random.Random(T)
+    cut = sorted(r.sample(range(1, T), B - 1)) if B > 1 else []
+    new = [b - a for a, b in zip([0] + cut, cut + [T])]
+    check(make(new, [r.randint(0, 200) for _ in new], 1, layout, page=8, seed=33))
+
+
+def test_most_requests():
+    """DSA_MAX_REQUESTS requests of a token each."""
+    B = 16384
+    w = make([1] * B, [0] * B, 1, "raw512", page=1, seed=34)
     check(w)
 
 
