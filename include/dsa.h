@@ -63,7 +63,7 @@ enum {
   DSA_ERR_LAYOUT = 3,    /* unknown layout, or a layout this entry point refuses */
   DSA_ERR_ROW_WIDTH = 4, /* query width or KV row width is not 512 [P1 Modifications] */
   DSA_ERR_TOPK_PAD = 5,  /* top-k width is not a positive multiple of 128 [P3 Modifications] */
-  DSA_ERR_HEADS = 6,     /* head count not in {8, 16, 32, 64, 128} */
+  DSA_ERR_HEADS = 6,     /* head count not in {8, 16, 32, 64, 128} (dsa_chunk_attn: not in 1 to 1024) */
   DSA_ERR_WORKSPACE = 7, /* workspace missing or smaller than dsa_sparse_attn_workspace_bytes */
   DSA_ERR_DEVICE = 8,    /* no current CUDA device of compute capability 10.3 */
   DSA_ERR_CUDA = 9,      /* a kernel launch failed */
@@ -87,7 +87,7 @@ enum {
 const char* dsa_status_string(int status);
 
 /* Diagnostics: sets the limit, in nanoseconds, of every bounded wait inside
- * the attention kernel (default 1 s) for the attention calls made after it,
+ * the attention kernels (default 1 s) for the attention calls made after it,
  * process-wide, and returns the previous limit.  A wait that runs out makes
  * the kernel give up: its other waits return at once, it waits (with a
  * separate 2 s bound) for its own copies and tensor-core operations in
@@ -330,12 +330,12 @@ int dsa_sparse_attn_decode_noalloc(const void* q_bf16_dev, int T, int H, int D,
  * the row entry of a partly filled page) sets DSA_DEV_ERR_PAGE_RANGE and
  * gives its tokens slot -1.
  *   seq_lens_dev, new_lens_dev  [B] int32; B >= 1, at most DSA_MAX_REQUESTS.
- *   page_table_dev      [B, max_pages] int32; new pages are stored, other
- *                       entries are left as they are.
- *   free_pages_dev      [free_cap] int32, read.
+ *   page_table_dev      [B, max_pages] int32, max_pages * page_size < 2^31; new pages
+ *                       are stored, other entries are left as they are.
+ *   free_pages_dev      [free_cap] int32, read; free_cap >= 1.
  *   free_count_dev      int32, read; free_count_out_dev int32, written; they
  *                       may be one address (the update of a captured step).
- *   slots_dev           [T] int64;  positions_dev, token_seq_dev [T] int32.
+ *   slots_dev           [T] int64;  positions_dev, token_seq_dev [T] int32; T >= 1.
  *   cu_q_dev            [B + 1] int32.
  *   kv_lens_dev         [B] int32; may be seq_lens_dev.
  * Buffers named otherwise do not overlap. */
@@ -439,7 +439,17 @@ size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
  * lies beyond the pool is masked (DSA_DEV_ERR_PAGE_RANGE).  A request whose
  * [cu_q[b], cu_q[b + 1]) is not an ascending range within [0, T] is skipped, a
  * kv_lens[b] below 0 counts as 0 and one above max_pages * page_size as that
- * (DSA_DEV_ERR_LENGTH).  Ranges of requests do not overlap.
+ * (DSA_DEV_ERR_LENGTH).  Ranges of requests do not overlap: rows that two of
+ * them claim get the result of either, or a mixture.
+ * Precision.  Sums, softmax statistics and outputs are FP32, O is rounded to
+ * BF16 once.  Queries (times a power of two for each row) and softmax weights
+ * enter the products as two E4M3 terms each: a query's entries exactly where
+ * they are within 2^14 of its row's largest, RoPE dims as BF16; weights to 8
+ * significant bits, and 2^-14 of the largest weight below that.  RoPE dims of
+ * a query are meant to lie below 2^63, and scales to be at least 2^-60 (of a
+ * row whose scales are all smaller, less is kept).  A row with an infinite or
+ * NaN scale, or a query with a NaN or an infinity, scores NaN: the results
+ * that see it are NaN, no others.  Equal calls give equal bits.
  *   q_bf16_dev      [T, H, 512] BF16, [T, H, 576] over 656-byte rows; 16-byte aligned.
  *   H               1 to 1024; T * H < 2^30.
  *   page_table_dev  [B, max_pages] int32.

@@ -167,7 +167,7 @@ const char* dsa_status_string(int status) {
     case DSA_ERR_LAYOUT: return "DSA_ERR_LAYOUT: unsupported KV layout for this entry point";
     case DSA_ERR_ROW_WIDTH: return "DSA_ERR_ROW_WIDTH: query and KV row width must be 512";
     case DSA_ERR_TOPK_PAD: return "DSA_ERR_TOPK_PAD: top-k width must be a positive multiple of 128";
-    case DSA_ERR_HEADS: return "DSA_ERR_HEADS: head count must be 8, 16, 32, 64 or 128";
+    case DSA_ERR_HEADS: return "DSA_ERR_HEADS: head count must be 8, 16, 32, 64 or 128 (dsa_chunk_attn: 1 to 1024)";
     case DSA_ERR_WORKSPACE: return "DSA_ERR_WORKSPACE: workspace missing or too small";
     case DSA_ERR_DEVICE: return "DSA_ERR_DEVICE: current device is not a compute capability 10.3 GPU";
     case DSA_ERR_CUDA: return "DSA_ERR_CUDA: kernel launch failed";
