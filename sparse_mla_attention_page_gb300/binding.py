@@ -464,7 +464,7 @@ def dsa_chunk_attn_workspace_bytes(T: int, H: int, B: int, layout) -> int:
 
 
 def chunk_workspace_for(T: int, H: int, B: int, layout, device=None) -> torch.Tensor:
-    """A device workspace for dsa_chunk_attn of up to T tokens of B requests."""
+    """A device workspace for dsa_chunk_attn of up to T tokens of up to B requests, with up to H heads."""
     return torch.empty(dsa_chunk_attn_workspace_bytes(T, H, B, layout), dtype=torch.uint8, device=device or "cuda")
 
 

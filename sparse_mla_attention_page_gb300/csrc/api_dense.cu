@@ -37,20 +37,24 @@ bool table_ok(int B, int max_pages, int page_size) {
 }
 
 // Where the parts of the attention's workspace begin (pointers from base on).
+// Its size grows with T, H and B alone, not with the rows of a unit that they
+// lead to, so that it serves every smaller call too.
 size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, char* base) {
   w.nc = dsa::chunk_columns(T, H, B);
   w.max_units = (int64_t)T * H / w.nc + B;     // full units, and the last of each request
   w.grid = sms;
+  const size_t units = (size_t)((int64_t)T * H / dsa::kFewestRows + B);
+  const size_t rows = (size_t)sms * 2 * dsa::chunk_columns(T, H, 1);
   size_t end = 0;
   auto take = [&](size_t bytes) {
     char* p = base + end;
     end += (bytes + 255) / 256 * 256;
     return p;
   };
-  w.units = reinterpret_cast<dsa::ChunkUnit*>(take((size_t)(w.max_units + 1) * sizeof(dsa::ChunkUnit)));
+  w.units = reinterpret_cast<dsa::ChunkUnit*>(take((units + 1) * sizeof(dsa::ChunkUnit)));
   w.splits = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
-  w.part_lse = reinterpret_cast<float*>(take((size_t)sms * 2 * w.nc * sizeof(float)));
-  w.part_o = reinterpret_cast<float*>(take((size_t)sms * 2 * w.nc * 512 * sizeof(float)));
+  w.part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
+  w.part_o = reinterpret_cast<float*>(take(rows * 512 * sizeof(float)));
   return end;
 }
 

@@ -86,8 +86,8 @@ struct ChunkArgs {
   float* lse;
   int32_t* err;
 };
-// Query rows of a unit of the work list: the widest that an average request
-// fills.
+// Query rows of a unit of the work list, 16 or 32.
+constexpr int kFewestRows = 16;
 int chunk_columns(int T, int H, int B);
 struct ChunkWork;      // chunk.cuh
 bool launch_chunk_attn(const ChunkWork& w, cudaStream_t stream);

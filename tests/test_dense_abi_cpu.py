@@ -101,6 +101,16 @@ def test_chunk_workspace(L):
         assert f(*bad) == 0
 
 
+def test_chunk_workspace_serves_smaller_calls(L):
+    """A call with no more tokens, heads and requests needs no more, also where its query rows group differently."""
+    sizes = [(T, H, B) for T in (1, 5, 17, 64, 300, 8192) for H in (1, 16, 128) for B in (1, 7, 64, 500)]
+    need = {s: L.dsa_chunk_attn_workspace_bytes(*s, 2) for s in sizes}
+    for s in sizes:
+        for t in sizes:
+            if all(x <= y for x, y in zip(s, t)):
+                assert need[s] <= need[t], (s, t)
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="needs a machine without a GPU")
 def test_good_arguments_without_a_gpu(L):
     """Valid arguments get as far as the device check."""
