@@ -352,9 +352,11 @@ def _refuse(t, name, dtype, shape, device, strided):
 
 def _arg(t, name: str, dtype: torch.dtype, shape, device: int):
     """Address of a contiguous tensor of the given type and shape (None: any) on the call's device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == device and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:       # not a tensor
+        pass
     _refuse(t, name, dtype, shape, device, False)
 
 
@@ -362,9 +364,11 @@ def _arg_strided(t, name: str, dtype: torch.dtype, shape, device: int):
     """The same for a tensor that is contiguous in its last dim only; None stays None."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
-            and (t.stride(-1) == 1 or t.shape[-1] == 1)):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.shape == shape and (t.stride(-1) == 1 or t.shape[-1] == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _refuse(t, name, dtype, shape, device, True)
 
 
@@ -374,14 +378,15 @@ def _flag(t, device: int):
 
 def _dims(t, name: str, n: int):
     """The shape of a tensor of n dims."""
-    if not isinstance(t, torch.Tensor) or t.dim() != n:
+    s = getattr(t, "shape", ())
+    if len(s) != n:
         raise ValueError(f"{name} must be a tensor of {n} dims")
-    return t.shape
+    return s
 
 
 def _call_device(stream):
     """(the current device, the stream's address on it)."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
