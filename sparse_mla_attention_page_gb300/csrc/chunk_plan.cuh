@@ -67,6 +67,14 @@ struct ChunkRange {
   int unit;          // that the first one belongs to
 };
 
+// Few short units, a CTA each: taken where no unit has more tiles than a CTA
+// would get of split ones and this many.  us with / without, two tiles more:
+// 2 x 20 tokens of 32 heads over 300, raw 13.4 / 18.3, rope 17.7 / 21.4; 30
+// single tokens over up to 300, raw 12.1 / 13.5; 300 tokens of 8 heads, raw
+// 13.5 / 18.9; three tiles more (16 single tokens over up to 500): raw 13.0 /
+// 12.2, rope 15.6 / 14.5.
+constexpr int kWholeTiles = 2;
+
 constexpr int kPlanScratch = DSA_MAX_REQUESTS * 4 + 256;   // bytes of shared memory
 
 // By all THREADS threads; mine and start (the range's first unit) lie in
@@ -129,6 +137,23 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   });
   int64_t n_tiles;
   int64_t tile0 = block_scan<THREADS>(tiles, &n_tiles, sums);
+  if (n_units <= min(w.grid, THREADS)) {
+    const int fair = (int)((n_tiles + w.grid - 1) / w.grid);       // tiles of a CTA where units are split
+    if (!__syncthreads_or(u1 > u0 && only.tiles > fair + kWholeTiles)) {
+      if (tid == 0) {
+        w.splits[cta].parts = 0;
+        if (cta >= n_units) mine.t0 = mine.t1 = 0;
+      }
+      if (u1 > u0 && u0 == cta) {
+        start = only;
+        start.tile0 = tile0;
+        mine.unit = u0;
+        mine.t0 = tile0;
+        mine.t1 = tile0 + only.tiles;
+      }
+      return;
+    }
+  }
   // cost: position v of the list, of length V, is tile (v - body) / kTileCost of
   // the unit whose tiles begin at body, or its first; CTA c begins at floor(c V / grid)
   const int64_t V = n_tiles * kTileCost + (int64_t)n_units * w.unit_cost;

@@ -303,6 +303,16 @@ def test_rows_around_a_group(layout, T, B):
     check(make(new, [r.randint(0, 200) for _ in new], 1, layout, page=8, seed=33))
 
 
+@pytest.mark.parametrize("tiles", [1, 3, 4])
+@pytest.mark.parametrize("B", [3, 150, 154])
+def test_groups_of_few_tiles(B, tiles):
+    """Row groups of so many 128-key tiles each: whole to an SM, or spread, on either side of the number of SMs."""
+    r = random.Random(35)
+    kv = [128 * tiles - r.randint(0, 1) * r.randint(0, 127) for _ in range(B)]
+    kv[0] = 128 * tiles
+    check(make([1] * B, [k - 1 for k in kv], 4, "rope656", page=32, seed=35))
+
+
 def test_most_requests():
     """DSA_MAX_REQUESTS requests of a token each."""
     B = 16384
