@@ -21,7 +21,12 @@
 // to 8 significant bits (as BF16 weights would have).  The terms are columns of
 // their own in both products, so a tile is read once for both.  p of the key
 // that sets the running maximum is 1 and may grow to 2^8.75 before the maximum
-// moves (E4M3 ends at 448); lo then still resolves 2^-14.
+// moves (E4M3 ends at 448); lo then still resolves 2^-14.  (With the maximum at
+// 2^4 lo needs no factor of its own, but M moves three times as often where
+// rows differ in size, and each move waits for the value products: 4096 tokens
+// over 8192 scaled rows took 3901 us against 3690.)  A thread's hi and lo
+// weights lie side by side, one store for both (1 % faster); its scores do
+// not, as one load of both spills registers.
 //
 // Group scales (528- and 656-byte rows): one pass of the score product for
 // each 128-dim group, multiplied by the row's scale as it is read out, and one
@@ -249,13 +254,14 @@ __device__ __forceinline__ void split2(uint32_t p, uint32_t& hi2, uint32_t& lo2)
   lo2 = h;
 }
 
-// N bytes (4 or 8) held as pairs, to shared memory.
+// 2 N bytes (N = 4 or 8: both terms), held as pairs, to shared memory.
 template <int N>
-__device__ __forceinline__ void st_bytes(uint32_t addr, const uint32_t (&t)[N / 2]) {
+__device__ __forceinline__ void st_bytes(uint32_t addr, const uint32_t (&hi)[N / 2], const uint32_t (&lo)[N / 2]) {
   if constexpr (N == 8)
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(t[0] | t[1] << 16), "r"(t[2] | t[3] << 16) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16),
+                 "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
   else
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(t[0] | t[1] << 16) : "memory");
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(hi[0] | hi[1] << 16), "r"(lo[0] | lo[1] << 16) : "memory");
 }
 
 // Two floats in one 64-bit register: half the instructions.
@@ -984,7 +990,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
             const float bg = g == 0 ? beta[0] : g == 1 ? beta[1] : g == 2 ? beta[2] : beta[3];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {                // hi, lo
-              const uint32_t at = lane_base + C::O_COL0 + g * C::NQ + t * NC;
+              const uint32_t at = lane_base + c0 + C::O_COL0 + g * C::NQ + t * CPT;
               uint32_t v[CPT];
               tmem_ld<CPT>(at, v);
               tmem_wait_ld();
@@ -1033,8 +1039,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       }
       if (g == 0 && it >= C::NPB)
         pv_wait(it - C::NPB);
-      st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(c0, row), hi2);
-      st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(NC + c0, row), lo2);
+      st_bytes<CPT>(at + g * C::P_GROUP + p_off<C::NQ>(2 * c0, row), hi2, lo2);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -1073,8 +1078,8 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     // block db's outputs of this thread's columns, normalised
     auto read_block = [&](int db, float (&y)[CPT]) {
       uint32_t v[CPT], lo[CPT];
-      tmem_ld<CPT>(lane_base + C::O_COL0 + db * C::NQ, v);
-      tmem_ld<CPT>(lane_base + C::O_COL0 + db * C::NQ + NC, lo);
+      tmem_ld<CPT>(lane_base + c0 + C::O_COL0 + db * C::NQ, v);
+      tmem_ld<CPT>(lane_base + c0 + C::O_COL0 + db * C::NQ + CPT, lo);
       tmem_wait_ld();
       const float unlift = C::kScaled ? __int_as_float((254 << 23) - __float_as_int(cg[db])) : 1.f;   // 1 / c_g
 #pragma unroll
