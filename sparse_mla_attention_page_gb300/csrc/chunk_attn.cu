@@ -988,16 +988,18 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {
             const float bg = g == 0 ? beta[0] : g == 1 ? beta[1] : g == 2 ? beta[2] : beta[3];
+            const uint32_t at = lane_base + c0 + C::O_COL0 + g * C::NQ;
+            uint32_t v[CPT], lo[CPT];                    // hi, lo
+            tmem_ld<CPT>(at, v);
+            tmem_ld<CPT>(at + CPT, lo);
+            tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {                // hi, lo
-              const uint32_t at = lane_base + c0 + C::O_COL0 + g * C::NQ + t * CPT;
-              uint32_t v[CPT];
-              tmem_ld<CPT>(at, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < CPT; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * (al[k] * bg));
-              tmem_st<CPT>(at, v);
+            for (int k = 0; k < CPT; ++k) {
+              v[k] = __float_as_uint(__uint_as_float(v[k]) * (al[k] * bg));
+              lo[k] = __float_as_uint(__uint_as_float(lo[k]) * (al[k] * bg));
             }
+            tmem_st<CPT>(at, v);
+            tmem_st<CPT>(at + CPT, lo);
           }
           tmem_wait_st();
         }
