@@ -911,8 +911,9 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       for (int k = 0; k < CPT; ++k)
         if (!valid || j >= vis[k]) x[k] = -INFINITY;
     }
-    // Does a column's running maximum have to move, or a c_g?  (Each column by
-    // itself: a row's bits do not depend on the rows it shares a unit with.)  One barrier of
+    // Does a column's running maximum have to move, or a c_g?  (A maximum moves
+    // for its own column only, so that a row's rounding does not hang on its
+    // neighbours'.)  One barrier of
     // the column quarter's warps ORs the threads' answers; only then are the
     // tile's maxima formed.
     float top = x[0];
