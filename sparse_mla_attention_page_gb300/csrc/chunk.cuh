@@ -7,8 +7,9 @@
 // key that its last row sees.  The units' tiles, one after another, are the
 // global tile list; CTA c of the persistent grid owns a range of it, so a unit
 // may be spread over CTAs.  The ranges are cut evenly by cost: a unit counts
-// chunk_unit_cost more than its tiles, for its query operand and its output.  Lengths live on the GPU: every CTA of
-// the attention kernel forms the list's prefix sums for itself.
+// chunk_unit_cost more than its tiles, for its query operand and its output.
+// Lengths live on the GPU: every CTA of the attention kernel forms the list's
+// prefix sums for itself.
 #pragma once
 #include <cstdint>
 
