@@ -421,16 +421,19 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
         cp_async_16_zfill(smem_u32(sm + C::SC_OFF + (m * kTile + ptid) * 16),
                           a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kD, row >= 0 ? 16u : 0u);
     }
-    if (C::kScaled) cp_async_arrive_noinc(smem_u32(&ms.meta_full[m]));
+    // A warp whose wait gave up publishes nothing more: units, and tiles, whose
+    // place in the ring may still be in use (without its arrival the tile's
+    // barrier stays open, and the ring ends before that barrier comes round).
+    if (C::kScaled && ok) cp_async_arrive_noinc(smem_u32(&ms.meta_full[m]));
     if (opens) {       // (the first unit is the plan's)
-      if (seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
+      if (ok && seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
       ++seg;
     }
     const bool opened = opens;
     opens = cur.advance(w, ptid);
     if (it + 1 < rg.n_it) look_up();
     const bool whole = named_bar_red_or(kProdBar, kProdThreads, ptid < kTile && row_here < 0) == 0;
-    if (ptid == 0) {
+    if (ptid == 0 && ok) {
       ms.clean[m] = whole;
       mbar_arrive(smem_u32(&ms.meta_full[m]));
       if (opened && seg > 1) prefetch_queries(a, ms.unit[(seg - 1) % kSegs]);
@@ -804,7 +807,11 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
   // rows of the pool behind which this thread's key of a box would lie outside
   const int in_box = kTma ? row & ((1 << w.box_shift) - 1) : 0;
   const uint32_t row_limit = (uint32_t)max((int64_t)0, a.pool_rows - in_box);
-  bool ok = true;                                        // false once a wait gave up: keep going through every barrier
+  // False once one of this thread's waits gave up.  While it is true, whatever
+  // the waits guard is in place: units are used, and queries read, behind it
+  // alone.  The threads of a column quarter leave together, in the tile in which
+  // one of them finds it false (they share named barriers).
+  bool ok = true;
   // PV of tile i; every tile's is waited for (NPB tiles on at the latest), so the parity tells them apart
   auto pv_wait = [&](int i) { ok &= mbar_wait(smem_u32(&ms.p_free[i % C::NPB]), (i / C::NPB) & 1, abort, w.wait_ns); };
   Segment sg;
@@ -919,7 +926,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     float top = x[0];
 #pragma unroll
     for (int k = 1; k < CPT; ++k) top = fmaxf(top, x[k]);
-    bool grow = pending || top > kTop;
+    bool grow = pending || top > kTop || !ok;
     // P's factors s_g / S c_g, at most 1 (what lies there for a row that nobody
     // sees, or for one that scores NaN, is cut to finite values: p is 0, or NaN)
     float f[C::G];
@@ -945,7 +952,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
         const float wsc = transpose_reduce<4, true>(t4, lane);
         if (lane < 4) ms.red_sc[cq][quarter][lane] = wsc;
       }
-      named_bar_sync(bar, 128);
+      if (named_bar_red_or(bar, 128, !ok)) break;
       const int cl = lane % CPT;
       const float tmax = fmaxf(fmaxf(ms.red[cq][0][cl], ms.red[cq][1][cl]), fmaxf(ms.red[cq][2][cl], ms.red[cq][3][cl]));
       const bool need = has ? tmax > kTop : tmax > -INFINITY;
@@ -1056,7 +1063,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     // every score pass of this tile is done, so the query operand may be replaced
     if (it + 1 < rg.n_it) {
       ok &= mbar_wait(smem_u32(&ms.meta_full[(it + 1) % kMeta]), ((it + 1) / kMeta) & 1, abort, w.wait_ns);
-      build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[(sg.seg + 1) % kSegs], par ^ 1);
+      if (__all_sync(0xffffffffu, ok)) build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[(sg.seg + 1) % kSegs], par ^ 1);
     }
     // the segment's end: denominators, O, LSE
     float lsum[CPT];
@@ -1075,7 +1082,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     tc_fence_after();
     const bool whole = u.tile0 >= rg.t0 && u.tile0 + u.tiles <= rg.t0 + rg.n_it;
     const int64_t part = ((int64_t)blockIdx.x * 2 + (rg.t0 >= u.tile0 ? 0 : 1)) * NC;
-    const int cols = u.cols - c0;                        // of this thread's columns
+    const int cols = ok ? u.cols - c0 : 0;               // of this thread's columns, those to be stored
     const int64_t row0 = u.row0;
     float li[CPT];
     ld_row<CPT>(&ms.by[c0], li);
@@ -1116,7 +1123,6 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       else w.part_lse[part + c0 + lane] = ms.alpha[c0 + lane];
     }
   }
-  (void)ok;
 }
 
 template <int kRegs>

@@ -479,3 +479,35 @@ def test_agrees_with_the_sparse_kernel():
                                    token_seq=torch.arange(4, dtype=torch.int32).cuda())
     assert (so.cpu().float() - o.float()).abs().max() < 2.0 ** -6 * o.float().abs().max()
     assert (sl.cpu() - lse).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("page", [64, 16])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_wait_that_runs_out_between_units(layout, page):
+    """Waits that run out while every SM works through several requests' row groups: nothing is written outside the
+    requests' rows and the workspace, a call whose flag is clear is right, and the next call is."""
+    r = random.Random(36)
+    w = make([r.randint(10, 80) for _ in range(24)], [r.randint(0, 400) for _ in range(24)], 16, layout, page=page,
+             seed=36, lead=5, tail=7)
+    T, H, _ = w["q"].shape
+    n = binding.dsa_chunk_attn_workspace_bytes(T, H, 24, layout)
+    room = torch.empty(n + 2 * 65536, dtype=torch.uint8, device="cuda")
+    ws, guards = room[65536:65536 + n], (room[:65536], room[65536 + n:])
+    want = run(w, ws=ws)
+    assert want[2] == 0
+    mine = torch.zeros(T, dtype=torch.bool)
+    mine[5:T - 7] = True
+    for limit in (0, 300, 1000, 3000, 10000, 30000):
+        for g in guards:
+            g.fill_(0xA5)
+        old = binding.dsa_set_wait_limit_ns(limit)
+        try:
+            o, lse, err = run(w, ws=ws)
+        finally:
+            binding.dsa_set_wait_limit_ns(old)
+        assert err in (0, binding.DSA_DEV_ERR_TIMEOUT) and (limit or err)
+        assert (o[~mine] == 7.0).all() and (lse[~mine] == 7.0).all() and all(bool((g == 0xA5).all()) for g in guards)
+        if err == 0:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        o, lse, err = run(w, ws=ws)
+        assert err == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
