@@ -513,7 +513,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
     }
   };
   look_up();
-  int slot = 0, phase = 0, seg = 0, issued = 0, metas = 0;
+  int slot = 0, phase = 0, seg = 0, issued = 0, metas = 0, ropes = 0;   // (blocks, tiles' rows and RoPE blocks requested)
   bool ok = true, opens = true;
   for (int it = 0; it < rg.n_it && ok; ++it) {
     const int m = it % kMeta;
@@ -532,6 +532,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
       if (lane == 0) mbar_arrive_tx(smem_u32(&ms.rope_full), n * 128);
       __syncwarp();
       if (row >= 0) tma_load(kv0 + C::ROPE_OFF, &maps.rows, kScaledRow, row, smem_u32(&ms.rope_full));
+      ++ropes;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -578,7 +579,7 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
     slot = slot == 0 ? C::NS - 1 : slot - 1;
     mbar_wait(smem_u32(&ms.full[slot]), phase, &no_abort, 2000000000ull);
   }
-  if (C::kRope && metas > 0) mbar_wait(smem_u32(&ms.rope_full), (metas - 1) & 1, &no_abort, 2000000000ull);
+  if (C::kRope && ropes > 0) mbar_wait(smem_u32(&ms.rope_full), (ropes - 1) & 1, &no_abort, 2000000000ull);
   if (C::kScaled)
     for (int i = max(0, metas - kMeta); i < metas; ++i)
       mbar_wait(smem_u32(&ms.meta_full[i % kMeta]), (i / kMeta) & 1, &no_abort, 2000000000ull);

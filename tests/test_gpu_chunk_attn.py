@@ -511,3 +511,27 @@ def test_wait_that_runs_out_between_units(layout, page):
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         o, lse, err = run(w, ws=ws)
         assert err == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_call_right_behind_one_that_gave_up():
+    """A call that gave up leaves no copy of its own in flight: calls queued directly behind it, which take over its
+    shared memory, are right."""
+    w = make([30, 1, 50, 9] * 6, [300, 700, 20, 130] * 6, 16, "rope656", seed=37)
+    want = run(w)
+    T, H, _ = w["q"].shape
+    d = {k: v.cuda() for k, v in w.items() if isinstance(v, torch.Tensor)}
+    ws = binding.chunk_workspace_for(T, H, 24, "rope656")
+    errs = torch.zeros(12, dtype=torch.int32, device="cuda")
+    outs = [(torch.zeros(T, H, 512, dtype=BF, device="cuda"), torch.zeros(T, H, device="cuda")) for _ in range(12)]
+    limit = binding.dsa_set_wait_limit_ns(0)
+    try:
+        for i, (o, lse) in enumerate(outs):
+            binding.dsa_set_wait_limit_ns(limit if i % 2 else (0, 500, 2000)[i // 2 % 3])
+            binding.dsa_chunk_attn(d["q"], d["pool"], "rope656", d["table"], 64, d["cu"], d["kv"], SCALE, o, lse, ws,
+                                   err_flag=errs[i:i + 1])
+    finally:
+        binding.dsa_set_wait_limit_ns(limit)
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(outs):
+        if i % 2:
+            assert int(errs[i]) == 0 and torch.equal(o.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
