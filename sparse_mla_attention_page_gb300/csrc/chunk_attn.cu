@@ -421,9 +421,9 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
         cp_async_16_zfill(smem_u32(sm + C::SC_OFF + (m * kTile + ptid) * 16),
                           a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kD, row >= 0 ? 16u : 0u);
     }
-    // A warp whose wait gave up publishes nothing more: units, and tiles, whose
-    // place in the ring may still be in use (without its arrival the tile's
-    // barrier stays open, and the ring ends before that barrier comes round).
+    // Once a wait has given up no unit is published: the softmax warps then run on,
+    // so that a free slot no longer tells that the units before are done with.
+    if (opens && seg > 0) ok = __all_sync(0xffffffffu, ok && *abort == 0);
     if (C::kScaled && ok) cp_async_arrive_noinc(smem_u32(&ms.meta_full[m]));
     if (opens) {       // (the first unit is the plan's)
       if (ok && seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
@@ -547,6 +547,9 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
         phase ^= 1;
       }
       if (k == 0) {        // (the slot is free, so the tile kMeta before is out of the way)
+        // no unit is published once a wait has given up (as in producer_role)
+        if (opens && seg > 0) ok = __all_sync(0xffffffffu, *abort == 0);
+        if (!ok) break;
         ++metas;
         if (mine) ms.rows[m][lane] = row;
         if (lane == 0) ms.clean[m] = whole;
@@ -697,14 +700,16 @@ __device__ void pv_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem
 
 // The query operand of one segment, and its columns' factors, visible keys and
 // maxima.  512 threads: column tid / TPH, dims [DPT (tid % TPH), + DPT).
+// there: the unit was published (false: of a call that gave up, whose queries
+// are not read).
 template <int NC, int kLayout, bool kTma>
-__device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Misc& ms, const ChunkUnit& u, int par) {
+__device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Misc& ms, const ChunkUnit& u, bool there, int par) {
   using C = Cfg<NC, kLayout, kTma>;
   constexpr int TPH = kSmxThreads / NC, DPT = kD / TPH, NV = DPT / 8;
   const ChunkArgs& a = w.a;
   const int col = threadIdx.x / TPH, part = threadIdx.x % TPH;
   const uint16_t* src = a.q + (u.row0 + col) * a.q_row;
-  const bool live_col = col < u.cols;
+  const bool live_col = there && col < u.cols;
   uint4 v[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -808,21 +813,16 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
   // rows of the pool behind which this thread's key of a box would lie outside
   const int in_box = kTma ? row & ((1 << w.box_shift) - 1) : 0;
   const uint32_t row_limit = (uint32_t)max((int64_t)0, a.pool_rows - in_box);
-  // False once one of this thread's waits gave up.  While it is true, whatever
-  // the waits guard is in place: units are used, and queries read, behind it
-  // alone.  The threads of a column quarter leave together, in the tile in which
-  // one of them finds it false (they share named barriers).
-  bool ok = true;
   // PV of tile i; every tile's is waited for (NPB tiles on at the latest), so the parity tells them apart
-  auto pv_wait = [&](int i) { ok &= mbar_wait(smem_u32(&ms.p_free[i % C::NPB]), (i / C::NPB) & 1, abort, w.wait_ns); };
+  auto pv_wait = [&](int i) { mbar_wait(smem_u32(&ms.p_free[i % C::NPB]), (i / C::NPB) & 1, abort, w.wait_ns); };
   Segment sg;
-  build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[0], 0);
+  build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[0], true, 0);
   for (int it = 0; it < rg.n_it; ++it) {
     const bool first = sg.starts();
     const int m = it % kMeta;
-    ok &= mbar_wait(smem_u32(&ms.meta_full[m]), (it / kMeta) & 1, abort, w.wait_ns);
+    mbar_wait(smem_u32(&ms.meta_full[m]), (it / kMeta) & 1, abort, w.wait_ns);
     if (first) {
-      ok &= mbar_wait(smem_u32(&ms.q_full), (sg.seg + 1) & 1, abort, w.wait_ns);
+      mbar_wait(smem_u32(&ms.q_full), (sg.seg + 1) & 1, abort, w.wait_ns);
       tile = sg.open(ms, rg.t0, it, rg.n_it);
       last = ms.unit[sg.seg % kSegs].last;
       full = ms.vis[sg.seg & 1][0] / kTile;
@@ -858,7 +858,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
 #pragma unroll
     for (int p = 0; p < C::NPASS; ++p) {
       if (p % C::PG == 0) {
-        ok &= mbar_wait(smem_u32(&ms.s_full[sb]), s_phase, abort, w.wait_ns);
+        mbar_wait(smem_u32(&ms.s_full[sb]), s_phase, abort, w.wait_ns);
         tc_fence_after();
       }
       const bool rope = C::kRope && p == 0;
@@ -927,7 +927,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     float top = x[0];
 #pragma unroll
     for (int k = 1; k < CPT; ++k) top = fmaxf(top, x[k]);
-    bool grow = pending || top > kTop || !ok;
+    bool grow = pending || top > kTop;
     // P's factors s_g / S c_g, at most 1 (what lies there for a row that nobody
     // sees, or for one that scores NaN, is cut to finite values: p is 0, or NaN)
     float f[C::G];
@@ -953,7 +953,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
         const float wsc = transpose_reduce<4, true>(t4, lane);
         if (lane < 4) ms.red_sc[cq][quarter][lane] = wsc;
       }
-      if (named_bar_red_or(bar, 128, !ok)) break;
+      named_bar_sync(bar, 128);
       const int cl = lane % CPT;
       const float tmax = fmaxf(fmaxf(ms.red[cq][0][cl], ms.red[cq][1][cl]), fmaxf(ms.red[cq][2][cl], ms.red[cq][3][cl]));
       const bool need = has ? tmax > kTop : tmax > -INFINITY;
@@ -1061,10 +1061,17 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     ++tile;
     if (sg.left > 0) continue;
     const ChunkUnit& u = ms.unit[sg.seg % kSegs];
-    // every score pass of this tile is done, so the query operand may be replaced
+    // Every score pass of this tile is done, so the query operand may be replaced.
+    // The next unit is there if no wait gave up so far: one that did leaves the
+    // flag set (its own result says less, as a barrier further on may be a whole
+    // number of phases behind).  Else the column quarter, whose threads share
+    // named barriers, leaves together.  (Each wait's result kept, or the quarter
+    // leaving from within the tile, take 2 to 6 % of the kernel's time.)
+    bool there = true;
     if (it + 1 < rg.n_it) {
-      ok &= mbar_wait(smem_u32(&ms.meta_full[(it + 1) % kMeta]), ((it + 1) / kMeta) & 1, abort, w.wait_ns);
-      if (__all_sync(0xffffffffu, ok)) build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[(sg.seg + 1) % kSegs], par ^ 1);
+      mbar_wait(smem_u32(&ms.meta_full[(it + 1) % kMeta]), ((it + 1) / kMeta) & 1, abort, w.wait_ns);
+      there = *abort == 0;
+      build_query<NC, kLayout, kTma>(w, sm, ms, ms.unit[(sg.seg + 1) % kSegs], there, par ^ 1);
     }
     // the segment's end: denominators, O, LSE
     float lsum[CPT];
@@ -1072,7 +1079,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     for (int k = 0; k < CP2; ++k) unpack2(l_part[k], lsum[2 * k], lsum[2 * k + 1]);
     const float wsum = transpose_reduce<CPT, false>(lsum, lane);
     if (lane < CPT) ms.red[cq][quarter][lane] = wsum;
-    named_bar_sync(bar, 128);
+    if (named_bar_red_or(bar, 128, !there)) break;
     if (quarter == 0 && lane < CPT) {
       const float l = (ms.red[cq][0][lane] + ms.red[cq][1][lane]) + (ms.red[cq][2][lane] + ms.red[cq][3][lane]);
       ms.by[c0 + lane] = l == 0.f ? 0.f : 1.f / l;
@@ -1083,7 +1090,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     tc_fence_after();
     const bool whole = u.tile0 >= rg.t0 && u.tile0 + u.tiles <= rg.t0 + rg.n_it;
     const int64_t part = ((int64_t)blockIdx.x * 2 + (rg.t0 >= u.tile0 ? 0 : 1)) * NC;
-    const int cols = ok ? u.cols - c0 : 0;               // of this thread's columns, those to be stored
+    const int cols = u.cols - c0;                        // of this thread's columns
     const int64_t row0 = u.row0;
     float li[CPT];
     ld_row<CPT>(&ms.by[c0], li);
