@@ -447,11 +447,15 @@ size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
  * BF16 once.  Queries (times a power of two for each row) and softmax weights
  * enter the products as two E4M3 terms each: a query's entries exactly where
  * they are within 2^14 of its row's largest, RoPE dims as BF16; weights to 8
- * significant bits, and 2^-14 of the largest weight below that.  RoPE dims of
- * a query are meant to lie below 2^63, and scales to be at least 2^-60 (of a
- * row whose scales are all smaller, less is kept).  A row with an infinite or
- * NaN scale, or a query with a NaN or an infinity, scores NaN: the results
- * that see it are NaN, no others.  Equal calls give equal bits.
+ * significant bits down to 2^-7 of the largest, below that to multiples of
+ * 2^-14 of it, up or down by the key's position, so that a long tail of small
+ * weights keeps its share of O: what this rounding leaves there is noise, in
+ * the RMS 0.6 % at most of the largest weight times the values, however many
+ * keys there are.  RoPE dims of a query are meant to lie below 2^63, and scales
+ * to be at least 2^-60 (of a row whose scales are all smaller, less is kept).
+ * A row with an infinite or NaN scale, or a query with a NaN or an infinity,
+ * scores NaN: the results that see it are NaN, no others.  Equal calls give
+ * equal bits.
  *   q_bf16_dev      [T, H, 512] BF16, [T, H, 576] over 656-byte rows; 16-byte aligned.
  *   H               1 to 1024; T * H < 2^30.
  *   page_table_dev  [B, max_pages] int32.

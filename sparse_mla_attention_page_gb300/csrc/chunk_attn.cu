@@ -17,22 +17,34 @@
 //
 // 16-bit data on 8-bit operands.  A BF16 query times a power of two for its row
 // splits into two E4M3 terms, q ~ hi + lo / 16, exactly where it is within
-// 2^14 of the row's largest entry; softmax weights likewise, p ~ hi + lo / 16,
-// to 8 significant bits (as BF16 weights would have).  The terms are columns of
-// their own in both products, so a tile is read once for both.  p of the key
-// that sets the running maximum is 1 and may grow to 2^8.75 before the maximum
-// moves (E4M3 ends at 448); lo then still resolves 2^-14.  (With the maximum at
-// 2^4 lo needs no factor of its own, but M moves three times as often where
-// rows differ in size, and each move waits for the value products: 4096 tokens
-// over 8192 scaled rows took 3901 us against 3690.)  A thread's hi and lo
-// weights lie side by side, one store for both (1 % faster); its scores do
-// not, as one load of both spills registers.
+// 2^14 of the row's largest entry; softmax weights likewise, p ~ hi + lo / 16.
+// The terms are columns of their own in both products, so a tile is read once
+// for both.  A thread's hi and lo weights lie side by side, one store for both
+// (1 % faster); its scores do not, as one load of both spills registers.
+//
+// Weights p = 2^(s - M) have 8 significant bits down to 2^-6 and lo's smallest
+// step, 2^-13, below.  l sums them unrounded, so what rounding takes from them
+// has to even out: a tail of keys below 2^-14 behind one that dominates (the
+// first of a context often does) would, rounded to nearest, leave O altogether
+// while l counts it (8192 keys 10 nats below one: 27 % of O; 93 % in the worst
+// of the tests).  So lo is rounded behind a shift within half a step that
+// differs from key to key (shift_of): as many weights go up as their size asks
+// for.  It joins the multiplication by 16 and costs nothing.  What is left is
+// noise: over the n tiles of a segment sqrt(128 n) 2^-14 at most, in the RMS, of
+// a weight 1.  A move therefore puts the tile's largest p at 2^lift, lift =
+// log2(n) / 2 - 2 for the n tiles to come, at least 1 (as a shift may cost a
+// whole step instead of half of one): 0.6 % of the largest weight at most,
+// however many keys there are.  p may then grow to 2^8.75 before M moves again (E4M3 ends at
+// 448).  A move waits for the value products, 0.9 of a tile's time, and they are
+// the more frequent the higher lift is where rows differ in size: 4096 tokens
+// over 8192 rows of 656 bytes take 4215 us with lift 0, 4490 with this one, and
+// 5540 with lift = log2(n), which keeps the loss of rounding to nearest below 1 %.
 //
 // Group scales (528- and 656-byte rows): one pass of the score product for
 // each 128-dim group, multiplied by the row's scale as it is read out, and one
 // P operand for each group against that group's block of values.  With S the
-// power of two above the row's largest scale, the running maximum M is kept of
-// s + log2 S, so that one exponential serves all four groups,
+// power of two above the row's largest scale, the reference M is one of s +
+// log2 S, so that one exponential serves all four groups,
 //   P_g = 2^(s + log2 S - M) (s_g / S) c_g,   l = sum 2^(s + log2 S - M) / S,
 // and c_g, a power of two for each group, lifts groups that are smaller than
 // their rows' largest throughout the segment.  (S and c_g are powers of two:
@@ -102,8 +114,8 @@ struct Misc {
   __align__(16) int32_t rows[kMeta][kTile];   // pool row of each key (TMA: of each box's first), -1: masked
   __align__(16) float sig[2][32];  // per segment parity: log2-domain factor of each query column
   __align__(16) int vis[2][32];    // keys that it sees
-  __align__(16) float nmax[2][32]; // minus its running maximum
-  __align__(16) float by[32], alpha[32];   // a move of the maxima, and its factor; at a segment's end 1 / l and LSE
+  __align__(16) float nmax[2][32]; // minus its reference M
+  __align__(16) float by[32], alpha[32];   // a move of the references, and its factor; at a segment's end 1 / l and LSE
   float red[4][4][8];             // [column quarter][lane quarter][column]
   float red_sc[4][4][4];           // [column quarter][lane quarter][group]
   ChunkRange range;                // the CTA's part of the tile list
@@ -241,17 +253,31 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N]) 
 }
 
 // Two E4M3 terms of a pair of FP16 values, p ~ hi + lo / 16 (the residual is
-// exact in FP16).
-__device__ __forceinline__ void split2(uint32_t p, uint32_t& hi2, uint32_t& lo2) {
+// exact in FP16); shift is added to lo before it is rounded.
+__device__ __forceinline__ void split2(uint32_t p, uint32_t shift, uint32_t& hi2, uint32_t& lo2) {
   uint32_t t, r;
   uint16_t h;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(p));
   hi2 = h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(t) : "h"(h));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(t));
-  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0x4C004C00u));
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(r) : "r"(0x4C004C00u), "r"(shift));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(r));
   lo2 = h;
+}
+
+// The shift of the weights of one key: (k - 512) 2^-19, k = 1, 3, .., 1023, in
+// both halves, within half of lo's smallest step, 2^-9.  Keys 0 .. 127 of a tile
+// get 128 values that are evenly spaced in every arithmetic progression of a
+// power of two keys (79 / 128 is near the golden ratio), four tiles' values lie
+// between each other's (317 / 512 likewise, and 317 is odd).
+__device__ __forceinline__ uint32_t shift_base(int row) { return 8u * ((79u * row) & 127u) + 1u; }
+__device__ __forceinline__ uint32_t shift_of(uint32_t base, int tile) {
+  const uint32_t k = ((base + 634u * (uint32_t)tile) & 0x3FFu) | 0x6400u;     // 1024 + k
+  uint32_t s = k | k << 16;
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(s) : "r"(0x66006600u));               // 1536
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(s) : "r"(0x00200020u));               // 2^-19
+  return s;
 }
 
 // 2 N bytes (N = 4 or 8: both terms), held as pairs, to shared memory.
@@ -699,7 +725,7 @@ __device__ void pv_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t tmem
 }
 
 // The query operand of one segment, and its columns' factors, visible keys and
-// maxima.  512 threads: column tid / TPH, dims [DPT (tid % TPH), + DPT).
+// references.  512 threads: column tid / TPH, dims [DPT (tid % TPH), + DPT).
 // there: the unit was published (false: of a call that gave up, whose queries
 // are not read).
 template <int NC, int kLayout, bool kTma>
@@ -756,7 +782,7 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
         const uint32_t q2 = live ? x[2 * i + j] : 0u;
         uint32_t y;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(bf16_bits_to_f32(q2 >> 16) * up), "f"(bf16_bits_to_f32(q2 & 0xFFFFu) * up));
-        split2(y, h2[j], l2[j]);
+        split2(y, 0u, h2[j], l2[j]);
       }
       hi[i] = h2[0] | h2[1] << 16;
       lo[i] = l2[0] | l2[1] << 16;
@@ -802,7 +828,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
   const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + c0;
   volatile int* abort = &ms.abort;
   uint64_t l_part[CP2];                                  // this row's share of the denominators
-  float m_lane = 0.f;                                    // running maximum of column c0 + lane % CPT (0: none yet)
+  float m_lane = 0.f;                                    // reference M of column c0 + lane % CPT (0: none yet)
   bool has = false;                                      // it is that of a key, or the column sees none at all
   bool pending = true;                                   // a column of the quarter still has none
   float cg[4] = {1.f, 1.f, 1.f, 1.f};                    // c_g
@@ -810,6 +836,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
   int slot0 = 0;                                         // ring slot of the tile's first block
   int tile = 0, last = 0;                                // tile of the unit, keys that anyone sees
   int full = 0;                                          // tiles that every column sees whole
+  const uint32_t base = shift_base(row);
   // rows of the pool behind which this thread's key of a box would lie outside
   const int in_box = kTma ? row & ((1 << w.box_shift) - 1) : 0;
   const uint32_t row_limit = (uint32_t)max((int64_t)0, a.pool_rows - in_box);
@@ -919,7 +946,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       for (int k = 0; k < CPT; ++k)
         if (!valid || j >= vis[k]) x[k] = -INFINITY;
     }
-    // Does a column's running maximum have to move, or a c_g?  (A maximum moves
+    // Does a column's reference have to move, or a c_g?  (A reference moves
     // for its own column only, so that a row's rounding does not hang on its
     // neighbours'.)  One barrier of
     // the column quarter's warps ORs the threads' answers; only then are the
@@ -956,8 +983,9 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       named_bar_sync(bar, 128);
       const int cl = lane % CPT;
       const float tmax = fmaxf(fmaxf(ms.red[cq][0][cl], ms.red[cq][1][cl]), fmaxf(ms.red[cq][2][cl], ms.red[cq][3][cl]));
+      const float lift = (float)max(1, (31 - __clz(sg.left + 1)) / 2 - 2);
       const bool need = has ? tmax > kTop : tmax > -INFINITY;
-      const float by = need ? tmax : 0.f;        // the maximum moves by this much
+      const float by = need ? tmax - lift : 0.f; // M moves by this much
       const float alpha_lane = need ? (has ? ex2_approx(-by) : 0.f) : 1.f;   // (nothing summed before the first key)
       has |= need;
       m_lane += by;
@@ -1033,6 +1061,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = make_uint4(0, 0, 0, 0);
     }
+    const uint32_t shift = shift_of(base, tile);
     const int pb = it % C::NPB;
     const uint32_t at = smem_u32(sm + C::P_OFF) + pb * C::P_BYTES;
 #pragma unroll
@@ -1047,7 +1076,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       for (int k = 0; k < CP2; ++k) {
         uint32_t v = p2[k];
         if (C::kScaled) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(f2));
-        split2(v, hi2[k], lo2[k]);
+        split2(v, shift, hi2[k], lo2[k]);
       }
       if (g == 0 && it >= C::NPB)
         pv_wait(it - C::NPB);
