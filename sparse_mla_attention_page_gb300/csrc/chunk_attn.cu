@@ -749,7 +749,7 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
     for (int j = 0; j < 4; ++j) {
       const float f0 = fabsf(bf16_bits_to_f32(x[j] & 0xFFFFu)), f1 = fabsf(bf16_bits_to_f32(x[j] >> 16));
       amax = fmaxf(amax, fmaxf(f0, f1));
-      nan |= !(f0 + f1 < INFINITY);
+      nan |= !(f0 < INFINITY && f1 < INFINITY);      // (the largest two have an infinite sum)
     }
   }
   if (nan) amax = INFINITY;

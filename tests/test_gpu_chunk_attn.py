@@ -535,3 +535,15 @@ def test_call_right_behind_one_that_gave_up():
     for i, (o, lse) in enumerate(outs):
         if i % 2:
             assert int(errs[i]) == 0 and torch.equal(o.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_largest_entries_side_by_side(layout):
+    """Entries of BF16's largest value next to each other are finite: the row is scored."""
+    w = make([3, 1], [200, 300], 8, layout, seed=38)
+    w["pool"][:] = w["pool"][:1]                       # equal keys: any finite score gives the same weights
+    w["q"][:, ::2] = 0
+    big = torch.finfo(BF).max
+    for at, h in ((0, 0), (10, 2), (255, 4), (510, 6)):
+        w["q"][:, h, at:at + 2] = torch.tensor([big, -big if at == 10 else big], dtype=BF)
+    check(w)
