@@ -752,6 +752,15 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
       nan |= !(f0 < INFINITY && f1 < INFINITY);      // (the largest two have an infinite sum)
     }
   }
+  constexpr int RD = kRopeDims / TPH;                // RoPE dims: part p holds [64 p / TPH, + 64 / TPH)
+  uint32_t pe[RD / 2];
+  if constexpr (C::kRope) {
+#pragma unroll
+    for (int i = 0; i < RD / 2; ++i) {
+      pe[i] = live_col ? __ldg(reinterpret_cast<const uint32_t*>(src + kD + part * RD) + i) : 0u;
+      nan |= (pe[i] & 0x7F80u) == 0x7F80u || (pe[i] & 0x7F800000u) == 0x7F800000u;
+    }
+  }
   if (nan) amax = INFINITY;
 #pragma unroll
   for (int off = TPH / 2; off >= 1; off /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -791,14 +800,12 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
     *reinterpret_cast<uint4*>(qb + kmajor_off<C::NQ>(col, k0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(qb + kmajor_off<C::NQ>(NC + col, k0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
-  if constexpr (C::kRope) {                          // 64 RoPE dims: part p holds [64 p / TPH, + 64 / TPH)
-    constexpr int RD = kRopeDims / TPH;              // 2, 4 or 8 dims
+  if constexpr (C::kRope) {
     uint32_t x[RD / 2];
 #pragma unroll
     for (int i = 0; i < RD / 2; ++i) {
-      const uint32_t q2 = live_col ? __ldg(reinterpret_cast<const uint32_t*>(src + kD + part * RD) + i) : 0u;
-      const __nv_bfloat162 y = __floats2bfloat162_rn(scale_pow2(bf16_bits_to_f32(q2 & 0xFFFFu), sh),
-                                                     scale_pow2(bf16_bits_to_f32(q2 >> 16), sh));
+      const __nv_bfloat162 y = __floats2bfloat162_rn(scale_pow2(bf16_bits_to_f32(pe[i] & 0xFFFFu), sh),
+                                                     scale_pow2(bf16_bits_to_f32(pe[i] >> 16), sh));
       x[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
     const int byte = part * RD * 2;                  // of the column's 128

@@ -547,3 +547,19 @@ def test_largest_entries_side_by_side(layout):
     for at, h in ((0, 0), (10, 2), (255, 4), (510, 6)):
         w["q"][:, h, at:at + 2] = torch.tensor([big, -big if at == 10 else big], dtype=BF)
     check(w)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_infinite_rope_dims_score_nan(value):
+    """A query with an infinite RoPE dim scores NaN also where every product has the same sign (all scores -inf)."""
+    w = make([1, 6, 1], [0, 2, 300], 16, "rope656", seed=39)
+    w["pool"][:, 528:] = torch.ones(w["pool"].shape[0], 64).to(BF).view(torch.uint8)
+    want_o, want_l = check(w)
+    hit = [(t, h) for t in (0, 1, 6, 7) for h in (0, 9)]
+    for t, h in hit:
+        w["q"][t, h, 512 + (5 * t + h) % 64] = value
+    o, lse, _ = run(w)
+    for t, h in hit:
+        assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h]), (t, h)
+        o[t, h], lse[t, h] = want_o[t, h], want_l[t, h]
+    assert torch.equal(o, want_o) and torch.equal(lse, want_l)
