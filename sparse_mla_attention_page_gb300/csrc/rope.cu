@@ -83,6 +83,9 @@ __device__ __forceinline__ uint32_t turned(uint32_t w, const Turn& r, int interl
 
 __global__ void __launch_bounds__(kThreads) rope_qkv656_kernel(const __grid_constant__ RopeArgs a, int heads_per_item,
                                                                int items_per_token) {
+  // as the KV writers: the attention behind it, a programmatic dependent, may
+  // set itself up meanwhile
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int64_t n_warps = ((int64_t)gridDim.x * kThreads) >> 5;

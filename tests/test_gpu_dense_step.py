@@ -74,3 +74,62 @@ def test_prompt_decode_release():
     assert int(count.item()) == 30 - held
     pages = [int(p) for b in range(B) for p in table[b, :ref.pages_of(length[b], page)].tolist()]
     assert sorted(pages + free[:30 - held].tolist()) == list(range(30))
+
+
+@pytest.mark.parametrize("new,ctx,H", [([1] * 24, [500] * 24, 16), ([700, 300], [100, 2000], 32), ([1], [3], 8)])
+def test_attention_directly_behind_the_rotary_writer(new, ctx, H):
+    """Attention queued right behind the writer of its queries and rows, over buffers that earlier calls still use:
+    eagerly and captured, the same bits as with a synchronisation in between."""
+    page, B, T = 64, len(new), sum(new)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    need = [ref.pages_of(a + b, page) for a, b in zip(new, ctx)]
+    table = torch.full((B, max(need)), -1, **I32)
+    at, cu, slots = 0, [0], []
+    for b in range(B):
+        table[b, :need[b]] = torch.arange(at, at + need[b])
+        slots += [at * page + ctx[b] + i for i in range(new[b])]
+        at += need[b]
+        cu.append(cu[-1] + new[b])
+    cu, kv = torch.tensor(cu, **I32), torch.tensor([a + b for a, b in zip(new, ctx)], **I32)
+    slots = torch.tensor(slots, device="cuda")
+    rnd = (lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16))
+    pool = torch.zeros(at * page, 656, dtype=torch.uint8, device="cuda")
+    binding.dsa_kv_write_rope656(rnd(at * page, 576), torch.arange(at * page, device="cuda"), pool)
+    spec = binding.rope_spec()
+    steps = [(rnd(T, H, 512), rnd(T, H, 64), rnd(T, 512), rnd(T, 64),
+              torch.randint(0, 10 ** 6, (1, T), generator=g, device="cuda", dtype=torch.int32)) for _ in range(6)]
+    q = torch.zeros(T, H, 576, dtype=torch.bfloat16, device="cuda")
+    ws = binding.chunk_workspace_for(T, H, B, "rope656")
+    outs = [(torch.zeros(T, H, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H, device="cuda")) for _ in steps]
+
+    def step(i, wait=False):
+        q_nope, q_pe, kv_c, k_pe, pos = steps[i]
+        binding.dsa_rope_qkv656(q_nope, q_pe, q, kv_c, k_pe, slots, pool, pos, spec)
+        if wait:
+            torch.cuda.synchronize()
+        binding.dsa_chunk_attn(q, pool, "rope656", table, page, cu, kv, SCALE, *outs[i], ws)
+
+    def results():
+        torch.cuda.synchronize()
+        r = [(o.clone(), lse.clone()) for o, lse in outs]
+        for o, lse in outs:
+            o.zero_()
+            lse.zero_()
+        return r
+
+    for i in range(6):
+        step(i, wait=True)
+        torch.cuda.synchronize()
+    want = results()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(6):
+            step(i)
+    for k in range(6):
+        if k % 2:
+            graph.replay()
+        else:
+            for i in range(6):
+                step(i)
+        for (o, lse), (wo, wl) in zip(results(), want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
