@@ -281,9 +281,10 @@ def dsa_gather_dequant(pool, layout, topk, out, idx_out, page_table=None, page_s
 
 def _kv_row_dim(pool, lay) -> int:
     """Key width held by one pool row (528- and 656-byte rows carry 16 bytes of
-    scales; 656-byte rows add 64 BF16 RoPE dims)."""
+    scales; 656-byte rows add 64 BF16 RoPE dims): 512 or 576 for the layout's own
+    row size alone."""
     if lay == DSA_KV_ROPE656:
-        return 512 + (pool.shape[1] - 528) // 2
+        return pool.shape[1] - 80
     return pool.shape[1] - (16 if lay == DSA_KV_SCALED528 else 0)
 
 

@@ -127,3 +127,11 @@ def test_binding_refuses_host_tensors():
         binding.dsa_pages_extend(x, x, x.view(1, 4), 16, x, x[:1], x[:1], x.long(), x, x, x, x)
     with pytest.raises((TypeError, RuntimeError)):
         binding.dsa_chunk_attn(torch.zeros(1, 1, 512), x, "raw512", x, 16, x, x, 1.0, x, x, x)
+
+
+def test_row_width_is_exact():
+    """A pool one byte (or a scale, or a RoPE dim) off its layout's row size is not taken for it."""
+    for lay, width, dims in ((0, 512, 512), (1, 528, 512), (2, 656, 576)):
+        assert binding._kv_row_dim(torch.empty(2, width), lay) == dims
+        for off in (-16, -2, -1, 1, 2, 16):
+            assert binding._kv_row_dim(torch.empty(2, width + off), lay) != dims
