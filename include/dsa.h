@@ -18,8 +18,12 @@
  *    synchronisation: each call only enqueues kernels on `stream`
  *    (a cudaStream_t passed as void*, NULL = the legacy default stream).
  *  - Arguments are validated on the host before anything is launched.  On a
- *    non-zero status nothing was launched and no output was touched.
- *    DSA_ERR_CUDA means a launch itself failed (cudaGetLastError).
+ *    non-zero status other than DSA_ERR_CUDA nothing was launched and no
+ *    output was touched.  DSA_ERR_CUDA means a launch itself failed
+ *    (cudaGetLastError); of a call that makes two, the first may run: its
+ *    outputs are then undefined (after dsa_pages_extend and dsa_pages_release
+ *    also the page table and the stack, whose count was not moved), and the
+ *    call is not to be repeated on them.
  *  - Data-dependent faults (a top-k index outside the pool or the page table,
  *    a bad page-table entry, a bad destination slot) never trap: the entry
  *    is skipped and a bit is OR-ed into the caller's int32 *err_flag_dev
@@ -66,7 +70,7 @@ enum {
   DSA_ERR_HEADS = 6,     /* head count not in {8, 16, 32, 64, 128} (dsa_chunk_attn: not in 1 to 1024) */
   DSA_ERR_WORKSPACE = 7, /* workspace missing or smaller than dsa_sparse_attn_workspace_bytes */
   DSA_ERR_DEVICE = 8,    /* no current CUDA device of compute capability 10.3 */
-  DSA_ERR_CUDA = 9,      /* a kernel launch failed */
+  DSA_ERR_CUDA = 9,      /* a kernel launch failed; the call's outputs are undefined */
   DSA_ERR_ALIGN = 10     /* a pointer is not 16-byte aligned (workspace: 256-byte) */
 };
 

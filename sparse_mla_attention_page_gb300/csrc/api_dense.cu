@@ -1,7 +1,7 @@
 // C ABI entry points of the dense serving operators (include/dsa.h): page
 // tables, rotary positions and the attention of new tokens.  Host-side
-// validation, then one launch sequence; on a non-zero status nothing was
-// launched.
+// validation, then one launch sequence; on a non-zero status other than
+// DSA_ERR_CUDA nothing was launched.
 #include <climits>
 #include <cmath>
 #include <cstdint>

@@ -49,7 +49,8 @@ struct __align__(16) ChunkSplit {
   int32_t slot0, next;
   int32_t pad[2];
 };
-constexpr int kFewParts = 8;         // split units of up to so many parts are merged a thread for each 8 dims
+constexpr int kFewParts = 8;         // split units of up to so many parts are merged a thread for each 4 dims
+constexpr int kMaxCtas = 1024;       // of the attention grid (one per SM); parts of a unit
 
 // Everything a call needs; the pointers from hdr on lie in the workspace.
 struct ChunkWork {

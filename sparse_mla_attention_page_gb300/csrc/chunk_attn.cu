@@ -1328,6 +1328,7 @@ int chunk_columns(int T, int H, int B) {
 }
 
 bool launch_chunk_attn(const ChunkWork& work, cudaStream_t stream) {
+  if (work.grid > kMaxCtas) return false;      // (the merge's limit, before anything is launched)
   ChunkWork w = work;
   // the largest power of two that divides the page and the tile: a box (rows
   // one by one where that is below 32, see above)

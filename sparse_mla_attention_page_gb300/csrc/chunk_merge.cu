@@ -30,7 +30,6 @@ constexpr int kVec = 2;                                   // float4 of a thread
 constexpr int kDimThreads = kSlice4 / kVec;
 constexpr int kLanes = kMergeThreads / kDimThreads;       // part lanes
 constexpr int kBatch = 5;                                 // parts of a lane whose loads are issued together (160 at once)
-constexpr int kMaxParts = 1024;                           // CTAs of the attention grid (one per SM)
 
 __device__ __forceinline__ void fold(float4& acc, float w, const float4& v) {
   acc.x = fmaf(w, v.x, acc.x);
@@ -60,7 +59,7 @@ __device__ __forceinline__ ChunkSplit split_of(const ChunkSplit* s) {
 
 // One slice of one row of a unit of many parts, by the whole block.
 __device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, int slice) {
-  __shared__ float wt[kMaxParts];
+  __shared__ float wt[kMaxCtas];
   __shared__ float red[kMergeThreads / 32], red2[kMergeThreads / 32];
   __shared__ float4 acc_s[kLanes][kSlice4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -131,8 +130,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The units of many parts: a bit for each CTA that one begins in, and its
   // entry (they begin more than kFewParts CTAs apart).
-  __shared__ uint32_t many[kMaxParts / 32];
-  __shared__ ChunkSplit big[kMaxParts / kFewParts];
+  __shared__ uint32_t many[kMaxCtas / 32];
+  __shared__ ChunkSplit big[kMaxCtas / kFewParts];
   for (int c0 = threadIdx.x & ~31; c0 < w.grid; c0 += kMergeThreads) {
     const int c = c0 + (threadIdx.x & 31);
     ChunkSplit s{};
@@ -181,7 +180,6 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
 }  // namespace
 
 bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
-  if (w.grid > kMaxParts) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(w.grid, kFewBlocks);
   cfg.blockDim = dim3(kMergeThreads);

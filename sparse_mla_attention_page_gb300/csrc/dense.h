@@ -28,7 +28,7 @@ struct ExtendArgs {
   int32_t* kv_lens;
   int32_t* err;
 };
-// false when nothing was launched (a launch attribute could not be set).
+// false when a launch failed or was not made (of two, the first may have been).
 bool launch_pages_extend(const ExtendArgs& a, int sms, cudaStream_t stream);
 
 struct ReleaseArgs {
