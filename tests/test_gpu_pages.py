@@ -207,3 +207,26 @@ def test_captured_steps():
         assert slots.tolist() == want["slots"] and table.tolist() == want["page_table"], step
         assert seq.tolist() == want["kv_lens"] and int(count.item()) == want["free_count"]
         lists = dict(seq=want["kv_lens"], table=want["page_table"], count=want["free_count"])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("T", [4095, 4096, 4097])
+def test_extend_around_one_cta(T, in_place):
+    """4096 token rows are the largest call of one CTA, one more the smallest with a grid and a finishing launch."""
+    w = make(40, 16, 90, 100, seed=13)
+    assert sum(w["new"]) <= T
+    w["T"] = T
+    check_extend(w, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,width", [(63, 65), (64, 64), (17, 241)])
+def test_release_around_one_cta(B, width, in_place):
+    """Tables of 4095, 4096 and 4097 entries, every page of them held."""
+    r = random.Random(B)
+    ids = list(range(B * width))
+    r.shuffle(ids)
+    w = dict(seq=[width * 4 - r.randint(0, 3) for _ in range(B)], new=[0] * B, page=4, count=3, T=1,
+             table=[ids[b * width:(b + 1) * width] for b in range(B)], free=[-1, -2, -3] + [-9] * (B * width))
+    for share in (0.3, 1.0):
+        check_release(w, [r.random() < share for _ in range(B)], in_place=in_place)
