@@ -20,13 +20,11 @@ namespace dsa {
 constexpr int kChunkTile = 128;      // keys of a tile
 
 // Costs of a tile, and of a unit beside its tiles'.  us of five prompts of up to
-// 2047 tokens and 16 heads, units of 1 to 16 tiles, for a unit cost of 3 / 4 / 5:
-//   rows by TMA       raw 237 / 213 / 196   scaled 303 / 279 / 277   rope 362 / 334 / 338
-//   rows one by one   raw 248 / 236 / 242   scaled 307 / 296 / 304   rope 370 / 360 / 368
+// 2047 tokens and 16 heads, units of 1 to 16 tiles, for a unit cost of 3 / 4 / 5 / 6 / 7:
+//   rows by TMA       raw 242 / 219 / 202 / 199 / 204   scaled 309 / 282 / 282 / 288   rope 382 / 360 / 363 / 365
+//   rows one by one   raw 277 / 250 / 235 / 239 / 245   scaled 319 / 298 / 303 / 309   rope 394 / 392 / 400 / 405
 constexpr int kTileCost = 2;
-constexpr int chunk_unit_cost(int layout, int box_shift) {
-  return layout == DSA_KV_RAW512 && box_shift > 0 ? 5 : 4;
-}
+constexpr int chunk_unit_cost(int layout) { return layout == DSA_KV_RAW512 ? 5 : 4; }
 
 struct __align__(16) ChunkUnit {
   int64_t tile0;     // first global tile

@@ -1336,7 +1336,7 @@ bool launch_chunk_attn(const ChunkWork& work, cudaStream_t stream) {
   int shift = 0;
   while (shift < 7 && page % (2 << shift) == 0) ++shift;
   w.box_shift = shift >= 5 ? shift : 0;
-  w.unit_cost = chunk_unit_cost(w.a.layout, w.box_shift);
+  w.unit_cost = chunk_unit_cost(w.a.layout);
   ChunkMaps maps{};
   if (w.box_shift > 0) {
     const int row_bytes = w.a.layout == DSA_KV_RAW512 ? kRawRow : w.a.layout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
