@@ -455,8 +455,10 @@ size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
  * 2^-14 of it, up or down by the key's position, so that a long tail of small
  * weights keeps its share of O: what this rounding leaves there is noise, in
  * the RMS 0.6 % at most of the largest weight times the values, however many
- * keys there are.  RoPE dims of a query are meant to lie below 2^63, and scales
- * to be at least 2^-60 (of a row whose scales are all smaller, less is kept).
+ * keys there are.  The largest latent entry of a query is meant to lie above
+ * 2^-100, and not 2^100 times below its RoPE dims, and rows' scales to be at
+ * least 2^-60 (of a query or row whose entries are all smaller, less is kept)
+ * and at most 2^96.
  * A row with an infinite or NaN scale, or a query with a NaN or an infinity,
  * scores NaN: the results that see it are NaN, no others.  Equal calls give
  * equal bits.

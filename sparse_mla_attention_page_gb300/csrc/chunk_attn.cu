@@ -754,16 +754,21 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
   }
   constexpr int RD = kRopeDims / TPH;                // RoPE dims: part p holds [64 p / TPH, + 64 / TPH)
   uint32_t pe[RD / 2];
+  float pmax = 0.f;
   if constexpr (C::kRope) {
 #pragma unroll
     for (int i = 0; i < RD / 2; ++i) {
       pe[i] = live_col ? __ldg(reinterpret_cast<const uint32_t*>(src + kD + part * RD) + i) : 0u;
       nan |= (pe[i] & 0x7F80u) == 0x7F80u || (pe[i] & 0x7F800000u) == 0x7F800000u;
+      pmax = fmaxf(pmax, fmaxf(fabsf(bf16_bits_to_f32(pe[i] & 0xFFFFu)), fabsf(bf16_bits_to_f32(pe[i] >> 16))));
     }
   }
   if (nan) amax = INFINITY;
 #pragma unroll
-  for (int off = TPH / 2; off >= 1; off /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  for (int off = TPH / 2; off >= 1; off /= 2) {
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (C::kRope) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
+  }
   int sh = 0;
   const float base = a.sm_scale * kLog2e;
   float sig = base;
@@ -771,13 +776,16 @@ __device__ __forceinline__ void build_query(const ChunkWork& w, uint8_t* sm, Mis
   if (live) {
     int e;
     const float f = frexpf(amax, &e);                // amax = f 2^e, f in [0.5, 1)
-    sh = min(f <= 0.875f ? 9 - e : 8 - e, 64);       // largest sh with amax 2^sh <= 448 (and the RoPE dims in range)
+    // largest sh with amax 2^sh <= 448, sig a normal number, and the RoPE dims
+    // times 2^sh below 2^112 (times the rows' 64, in range)
+    sh = min(f <= 0.875f ? 9 - e : 8 - e, 112);
+    if (C::kRope && pmax > 0.f) sh = min(sh, 112 - (ilogbf(pmax) + 1));
     sig = scale_pow2(base, -sh);
   } else if (amax > 0.f) {
     sig = __int_as_float(0x7FC00000);                // a row with a NaN or an infinity scores NaN
   }
   uint8_t* qb = sm + C::Q_OFF;
-  const float up = live ? __int_as_float((127 + sh) << 23) : 0.f;   // 2^sh, sh in [-120, 64]
+  const float up = live ? __int_as_float((127 + sh) << 23) : 0.f;   // 2^sh, sh in [-120, 112]
 #pragma unroll
   for (int c = 0; c < NV / 2; ++c) {
     uint32_t hi[4], lo[4];

@@ -563,3 +563,49 @@ def test_infinite_rope_dims_score_nan(value):
         assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h]), (t, h)
         o[t, h], lse[t, h] = want_o[t, h], want_l[t, h]
     assert torch.equal(o, want_o) and torch.equal(lse, want_l)
+
+
+def scaled_by(w, layout, e):
+    """Queries times 2^-e and rows (scales and RoPE dims) times 2^e: the same scores."""
+    w["q"] = (w["q"].double() * 2.0 ** -e).to(BF)
+    s = w["pool"][:, 512:528].contiguous().view(torch.float32) * 2.0 ** e
+    w["pool"][:, 512:528] = s.view(torch.uint8)
+    if layout == "rope656":
+        pe = (w["pool"][:, 528:].contiguous().view(BF).double() * 2.0 ** e).to(BF)
+        w["pool"][:, 528:] = pe.view(torch.uint8)
+    return w
+
+
+@pytest.mark.parametrize("layout", ["scaled528", "rope656"])
+@pytest.mark.parametrize("e", [-40, 40, 60, 80, 95])
+def test_small_queries_over_large_rows(layout, e):
+    """The queries' power of two reaches every magnitude that finite scores leave room for."""
+    check(scaled_by(make([1, 20], [300, 150], 16, layout, seed=40), layout, e))
+
+
+@pytest.mark.parametrize("big", [20, 60, 100])
+def test_large_rope_dims_of_a_query(big):
+    """RoPE dims of a query far above its latent dims, over rows whose RoPE dims are as much smaller."""
+    w = make([1, 20], [300, 150], 16, "rope656", seed=41)
+    w["q"][:, :, 512:] = (w["q"][:, :, 512:].double() * 2.0 ** big).to(BF)
+    pe = (w["pool"][:, 528:].contiguous().view(BF).double() * 2.0 ** -big).to(BF)
+    w["pool"][:, 528:] = pe.view(torch.uint8)
+    check(w)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("scale", [0.0, -0.03, 1.0])
+def test_other_score_scales(layout, scale, monkeypatch):
+    """No scale, a negative one, one that peaks the softmax."""
+    monkeypatch.setitem(globals(), "SCALE", scale)
+    check(make([1, 20], [700, 150], 16, layout, seed=42))
+
+
+@pytest.mark.parametrize("layout", ["scaled528", "rope656"])
+def test_negative_scales(layout):
+    w = make([1, 20], [700, 150], 16, layout, seed=43)
+    s = w["pool"][:, 512:528].contiguous().view(torch.float32)
+    s[::3] *= -1
+    s[:, 2] *= -1
+    w["pool"][:, 512:528] = s.view(torch.uint8)
+    check(w)
