@@ -454,8 +454,9 @@ size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
  * significant bits down to 2^-7 of the largest, below that to multiples of
  * 2^-14 of it, up or down by the key's position, so that a long tail of small
  * weights keeps its share of O: what this rounding leaves there is noise, in
- * the RMS 0.6 % at most of the largest weight times the values, however many
- * keys there are.  The largest latent entry of a query is meant to lie above
+ * the RMS 0.6 % at most of the largest weight times the values (0.15 % of the
+ * largest weight times 448 of its row's largest scale), however many keys there
+ * are.  The largest latent entry of a query is meant to lie above
  * 2^-100, and not 2^100 times below its RoPE dims, and rows' scales to be at
  * least 2^-60 (of a query or row whose entries are all smaller, less is kept)
  * and at most 2^96.
