@@ -34,15 +34,15 @@
 // a weight 1.  A move therefore puts the tile's largest p at 2^lift, lift =
 // log2(n) / 2 - 2 for the n tiles to come, at least 1 (as a shift may cost a
 // whole step instead of half of one): 0.6 % of the largest weight at most,
-// however many keys there are.  Scaled rows get 2 more, as their operands hold
-// s_g / S of a weight (below), and S follows the largest group of the largest
-// row: with them a context behind a dominant key whose largest group is 8 times
-// the others' comes out within 1 %, without them within 2 to 3 %.  p may grow to
-// 2^8.75 before M moves again (E4M3 ends at 448).  A move waits for the value
-// products, 0.9 of a tile's time, and moves are the more frequent the higher lift
-// is where rows differ in size: 4096 tokens over 8192 rows of 656 bytes take 4215
-// us with lift 0, 4460 with 1, 4670 with 3, and 5540 with lift = log2(n), which
-// would keep the loss of rounding to nearest below 1 %.
+// however many keys there are.  Over scaled rows lift = log2(n) / 2, at least 1,
+// as their operands hold s_g / S of a weight (below), and S follows the largest
+// group of the largest row: a context behind a dominant key whose largest group
+// is 8 times the others' comes out within 1 %, with 2 less within 2 to 3 %.  p
+// may grow to 2^8.75 before M moves again (E4M3 ends at 448).  A move waits for
+// the value products, 0.9 of a tile's time, and moves are the more frequent the
+// higher lift is where rows differ in size: 4096 tokens over 8192 rows of 656
+// bytes take 4215 us with lift 0, 4460 with 1, 4670 with this rule, and 5540 with
+// lift = log2(n), which would keep the loss of rounding to nearest below 1 %.
 //
 // Group scales (528- and 656-byte rows): one pass of the score product for
 // each 128-dim group, multiplied by the row's scale as it is read out, and one
@@ -1003,7 +1003,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       named_bar_sync(bar, 128);
       const int cl = lane % CPT;
       const float tmax = fmaxf(fmaxf(ms.red[cq][0][cl], ms.red[cq][1][cl]), fmaxf(ms.red[cq][2][cl], ms.red[cq][3][cl]));
-      const float lift = (float)min(max(1, (31 - __clz(sg.left + 1)) / 2 - 2) + (C::kScaled ? 2 : 0), kMaxLift);
+      const float lift = (float)min(max(1, (31 - __clz(sg.left + 1)) / 2 - (C::kScaled ? 0 : 2)), kMaxLift);
       const bool need = has ? tmax > kTop : tmax > -INFINITY;
       const float by = need ? tmax - lift : 0.f; // M moves by this much
       const float alpha_lane = need ? (has ? ex2_approx(-by) : 0.f) : 1.f;   // (nothing summed before the first key)
