@@ -21,8 +21,8 @@ constexpr int kChunkTile = 128;      // keys of a tile
 
 // Costs of a tile, and of a unit beside its tiles'.  us of five prompts of up to
 // 2047 tokens and 16 heads, units of 1 to 16 tiles, for a unit cost of 3 / 4 / 5 / 6 / 7:
-//   rows by TMA       raw 242 / 219 / 202 / 199 / 204   scaled 309 / 282 / 282 / 288   rope 382 / 360 / 363 / 365
-//   rows one by one   raw 277 / 250 / 235 / 239 / 245   scaled 319 / 298 / 303 / 309   rope 394 / 392 / 400 / 405
+//   rows by TMA       raw 242 / 218 / 202 / 199 / 204   scaled 310 / 284 / 287 / 294 / 295   rope 373 / 353 / 361 / 365 / 371
+//   rows one by one   raw 277 / 250 / 235 / 239 / 245   scaled 321 / 302 / 311 / 315 / 325   rope 377 / 380 / 388 / 397 / 403
 constexpr int kTileCost = 2;
 constexpr int chunk_unit_cost(int layout) { return layout == DSA_KV_RAW512 ? 5 : 4; }
 

@@ -62,9 +62,9 @@
 // that reads it last has finished.  Pages of a multiple of 32 rows come by TMA
 // (one warp, boxes of 32 to 128 rows: a page never ends inside a box); other
 // page sizes row by row with 16-byte cp.async (six warps).  us by TMA / row by
-// row, pages of 16 (boxes of 16): 1024 tokens of 16 heads over 8192, raw 434 /
-// 370, scaled 565 / 464, rope 637 / 583; 64 single tokens over up to 8192, raw
-// 47.6 / 42.8; pages of 32 (prompts of up to 2047 tokens, raw): 211 / 236.
+// row, pages of 16 (boxes of 16): 1024 tokens of 16 heads over 8192, raw 439 /
+// 374, scaled 573 / 493, rope 650 / 615; 64 single tokens over up to 8192, raw
+// 47.3 / 42.6; pages of 32 (prompts of up to 2047 tokens, raw): 213 / 235.
 //
 // What lies in shared memory for a key that nobody sees (the rest of a page, a
 // box that was not loaded) has no effect: its weights are 0, and a row that
@@ -161,8 +161,8 @@ struct Cfg {
   // The row-by-row producers: groups that take the blocks in turn, warps of a
   // group, quads of rows of a warp.  A block's barrier takes an arrival from
   // each thread of a group: three groups of two warps run raw and scaled rows
-  // 9 and 6 % faster than one of six (1024 tokens of 16 heads over 8192: 375
-  // against 412 us, 480 against 513); with the RoPE block they lose 2 to 8 %.
+  // 8 and 6 % faster than one of six (1024 tokens of 16 heads over 8192: 374
+  // against 405 us, 493 against 525); with the RoPE block they lose 8 %.
   static constexpr int GROUPS = kRope ? 1 : 3;
   static constexpr int GW = kProdWarps / GROUPS, QW = (kQuads + GW - 1) / GW;
   static_assert(kProdWarps % GROUPS == 0 && GW % 2 == 0, "rows of a thread share their place in the swizzle");
@@ -1332,9 +1332,9 @@ bool launch_nc(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
 
 // 16 rows where the average request has no more, else 32: half the columns
 // need less of everything but the rows' bytes, two units of 16 read the rows
-// twice.  us with 16 / 32, 64 requests of up to 8192 rows: 16 heads, raw 41.7 /
-// 44.8, rope 53.0 / 57.0; 24 heads, raw 57.7 / 46.1, rope 81.9 / 60.1; one of
-// 131072: 16 heads, raw 22.7 / 24.0; 32 heads 29.7 / 24.5.
+// twice.  us with 16 / 32, 64 requests of up to 8192 rows: 16 heads, raw 40.6 /
+// 43.4, rope 52.4 / 58.8; 24 heads, raw 57.3 / 45.9, rope 81.9 / 61.1; one of
+// 131072: 16 heads, raw 21.7 / 23.3; 32 heads 29.3 / 23.8.
 int chunk_columns(int T, int H, int B) {
   const int64_t rows = ((int64_t)T * H + B - 1) / B;     // of an average request
   return rows <= kFewestRows ? kFewestRows : 32;

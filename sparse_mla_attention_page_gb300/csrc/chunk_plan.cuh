@@ -69,10 +69,10 @@ struct ChunkRange {
 
 // Few short units, a CTA each: taken where no unit has more tiles than a CTA
 // would get of split ones and this many.  us with / without, two tiles more:
-// 2 x 20 tokens of 32 heads over 300, raw 13.4 / 18.3, rope 17.7 / 21.4; 30
-// single tokens over up to 300, raw 12.1 / 13.5; 300 tokens of 8 heads, raw
-// 13.5 / 18.9; three tiles more (16 single tokens over up to 500): raw 13.0 /
-// 12.2, rope 15.6 / 14.5.
+// 2 x 20 tokens of 32 heads over 300, raw 13.7 / 18.6, rope 18.1 / 21.8; 30
+// single tokens over up to 300, raw 12.5 / 13.9; 300 tokens of 8 heads, raw
+// 13.8 / 19.0; three tiles more (16 single tokens over up to 500): raw 13.5 /
+// 13.7, rope 16.2 / 16.4.
 constexpr int kWholeTiles = 2;
 
 constexpr int kPlanScratch = DSA_MAX_REQUESTS * 4 + 256;   // bytes of shared memory

@@ -58,10 +58,10 @@ def channel(kind, n, g):
     return c
 
 
-def check(kind, layout, keys, requests, H, gaps, equal_values=False, seed=0):
+def check(kind, layout, keys, requests, H, gaps, equal_values=False, seed=0, mean=1.0, dev=0.25):
     """`requests` requests of one token over the same pages; head h scores its top key gaps[h % len] nats above 0."""
     g = torch.Generator().manual_seed(seed)
-    x = 1.0 + (0 if equal_values else 0.25) * torch.randn(keys, 512, generator=g)
+    x = mean + (0 if equal_values else dev) * torch.randn(keys, 512, generator=g)
     x[:, 0] = channel(kind, keys, g)
     pool = rows_of(x, layout)
     page = 64
@@ -110,6 +110,14 @@ GAPS = [6, 7, 8, 9, 9.5, 10, 10.5, 11, 12, 13, 14, 15, 16, 18, 20, 24]
 def test_tail_of_a_dominant_key(layout, kind, keys, requests, H):
     """Row groups that one SM takes whole, of 16 and 32 query rows, and ones spread over SMs."""
     check(kind, layout, keys, requests, H, GAPS)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("kind", ["first", "spread"])
+@pytest.mark.parametrize("keys,requests,H", [(8192, 160, 16), (16384, 90, 32)])
+def test_tail_of_large_rows(layout, kind, keys, requests, H):
+    """Latents of N(0, 8^2): sums that cancel."""
+    check(kind, layout, keys, requests, H, GAPS, mean=0.0, dev=8.0, seed=1)
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
