@@ -272,10 +272,10 @@ __device__ __forceinline__ void split2(uint32_t p, uint32_t shift, uint32_t& hi2
 }
 
 // The shift of the weights of one key: (k - 512) 2^-19, k = 1, 3, .., 1023, in
-// both halves, within half of lo's smallest step, 2^-9.  Keys 0 .. 127 of a tile
-// get 128 values that are evenly spaced in every arithmetic progression of a
-// power of two keys (79 / 128 is near the golden ratio), four tiles' values lie
-// between each other's (317 / 512 likewise, and 317 is odd).
+// both halves, within half of lo's smallest step, 2^-9.  The 128 keys of a tile
+// get values 2^-16 apart, those of keys a power of two apart evenly spaced too,
+// and of neighbours nearly so (79 / 128 is near the golden ratio); four tiles'
+// values lie between each other's (634 is 2 modulo 8).
 __device__ __forceinline__ uint32_t shift_base(int row) { return 8u * ((79u * row) & 127u) + 1u; }
 __device__ __forceinline__ uint32_t shift_of(uint32_t base, int tile) {
   const uint32_t k = ((base + 634u * (uint32_t)tile) & 0x3FFu) | 0x6400u;     // 1024 + k
