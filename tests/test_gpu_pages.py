@@ -230,3 +230,38 @@ def test_release_around_one_cta(B, width, in_place):
              table=[ids[b * width:(b + 1) * width] for b in range(B)], free=[-1, -2, -3] + [-9] * (B * width))
     for share in (0.3, 1.0):
         check_release(w, [r.random() < share for _ in range(B)], in_place=in_place)
+
+
+def test_captured_steps_of_a_grid():
+    """Calls of a grid and its finishing launch, lengths and count in place: pages handed out and returned in one
+    captured step, replayed with other lengths each time."""
+    r = random.Random(14)
+    B, page, width, T = 90, 16, 80, 9000
+    n_pages = B * width
+    ids = list(range(n_pages))
+    r.shuffle(ids)
+    w = dict(seq=[0] * B, table=[[-1] * width for _ in range(B)], free=ids, count=n_pages)
+    seq, new = torch.tensor(w["seq"], **I32), torch.zeros(B, **I32)
+    table, free, count = torch.tensor(w["table"], **I32), torch.tensor(w["free"], **I32), torch.tensor([n_pages], **I32)
+    done = torch.zeros(B, dtype=torch.bool, device="cuda")
+    slots, pos, ts = torch.zeros(T, dtype=torch.int64, device="cuda"), torch.zeros(T, **I32), torch.zeros(T, **I32)
+    cu, err = torch.zeros(B + 1, **I32), torch.zeros(1, **I32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        binding.dsa_pages_extend(seq, new, table, page, free, count, count, slots, pos, ts, cu, seq, err_flag=err)
+        binding.dsa_pages_release(done, seq, table, page, free, count, count, seq, err_flag=err)
+    for step in range(5):
+        grow = [r.randint(0, 190) for _ in range(B)]
+        out = [r.random() < 0.3 for _ in range(B)]
+        new.copy_(torch.tensor(grow))
+        done.copy_(torch.tensor(out))
+        g.replay()
+        torch.cuda.synchronize()
+        a = ref.extend(w["seq"], grow, w["table"], page, w["free"], w["count"], T)
+        b = ref.release(out, a["kv_lens"], a["page_table"], page, w["free"], a["free_count"])
+        assert slots.tolist() == a["slots"] and pos.tolist() == a["positions"] and ts.tolist() == a["token_seq"], step
+        assert cu.tolist() == a["cu_q"] and table.tolist() == a["page_table"]
+        assert seq.tolist() == b["seq_lens"] and int(count) == b["free_count"] and free.tolist() == b["free_pages"]
+        assert int(err) == a["err"] | b["err"]
+        err.zero_()
+        w = dict(seq=b["seq_lens"], table=a["page_table"], free=b["free_pages"], count=b["free_count"])
