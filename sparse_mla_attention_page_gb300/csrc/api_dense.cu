@@ -58,6 +58,18 @@ size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, char* base
   return end;
 }
 
+// Radians as the fraction of a turn, in units of 2^-64 turn.  1 / 2 pi and the
+// product are kept as two doubles each: a position is up to 2^31 such steps.
+uint64_t turn_of(double radians) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;    // 1 / 2 pi
+  double hi = radians * kHi;
+  double lo = std::fma(radians, kHi, -hi) + radians * kLo;
+  hi -= std::floor(hi);
+  lo -= std::nearbyint(lo);
+  const uint64_t whole = hi < 1.0 ? (uint64_t)std::ldexp(hi, 64) : 0;
+  return whole + ((uint64_t)(int64_t)std::ldexp(lo, 62) << 2);
+}
+
 bool chunk_sizes_ok(int T, int H, int B) {
   return T >= 0 && H >= 1 && H <= 1024 && (int64_t)T * H <= INT32_MAX / 2 && B >= 1 && B <= DSA_MAX_REQUESTS;
 }
@@ -128,10 +140,7 @@ int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t 
   for (int i = 0; i < 32; ++i) {
     if (rope->axis[i] < 0 || rope->axis[i] >= rope->n_axes || !std::isfinite(rope->inv_freq[i])) return DSA_ERR_SHAPE;
     a.axis[i] = (uint8_t)rope->axis[i];
-    // the fraction of a turn a position adds, in units of 2^-64 turn
-    double f = rope->inv_freq[i] * 0.15915494309189533577;
-    f -= std::floor(f);
-    a.turn[i] = f < 1.0 ? (uint64_t)std::ldexp(f, 64) : 0;
+    a.turn[i] = turn_of(rope->inv_freq[i]);
   }
   if (T == 0) return DSA_OK;
   const bool q = q_pe_dev != nullptr, kv = kv_c_dev != nullptr;

@@ -186,3 +186,36 @@ def test_other_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(q.cpu(), want) and torch.equal(p.cpu(), pool)
+
+
+def exact_turned(x, positions, axis, inv_freq, interleaved):
+    """x [T, 64] float64 turned by angles that are reduced in 80 decimal digits."""
+    import decimal
+    with decimal.localcontext() as ctx:
+        ctx.prec = 80
+        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899863")
+        out = np.array(x, dtype=np.float64)
+        for i in range(32):
+            step = decimal.Decimal(float(inv_freq[i]))
+            ang = np.array([float((int(p) * step) % two_pi) for p in positions[axis[i]]])
+            ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + 32)
+            a, b = x[:, ia], x[:, ib]
+            out[:, ia], out[:, ib] = a * np.cos(ang) - b * np.sin(ang), b * np.cos(ang) + a * np.sin(ang)
+    return out
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("top", [1.0, 40.0, 1e4, 1e7])
+def test_far_positions_at_any_frequency(top, interleaved):
+    """Positions up to 2^31 and frequencies of many turns a step keep full precision."""
+    w = inputs(40, 2, seed=21, axes=1, far=2 ** 31 - 1)
+    w["positions"][0, :4] = torch.tensor([2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2, 1], dtype=torch.int32)
+    spec = binding.rope_spec(inv_freq=[top * 0.7 ** i * (-1) ** i for i in range(32)], axis=[0] * 32, interleaved=interleaved)
+    q, _, err = run(w, spec)
+    assert err == 0
+    for h in range(2):
+        x = w["q_pe"][:, h].double().numpy()
+        want = exact_turned(x, w["positions"].tolist(), [0] * 32, list(spec.inv_freq), interleaved)
+        mag = np.abs(x).max(-1, keepdims=True) * 2
+        d = np.abs(q[:, h, 512:].double().numpy() - want)
+        assert (d <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * mag).all(), d.max()
