@@ -57,8 +57,31 @@ extern "C" {
  *                    little-endian BF16 at byte offsets 528 + 2j: keys and
  *                    queries are 576 wide, values are the 512 latent dims
  *                    ["[DSA] Support group-scaled FP8 NoPE KV reads for CUDA
- *                    TileLang", Motivation: the 656-byte layout]. */
-typedef enum { DSA_KV_RAW512 = 0, DSA_KV_SCALED528 = 1, DSA_KV_ROPE656 = 2 } dsa_kv_layout;
+ *                    TileLang", Motivation: the 656-byte layout].
+ *  DSA_KV_FP4_288    4-bit rows: E2M1 codes (magnitudes 0, 0.5, 1, 1.5, 2, 3,
+ *                    4, 6) of the 512 dims, an exponent for each block of 16
+ *                    dims, an FP32 scale for each group of 128:
+ *                      value = code * 2^(e - 5) * scale,  e in 0 .. 11.
+ *                    Bytes [0, 256): word w (little-endian, 32 bits) holds
+ *                    dims 8 w + i, i = 0 .. 7: the number of the magnitude in
+ *                    bits 4 i .. 4 i + 2, the sign in bit 8 i + 7 for i < 4 and
+ *                    in bit 8 (i - 4) + 3 for i >= 4.  [256, 272): scale g at
+ *                    256 + 4 g.  [272, 288): e of block j in byte 272 + j / 2,
+ *                    the low nibble for even j (12 to 15 are never written and
+ *                    read as unspecified values).  A group of scale NaN reads
+ *                    as NaN.
+ *  DSA_KV_FP4_416    the 288-byte row, then the 64 RoPE dims as BF16 at byte
+ *                    offsets 288 + 2j: 576-wide keys, as DSA_KV_ROPE656.
+ * The 4-bit layouts are taken by dsa_kv_write_fp4, dsa_kv_read,
+ * dsa_chunk_attn and dsa_prefix_attn; every entry point that names no layouts
+ * of its own takes the first three. */
+typedef enum {
+  DSA_KV_RAW512 = 0,
+  DSA_KV_SCALED528 = 1,
+  DSA_KV_ROPE656 = 2,
+  DSA_KV_FP4_288 = 16,
+  DSA_KV_FP4_416 = 17
+} dsa_kv_layout;
 
 enum {
   DSA_OK = 0,
@@ -103,8 +126,8 @@ const char* dsa_status_string(int status);
  * issued from other threads. */
 uint64_t dsa_set_wait_limit_ns(uint64_t ns);
 
-/* Bytes of one physical KV row: 512, 528 or 656 ("exported buffer lengths",
- * [P1 Speed Tests and Profiling]); 0 for an unknown layout. */
+/* Bytes of one physical KV row: 512, 528, 656, 288 or 416 ("exported buffer
+ * lengths", [P1 Speed Tests and Profiling]); 0 for an unknown layout. */
 size_t dsa_kv_row_bytes(int layout);
 
 /* ------------------------------------------------------------- KV writers */
@@ -269,6 +292,50 @@ int dsa_gather_dequant(const void* pool_dev, int64_t pool_rows, int layout,
                        void* out_bf16_dev, size_t out_bytes, int32_t* idx_out_dev, int32_t* err_flag_dev,
                        void* stream);
 
+/* ------------------------------- 4-bit rows, and rows read back by request */
+
+/* New BF16 rows into a pool of 4-bit rows, quantised as they are written.  For
+ * each group of 128 dims s = amax / 384 (FP32, IEEE division) and y = x / s
+ * (the same); for each block of 16 dims e is the smallest of 0 .. 11 with
+ * max |y| <= 7 * 2^(e - 5), and code = E2M1(y * 2^(5 - e)), round to nearest,
+ * ties to the even code, at most 6.  amax == 0 stores s = 0.  A group with a
+ * NaN or an infinity stores scale NaN.  RoPE dims are stored as they are.
+ *   kv_c_dev   [n_rows, 512] BF16, rows kv_c_stride elements apart (a multiple
+ *              of 8, >= 0), 16-byte aligned.
+ *   k_pe_dev   [n_rows, 64] BF16, rows k_pe_stride elements apart (even,
+ *              >= 0), 4-byte aligned: 416-byte rows; NULL: 288-byte rows.
+ *   slots_dev  [n_rows] int64 physical destination rows, distinct; slot < 0
+ *              skips the row, slot >= pool_rows sets DSA_DEV_ERR_SLOT_RANGE.
+ *   pool_dev   [pool_rows, 288 or 416] bytes, 16-byte aligned; overlaps no input.
+ * n_rows == 0 is a no-op. */
+int dsa_kv_write_fp4(const void* kv_c_dev, int64_t kv_c_stride, const void* k_pe_dev, int64_t k_pe_stride,
+                     int64_t n_rows, const int64_t* slots_dev, void* pool_dev, int64_t pool_rows,
+                     int32_t* err_flag_dev, void* stream);
+
+/* Reads requests' rows back as BF16, in token order: row i of request b,
+ * i < cu_rows[b + 1] - cu_rows[b], is the row of key j = starts[b] + i (starts
+ * NULL: from 0),
+ *   out[cu_rows[b] + i] = bf16_rn(fp32(code_d) * s_g), d = 0 .. 511
+ * (raw rows: s = 1, exact; 4-bit rows: code 2^(e - 5)), followed for 656- and
+ * 416-byte rows by their 64 RoPE dims as stored.
+ * Rows of out outside [cu_rows[0], cu_rows[B]), and what out_stride leaves
+ * between rows, stay as they were.  A key whose page-table entry is negative or
+ * lies beyond the pool (DSA_DEV_ERR_PAGE_RANGE), and one with starts[b] < 0 or
+ * j >= max_pages * page_size (DSA_DEV_ERR_LENGTH), leaves its row of out as it
+ * was.  cu_rows that does not ascend within [0, out_rows] sets
+ * DSA_DEV_ERR_LENGTH; which rows are read is then unspecified, and nothing
+ * outside out is written.
+ *   layout          any of the five.
+ *   page_table_dev  [B, max_pages] int32;  B at most DSA_MAX_REQUESTS.
+ *   cu_rows_dev     [B + 1] int32;  starts_dev [B] int32 or NULL.
+ *   out_bf16_dev    [out_rows, 512 or 576] BF16, rows out_stride elements apart
+ *                   (a multiple of 8, at least the width), 16-byte aligned,
+ *                   out_rows < 2^31; overlaps no input.
+ * out_rows == 0 is a no-op. */
+int dsa_kv_read(const void* pool_dev, int64_t pool_rows, int layout, const int32_t* page_table_dev, int B,
+                int max_pages, int page_size, const int32_t* cu_rows_dev, const int32_t* starts_dev,
+                void* out_bf16_dev, int64_t out_rows, int64_t out_stride, int32_t* err_flag_dev, void* stream);
+
 /* ------------------------------------------- decode without allocation */
 
 /* Largest split-K workspace dsa_sparse_attn_decode_noalloc can serve (32 MiB). */
@@ -355,7 +422,7 @@ int dsa_pages_extend(const int32_t* seq_lens_dev, const int32_t* new_lens_dev, i
  * free_count_out = free_count + pages returned; seq_lens_out[b] = 0 for a
  * finished request, seq_lens[b] for the others; the page table is read only
  * (its rows are stale for a request of length 0).  A page belongs to one
- * request: pages that requests share are not counted.  All or nothing: a
+ * request: pages that requests share are for dsa_pages_release_own.  All or nothing: a
  * length outside [0, max_pages * page_size] or free_count outside
  * [0, free_cap] (DSA_DEV_ERR_LENGTH) or a stack without room
  * (DSA_DEV_ERR_NO_PAGES) leaves free_pages as it was and copies free_count and
@@ -369,6 +436,21 @@ int dsa_pages_release(const uint8_t* finished_dev, const int32_t* seq_lens_dev, 
                       int32_t* free_pages_dev, int free_cap, const int32_t* free_count_dev,
                       int32_t* free_count_out_dev, int32_t* seq_lens_out_dev, int32_t* err_flag_dev,
                       void* stream);
+
+/* dsa_pages_release for requests that begin with pages they do not own: the
+ * first shared_pages[b] pages of request b belong to a prefix that other
+ * requests hold too (its owner put them into the page-table rows and returns
+ * them by itself), and only the pages behind them go back to the stack.
+ * Request b is entered with seq_lens[b] = shared_pages[b] * page_size and its
+ * row's first entries set; dsa_pages_extend then hands out pages from there on.
+ *   shared_pages_dev  [B] int32; below 0: DSA_DEV_ERR_LENGTH, nothing is
+ *                     returned; a request that holds no more pages returns none.
+ * Everything else as dsa_pages_release. */
+int dsa_pages_release_own(const uint8_t* finished_dev, const int32_t* shared_pages_dev,
+                          const int32_t* seq_lens_dev, int B, const int32_t* page_table_dev, int max_pages,
+                          int page_size, int32_t* free_pages_dev, int free_cap, const int32_t* free_count_dev,
+                          int32_t* free_count_out_dev, int32_t* seq_lens_out_dev, int32_t* err_flag_dev,
+                          void* stream);
 
 /* ------------------------------------------------- rotary positions */
 

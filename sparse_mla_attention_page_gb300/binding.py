@@ -20,7 +20,11 @@ from . import build as _build
 DSA_KV_RAW512 = 0
 DSA_KV_SCALED528 = 1
 DSA_KV_ROPE656 = 2
-LAYOUTS = {"raw512": DSA_KV_RAW512, "scaled528": DSA_KV_SCALED528, "rope656": DSA_KV_ROPE656}
+DSA_KV_FP4_288 = 16
+DSA_KV_FP4_416 = 17
+LAYOUTS = {"raw512": DSA_KV_RAW512, "scaled528": DSA_KV_SCALED528, "rope656": DSA_KV_ROPE656,
+           "fp4_288": DSA_KV_FP4_288, "fp4_416": DSA_KV_FP4_416}
+_ROW_BYTES = {DSA_KV_RAW512: 512, DSA_KV_SCALED528: 528, DSA_KV_ROPE656: 656, DSA_KV_FP4_288: 288, DSA_KV_FP4_416: 416}
 
 DSA_DEV_ERR_INDEX_RANGE = 1
 DSA_DEV_ERR_PAGE_RANGE = 2
@@ -39,6 +43,7 @@ EXPORTS = (
     "dsa_sparse_attn_prefill_q8", "dsa_gather_dequant_workspace_bytes", "dsa_gather_dequant",
     "dsa_sparse_attn_decode_noalloc", "dsa_set_wait_limit_ns",
     "dsa_pages_extend", "dsa_pages_release", "dsa_rope_qkv656", "dsa_chunk_attn_workspace_bytes", "dsa_chunk_attn",
+    "dsa_kv_write_fp4", "dsa_kv_read", "dsa_pages_release_own",
 )
 
 
@@ -112,6 +117,12 @@ def lib() -> ctypes.CDLL:
             L.dsa_chunk_attn.restype = i32
             L.dsa_chunk_attn.argtypes = [vp, i32, i32, i32, vp, i64, i32, i32, vp, i32, i32, i32, vp, vp, i32,
                                          c.c_float, vp, vp, vp, c.c_size_t, vp, vp]
+            L.dsa_kv_write_fp4.restype = i32
+            L.dsa_kv_write_fp4.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, vp, vp]
+            L.dsa_kv_read.restype = i32
+            L.dsa_kv_read.argtypes = [vp, i64, i32, vp, i32, i32, i32, vp, vp, vp, i64, i64, vp, vp]
+            L.dsa_pages_release_own.restype = i32
+            L.dsa_pages_release_own.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp]
             _lib = L
     return _lib
 
@@ -281,8 +292,10 @@ def dsa_gather_dequant(pool, layout, topk, out, idx_out, page_table=None, page_s
 
 def _kv_row_dim(pool, lay) -> int:
     """Key width held by one pool row (528- and 656-byte rows carry 16 bytes of
-    scales; 656-byte rows add 64 BF16 RoPE dims): 512 or 576 for the layout's own
-    row size alone."""
+    scales; 656-byte rows add 64 BF16 RoPE dims; 4-bit rows hold 512 dims in 288
+    bytes): 512 or 576 for the layout's own row size alone."""
+    if lay in (DSA_KV_FP4_288, DSA_KV_FP4_416):
+        return pool.shape[1] + (224 if lay == DSA_KV_FP4_288 else 160)
     if lay == DSA_KV_ROPE656:
         return pool.shape[1] - 80
     return pool.shape[1] - (16 if lay == DSA_KV_SCALED528 else 0)
@@ -426,6 +439,55 @@ def dsa_pages_release(finished, seq_lens, page_table, page_size, free_pages, fre
         _arg(page_table, "page_table", i32, None, dev), W, page_size, _arg(free_pages, "free_pages", i32, None, dev), cap,
         _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev),
         _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev), _flag(err_flag, dev), s), "dsa_pages_release")
+
+
+def dsa_pages_release_own(finished, shared_pages, seq_lens, page_table, page_size, free_pages, free_count,
+                          free_count_out, seq_lens_out, err_flag=None, stream=None) -> None:
+    """dsa_pages_release, but for the first shared_pages [B] pages of each request, which belong to a prefix that
+    other requests hold too (see include/dsa.h)."""
+    dev, s = _call_device(stream)
+    i32 = torch.int32
+    B, W = _dims(page_table, "page_table", 2)
+    cap, = _dims(free_pages, "free_pages", 1)
+    _check((_lib or lib()).dsa_pages_release_own(
+        _arg(finished, "finished", torch.bool, (B,), dev), _arg(shared_pages, "shared_pages", i32, (B,), dev),
+        _arg(seq_lens, "seq_lens", i32, (B,), dev), B,
+        _arg(page_table, "page_table", i32, None, dev), W, page_size, _arg(free_pages, "free_pages", i32, None, dev), cap,
+        _arg(free_count, "free_count", i32, (1,), dev), _arg(free_count_out, "free_count_out", i32, (1,), dev),
+        _arg(seq_lens_out, "seq_lens_out", i32, (B,), dev), _flag(err_flag, dev), s), "dsa_pages_release_own")
+
+
+def dsa_kv_write_fp4(kv_c, slots, pool, k_pe=None, err_flag=None, stream=None) -> None:
+    """pool [rows, 288] uint8 <- the latents kv_c [n, 512] in 4 bits at rows ``slots``; with k_pe [n, 64], pool
+    [rows, 416] and the RoPE dims behind them (see include/dsa.h)."""
+    dev, s = _call_device(stream)
+    bf = torch.bfloat16
+    n, _ = _dims(kv_c, "kv_c", 2)
+    rows, _ = _dims(pool, "pool", 2)
+    st = (lambda t: 0 if t is None or n <= 1 else t.stride(0))
+    _check((_lib or lib()).dsa_kv_write_fp4(
+        _arg_strided(kv_c, "kv_c", bf, (n, 512), dev), st(kv_c), _arg_strided(k_pe, "k_pe", bf, (n, 64), dev), st(k_pe), n,
+        _arg(slots, "slots", torch.int64, (n,), dev),
+        _arg(pool, "pool", torch.uint8, (rows, 288 if k_pe is None else 416), dev), rows, _flag(err_flag, dev), s),
+        "dsa_kv_write_fp4")
+
+
+def dsa_kv_read(pool, layout, page_table, page_size, cu_rows, out, starts=None, err_flag=None, stream=None) -> None:
+    """out [n, 512 or 576] BF16 <- the rows of the requests in token order: request b's rows starts[b] (0) and on go to
+    out[cu_rows[b]:cu_rows[b + 1]] (see include/dsa.h).  out may be strided in its first dim."""
+    dev, s = _call_device(stream)
+    lay = LAYOUTS.get(layout, layout)
+    i32 = torch.int32
+    B, W = _dims(page_table, "page_table", 2)
+    rows, _ = _dims(pool, "pool", 2)
+    n, _ = _dims(out, "out", 2)
+    width = 576 if lay in (DSA_KV_ROPE656, DSA_KV_FP4_416) else 512
+    _check((_lib or lib()).dsa_kv_read(
+        _arg(pool, "pool", torch.uint8, (rows, _ROW_BYTES.get(lay)), dev), rows, lay,
+        _arg(page_table, "page_table", i32, None, dev), B, W, page_size, _arg(cu_rows, "cu_rows", i32, (B + 1,), dev),
+        None if starts is None else _arg(starts, "starts", i32, (B,), dev),
+        _arg_strided(out, "out", torch.bfloat16, (n, width), dev), n, out.stride(0) if n > 1 else width,
+        _flag(err_flag, dev), s), "dsa_kv_read")
 
 
 def rope_spec(theta=10000.0, sections=(32,), interleaved=False, inv_freq=None, axis=None, mscale=1.0) -> DsaRope:

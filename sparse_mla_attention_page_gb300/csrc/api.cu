@@ -182,6 +182,8 @@ size_t dsa_kv_row_bytes(int layout) {
   if (layout == DSA_KV_RAW512) return 512;
   if (layout == DSA_KV_SCALED528) return 528;
   if (layout == DSA_KV_ROPE656) return 656;
+  if (layout == DSA_KV_FP4_288) return 288;
+  if (layout == DSA_KV_FP4_416) return 416;
   return 0;
 }
 
@@ -216,7 +218,8 @@ int dsa_quantize_q8(const void* q_bf16_dev, int64_t n_vec, void* q8_dev, float* 
 }
 
 size_t dsa_gather_dequant_workspace_bytes(int T, int K, int64_t pool_rows, int layout) {
-  if (T < 0 || K < 0 || pool_rows < 0 || dsa_kv_row_bytes(layout) == 0) return 0;
+  if (T < 0 || K < 0 || pool_rows < 0) return 0;
+  if (layout != DSA_KV_RAW512 && layout != DSA_KV_SCALED528 && layout != DSA_KV_ROPE656) return 0;
   const size_t width = layout == DSA_KV_ROPE656 ? 576 : 512;
   return (size_t)dsa::gather_rows(pool_rows, (int64_t)T * K) * width * 2;
 }

@@ -70,6 +70,22 @@ uint64_t turn_of(double radians) {
   return whole + ((uint64_t)(int64_t)std::ldexp(lo, 62) << 2);
 }
 
+int release_pages(const dsa::ReleaseArgs& a, void* stream) {
+  if (!table_ok(a.B, a.max_pages, a.page_size) || a.free_cap < 1) return DSA_ERR_SHAPE;
+  if (any_null(a.finished) || any_null(a.seq_lens, a.page_table, a.free_count) ||
+      any_null(a.free_pages, a.free_count_out, a.seq_lens_out))
+    return DSA_ERR_NULL;
+  for (const void* p : {(const void*)a.seq_lens, (const void*)a.page_table, (const void*)a.free_pages,
+                        (const void*)a.free_count, (const void*)a.free_count_out, (const void*)a.seq_lens_out,
+                        (const void*)a.err})
+    if (!aligned(p, 4)) return DSA_ERR_ALIGN;
+  int sms = 0;
+  const int st = dsa::current_device_sms(&sms);
+  if (st != DSA_OK) return st;
+  cudaGetLastError();
+  return launch_status(dsa::launch_pages_release(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
 bool chunk_sizes_ok(int T, int H, int B) {
   return T >= 0 && H >= 1 && H <= 1024 && (int64_t)T * H <= INT32_MAX / 2 && B >= 1 && B <= DSA_MAX_REQUESTS;
 }
@@ -108,23 +124,22 @@ int dsa_pages_release(const uint8_t* finished_dev, const int32_t* seq_lens_dev, 
                       const int32_t* page_table_dev, int max_pages, int page_size, int32_t* free_pages_dev,
                       int free_cap, const int32_t* free_count_dev, int32_t* free_count_out_dev,
                       int32_t* seq_lens_out_dev, int32_t* err_flag_dev, void* stream) {
+  return release_pages({finished_dev, nullptr, seq_lens_dev, B, page_table_dev, max_pages, page_size, free_pages_dev,
+                        free_cap, free_count_dev, free_count_out_dev, seq_lens_out_dev, err_flag_dev},
+                       stream);
+}
+
+int dsa_pages_release_own(const uint8_t* finished_dev, const int32_t* shared_pages_dev,
+                          const int32_t* seq_lens_dev, int B, const int32_t* page_table_dev, int max_pages,
+                          int page_size, int32_t* free_pages_dev, int free_cap, const int32_t* free_count_dev,
+                          int32_t* free_count_out_dev, int32_t* seq_lens_out_dev, int32_t* err_flag_dev,
+                          void* stream) {
   if (!table_ok(B, max_pages, page_size) || free_cap < 1) return DSA_ERR_SHAPE;
-  if (any_null(finished_dev) || any_null(seq_lens_dev, page_table_dev, free_pages_dev, free_count_dev,
-                                         free_count_out_dev, seq_lens_out_dev))
-    return DSA_ERR_NULL;
-  for (const void* p : {(const void*)seq_lens_dev, (const void*)page_table_dev, (const void*)free_pages_dev,
-                        (const void*)free_count_dev, (const void*)free_count_out_dev,
-                        (const void*)seq_lens_out_dev, (const void*)err_flag_dev})
-    if (!aligned(p, 4)) return DSA_ERR_ALIGN;
-  int sms = 0;
-  const int st = dsa::current_device_sms(&sms);
-  if (st != DSA_OK) return st;
-  const dsa::ReleaseArgs a{finished_dev, seq_lens_dev,   B,
-                           page_table_dev, max_pages,    page_size,
-                           free_pages_dev, free_cap,     free_count_dev,
-                           free_count_out_dev, seq_lens_out_dev, err_flag_dev};
-  cudaGetLastError();
-  return launch_status(dsa::launch_pages_release(a, sms, static_cast<cudaStream_t>(stream)));
+  if (shared_pages_dev == nullptr) return DSA_ERR_NULL;
+  if (!aligned(shared_pages_dev, 4)) return DSA_ERR_ALIGN;
+  return release_pages({finished_dev, shared_pages_dev, seq_lens_dev, B, page_table_dev, max_pages, page_size,
+                        free_pages_dev, free_cap, free_count_dev, free_count_out_dev, seq_lens_out_dev, err_flag_dev},
+                       stream);
 }
 
 int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t pos_stride, int T, int H,

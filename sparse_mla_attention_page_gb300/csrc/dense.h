@@ -33,6 +33,7 @@ bool launch_pages_extend(const ExtendArgs& a, int sms, cudaStream_t stream);
 
 struct ReleaseArgs {
   const uint8_t* finished;
+  const int32_t* shared;  // leading pages of each request that it does not own; nullptr: none
   const int32_t* seq_lens;
   int B;
   const int32_t* page_table;

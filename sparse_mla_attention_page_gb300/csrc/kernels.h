@@ -82,6 +82,36 @@ void launch_gather_dequant(const GatherArgs& g, int sms, cudaStream_t stream);
 // Merges the partial results of split units (after the attention kernel).
 void launch_combine(const AttnArgs& a, cudaStream_t stream);
 
+// Writer of 4-bit rows (kv_fp4.cu).
+struct Fp4WriteArgs {
+  const uint16_t* kv_c;   // BF16 [n_rows, 512]
+  int64_t kv_stride;
+  const uint16_t* k_pe;   // BF16 [n_rows, 64]; nullptr: 288-byte rows
+  int64_t k_pe_stride;
+  int64_t n_rows;
+  const int64_t* slots;
+  uint8_t* pool;
+  int64_t pool_rows;
+  int32_t* err;
+};
+void launch_kv_write_fp4(const Fp4WriteArgs& a, int sms, cudaStream_t stream);
+
+// Reader of requests' rows (kv_read.cu).
+struct KvReadArgs {
+  const uint8_t* pool;
+  int64_t pool_rows;
+  int layout;
+  const int32_t* page_table;
+  int B, max_pages, page_size;
+  const int32_t* cu_rows; // [B + 1] rows of out
+  const int32_t* starts;  // [B] first rows read, or nullptr
+  uint16_t* out;          // BF16 [out_rows, 512 or 576], rows out_stride apart
+  int64_t out_rows, out_stride;
+  int32_t* err;
+};
+// false when nothing was launched
+bool launch_kv_read(const KvReadArgs& a, int sms, cudaStream_t stream);
+
 // DSA_OK and the SM count when the current device has compute capability
 // 10.3, else DSA_ERR_DEVICE.
 int current_device_sms(int* sms);

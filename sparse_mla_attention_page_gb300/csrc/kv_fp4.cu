@@ -1,0 +1,109 @@
+// The writer of 4-bit rows (fp4_rows.cuh): new BF16 latent rows, and their RoPE
+// dims, quantised and scattered into the paged pool.
+//
+// For each group of 128 dims s = amax / 384 (FP32, IEEE), y = x / s; for each
+// block of 16 dims e is the smallest of 0 .. 11 with max |y| <= 7 2^(e - 5),
+// and code = E2M1(y 2^(5 - e)).  7 and not 6: a value between 6 and 7 is off by
+// at most 1 as the code 6 of the smaller exponent and by as much under the
+// larger one, which would cost the block's other dims a bit.
+//
+// HBM-bound: 1024 (1152) bytes read and 288 (416) written a row.  A warp per
+// row, lane l dims [8 l, 8 l + 8) and 256 + the same, so that each load
+// instruction reads 512 contiguous bytes and each store writes 128 or more.
+// Two lanes hold a block, sixteen a group.
+#include "dsa_common.cuh"
+#include "fp4_rows.cuh"
+#include "kernels.h"
+#include "row_codec.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint32_t max_bits(uint32_t v, int lanes) {
+  for (int o = lanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Eight dims of this lane (one of a block's two and a group's sixteen): their
+// word, the block's exponent nibble and the group's scale.
+__device__ __forceinline__ void quantise8(float* v, uint32_t& word, uint32_t& e, float& s) {
+  uint32_t top = 0;                    // as bits: a NaN is the largest
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+  const uint32_t block = max_bits(top, 2), group = max_bits(block, 16);
+  const bool odd = group >= 0x7F800000u;
+  s = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(__uint_as_float(group), kFp4Top);
+  const bool none = odd || s == 0.f;
+  const float y = none ? 0.f : __fdiv_rn(__uint_as_float(block), s);
+  e = 0;
+#pragma unroll
+  for (int k = 0; k < 11; ++k) e += y > 0.21875f * (float)(1 << k);      // 7 2^-5, 7 2^-4, ..
+  const float up = __uint_as_float((127u + 5u - e) << 23);               // 2^(5 - e)
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = none ? copysignf(0.f, v[k]) : __fdiv_rn(v[k], s) * up;
+  word = fp4_word(v);
+}
+
+template <bool kRope>
+__global__ void __launch_bounds__(kThreads, 4) kv_write_fp4_kernel(const __grid_constant__ Fp4WriteArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");        // as the other writers
+  constexpr int kRow = kRope ? kFp4RopeRow : kFp4Row;
+  const int lane = threadIdx.x & 31;
+  const int64_t n_warps = ((int64_t)gridDim.x * kThreads) >> 5;
+  auto put = [&](int64_t slot, Row16& r, uint32_t rope) {
+    if (slot < 0) return;
+    if (slot >= a.pool_rows) {
+      if (lane == 0) set_err(a.err, DSA_DEV_ERR_SLOT_RANGE);
+      return;
+    }
+    uint32_t w[2], e[2];
+    float s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) quantise8(r.v + 8 * h, w[h], e[h], s[h]);
+    uint8_t* row = a.pool + slot * kRow;
+    reinterpret_cast<uint32_t*>(row)[lane] = w[0];
+    reinterpret_cast<uint32_t*>(row + 128)[lane] = w[1];
+    if (kRope) reinterpret_cast<uint32_t*>(row + kFp4Row)[lane] = rope;
+    // nibble l / 2 of each half, from both lanes of a block
+    const int at = (lane >> 1 & 7) * 4;
+    uint4 x;
+    x.x = __reduce_or_sync(0xffffffffu, lane < 16 ? e[0] << at : 0u);
+    x.y = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : e[0] << at);
+    x.z = __reduce_or_sync(0xffffffffu, lane < 16 ? e[1] << at : 0u);
+    x.w = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : e[1] << at);
+    const float s1 = __shfl_sync(0xffffffffu, s[0], 16), s3 = __shfl_sync(0xffffffffu, s[1], 16);
+    if (lane == 0) {
+      *reinterpret_cast<float4*>(row + kFp4Scales) = make_float4(s[0], s1, s[1], s3);
+      *reinterpret_cast<uint4*>(row + kFp4Exps) = x;
+    }
+  };
+  auto rope_of = [&](int64_t i) {
+    return kRope ? __ldcs(reinterpret_cast<const uint32_t*>(a.k_pe + i * a.k_pe_stride) + lane) : 0u;
+  };
+  // two rows per warp and pass, all loads issued before any is used
+  for (int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i0 < a.n_rows; i0 += 2 * n_warps) {
+    const int64_t i1 = i0 + n_warps;
+    const bool two = i1 < a.n_rows;
+    const int64_t s0 = __ldg(a.slots + i0), s1 = two ? __ldg(a.slots + i1) : -1;
+    Row16 r0, r1;
+    load_row16(a.kv_c + i0 * a.kv_stride, lane, r0);
+    if (two) load_row16(a.kv_c + i1 * a.kv_stride, lane, r1);
+    const uint32_t p0 = rope_of(i0), p1 = two ? rope_of(i1) : 0u;
+    put(s0, r0, p0);
+    if (two) put(s1, r1, p1);
+  }
+}
+
+}  // namespace
+
+void launch_kv_write_fp4(const Fp4WriteArgs& a, int sms, cudaStream_t stream) {
+  // sixteen rows a block and pass, at most one wave of four blocks per SM
+  const int64_t blocks = (a.n_rows + 15) / 16, cap = (int64_t)sms * 4;
+  const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
+  if (a.k_pe != nullptr) kv_write_fp4_kernel<true><<<grid, kThreads, 0, stream>>>(a);
+  else kv_write_fp4_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+}
+
+}  // namespace dsa

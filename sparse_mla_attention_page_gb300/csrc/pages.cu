@@ -123,15 +123,16 @@ __global__ void __launch_bounds__(kThreads, 1) pages_release_kernel(const __grid
   const int32_t count = *static_cast<const volatile int32_t*>(a.free_count);   // read once: the output may alias it
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  auto kept = [&](int b) { return a.shared != nullptr ? __ldg(a.shared + b) : 0; };
   auto back = [&](int b) -> int64_t {
     const int64_t s = a.seq_lens[b];
-    return a.finished[b] && s > 0 ? pages_of(s, a.page_size) : 0;
+    return a.finished[b] && s > 0 ? max((int64_t)0, pages_of(s, a.page_size) - kept(b)) : 0;
   };
   bool bad = count < 0 || count > a.free_cap;
   int64_t pages = 0;
   for (int b = b0; b < b1; ++b) {
     const int64_t s = a.seq_lens[b];
-    bad |= s < 0 || s > room;
+    bad |= s < 0 || s > room || kept(b) < 0;
     pages += back(b);
   }
   int64_t all_pages;
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_release_kernel(const __grid
     bool bad_page = false;
     for (int k = gtid; k < n_pages; k += gsize) {
       const int b = scan_owner(page0, a.B, k);
-      const int32_t page = __ldg(a.page_table + (int64_t)b * a.max_pages + (k - page0[b]));
+      const int32_t page = __ldg(a.page_table + (int64_t)b * a.max_pages + kept(b) + (k - page0[b]));
       bad_page |= page < 0;
       a.free_pages[count + k] = page;
     }
