@@ -222,7 +222,7 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
                    void* stream) {
   if (T < 0 || pool_rows < 0) return DSA_ERR_SHAPE;
   if (dsa_kv_row_bytes(layout) == 0) return DSA_ERR_LAYOUT;
-  const int width = layout == DSA_KV_ROPE656 ? 576 : 512;
+  const int width = layout == DSA_KV_ROPE656 || layout == DSA_KV_FP4_416 ? 576 : 512;
   if (D != width || kv_row_dim != width) return DSA_ERR_ROW_WIDTH;
   if (H < 1 || H > 1024) return DSA_ERR_HEADS;
   if (T == 0) return DSA_OK;

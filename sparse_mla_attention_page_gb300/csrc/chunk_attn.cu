@@ -55,6 +55,9 @@
 // nothing is rounded but P itself.)  RoPE dims are one more pass, BF16, with
 // the row's power of two in the query.
 //
+// 4-bit rows expand to the bytes and scales of the 528-byte rows before they
+// reach the ring (expand_role), and everything behind it is as for those.
+//
 // Warp roles: 16 softmax warps (warp w: TMEM lane quarter w % 4 = 32 keys of
 // the tile, column quarter w / 4), one issuing thread for each product, and
 // producers that translate keys to rows and bring them into a ring of 16 KB
@@ -79,6 +82,7 @@
 #include "chunk.cuh"
 #include "chunk_plan.cuh"
 #include "dsa_common.cuh"
+#include "fp4_rows.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
@@ -128,11 +132,19 @@ struct Misc {
 constexpr int kMiscBytes = 5120;
 static_assert(sizeof(Misc) <= kMiscBytes, "misc area");
 
+constexpr int row_bytes(int layout) {
+  return layout == DSA_KV_RAW512 ? kRawRow : layout == DSA_KV_SCALED528 ? kScaledRow : layout == DSA_KV_ROPE656 ? kRopeRow
+         : layout == DSA_KV_FP4_288 ? kFp4Row : kFp4RopeRow;
+}
+
 template <int NC, int kLayout, bool kTma>
 struct Cfg {
   static constexpr bool kScaled = kLayout != DSA_KV_RAW512;
-  static constexpr bool kRope = kLayout == DSA_KV_ROPE656;
-  static constexpr int R = kLayout == DSA_KV_RAW512 ? kRawRow : kLayout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
+  static constexpr bool kFp4 = kLayout == DSA_KV_FP4_288 || kLayout == DSA_KV_FP4_416;
+  static constexpr bool kRope = kLayout == DSA_KV_ROPE656 || kLayout == DSA_KV_FP4_416;
+  static constexpr int R = row_bytes(kLayout);
+  static constexpr int ROPE_AT = kFp4 ? kFp4Row : kScaledRow;    // byte of a row
+  static_assert(!(kFp4 && kTma), "4-bit rows are expanded by threads");
   static constexpr int CPT = NC / 4;                 // query columns of a softmax thread
   // Registers: the launch gives every thread LAUNCH_REGS; the softmax warps
   // then take SMX_REGS and the others give back to OTHER_REGS.
@@ -163,10 +175,14 @@ struct Cfg {
   // each thread of a group: three groups of two warps run raw and scaled rows
   // 8 and 6 % faster than one of six (1024 tokens of 16 heads over 8192: 374
   // against 405 us, 493 against 525); with the RoPE block they lose 8 %.
-  static constexpr int GROUPS = kRope ? 1 : 3;
+  static constexpr int GROUPS = kRope || kFp4 ? 1 : 3;
   static constexpr int GW = kProdWarps / GROUPS, QW = (kQuads + GW - 1) / GW;
   static_assert(kProdWarps % GROUPS == 0 && GW % 2 == 0, "rows of a thread share their place in the swizzle");
-  static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES + ROPE_BYTES;
+  // Of the producers that expand 4-bit rows: scales and exponents of two tiles
+  // (32 bytes a key), rows of three.
+  static constexpr int TAIL_BYTES = kFp4 ? 2 * kTile * 32 : 0, AHEAD_BYTES = kFp4 ? 3 * kTile * 4 : 0;
+  static constexpr int FULL_ARRIVALS = kTma ? 1 : kFp4 ? kProdWarps : 32 * GW;
+  static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES + ROPE_BYTES + TAIL_BYTES + AHEAD_BYTES;
   static constexpr int NS_FIT = (kSmemLimit - FIXED - NPB * P_BYTES) / kBlock;
   static constexpr int NS = NS_FIT < kMaxBlocks ? NS_FIT : kMaxBlocks;
   static constexpr int ROPE_OFF = NS * kBlock;
@@ -174,7 +190,9 @@ struct Cfg {
   static constexpr int QR_OFF = Q_OFF + Q_BYTES;
   static constexpr int P_OFF = QR_OFF + QR_BYTES;
   static constexpr int SC_OFF = P_OFF + NPB * P_BYTES;
-  static constexpr int MISC_OFF = SC_OFF + SC_BYTES;
+  static constexpr int TAIL_OFF = SC_OFF + SC_BYTES;
+  static constexpr int AHEAD_OFF = TAIL_OFF + TAIL_BYTES;
+  static constexpr int MISC_OFF = AHEAD_OFF + AHEAD_BYTES;
   static constexpr int SMEM = MISC_OFF + kMiscBytes + 1024;
   static_assert(NS > 4, "a tile's blocks and one more");
   static_assert(NS * kBlock >= kPlanScratch, "the plan's scratch lies in the ring");
@@ -504,6 +522,173 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
         phase ^= 1;
       }
     }
+  }
+  cp_async_wait_all();
+}
+
+// The producers of 4-bit rows: they expand them to the E4M3 bytes of a 528-byte
+// row (fp4_rows.cuh) on their way into the ring.  A warp takes four rows at a
+// time (lane: 16 dims of one of them), six of them a block at most.  Codes come
+// two blocks ahead into registers, 24 of them, from lines that were requested
+// into the L2 cache a tile ahead; scales and exponents a tile ahead into shared
+// memory.  (Codes staged in shared memory as well would take two of the ring's
+// blocks.)  About 30 instructions for 16 dims of four rows, 960 issue cycles of a
+// tile's 3000 to 4000.
+template <int NC, int kLayout>
+__device__ void expand_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const Range& rg) {
+  using C = Cfg<NC, kLayout, false>;
+  constexpr int kMine = (kQuads + kProdWarps - 1) / kProdWarps;     // quads of rows of a warp
+  const ChunkArgs& a = w.a;
+  const int ptid = threadIdx.x - kProdWarp0 * 32, pw = ptid >> 5, lane = ptid & 31;
+  const int rq = lane >> 3, ch = lane & 7;
+  volatile int* abort = &ms.abort;
+  const uint32_t kv0 = smem_u32(sm);
+  int32_t (*ahead)[kTile] = reinterpret_cast<int32_t(*)[kTile]>(sm + C::AHEAD_OFF);   // pool rows of tile t in ahead[t % 3]
+  uint8_t* tails = sm + C::TAIL_OFF;                                                  // tile t's in half t % 2
+  Walk cur(w, ms, ptid);
+  int32_t entry = -1, off = 0;
+  bool seen = false;
+  auto look_up = [&]() {       // thread -> key ptid of the walk's tile
+    const int j = cur.tile * kTile + ptid;
+    seen = ptid < kTile && j < cur.last;
+    if (seen) {
+      const int page = j / a.page_size;
+      off = j - page * a.page_size;
+      entry = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
+    }
+  };
+  // the looked-up key's row; its codes are requested into L2
+  auto resolve = [&](int tile) -> int32_t {
+    int32_t row = -1;
+    if (seen) {
+      const int64_t r = (int64_t)entry * a.page_size + off;
+      if (entry < 0 || r >= a.pool_rows) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
+      else row = (int32_t)r;
+    }
+    if (ptid < kTile) ahead[tile % 3][ptid] = row;
+    if (row >= 0) {
+      const uint8_t* p = a.pool + (int64_t)row * C::R;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 128));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + C::R - 1));
+    }
+    return row;
+  };
+  // scales and exponents of key ptid of a tile
+  auto request_tail = [&](int tile, int32_t row) {
+    if (ptid >= kTile) return;
+    const uint8_t* p = a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kFp4Scales;
+    const uint32_t dst = smem_u32(tails + ((tile & 1) * kTile + ptid) * 32), n = row >= 0 ? 16u : 0u;
+    cp_async_16_zfill(dst, p, n);
+    cp_async_16_zfill(dst + 16, p + 16, n);
+  };
+  uint2 code[2][kMine];
+  auto load = [&](int buf, int tile, int k) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int q = pw + i * kProdWarps;
+      const int32_t row = q < kQuads ? ahead[tile % 3][4 * q + rq] : -1;
+      code[buf][i] = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.pool + (int64_t)row * C::R + k * 64) + ch) : make_uint2(0, 0);
+    }
+  };
+  int slot = 0, phase = 0, seg = 0;
+  bool ok = true;              // false once a wait gave up: keep going through every barrier
+  auto acquire = [&]() {
+    ok = ok && mbar_wait(smem_u32(&ms.empty[slot]), phase ^ 1, abort, w.wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+  };
+  auto rope = [&](int it) {    // RoPE dims of tile it, once the score product has read the ones before
+    if (!C::kRope) return;
+    ok = ok && mbar_wait(smem_u32(&ms.rope_empty), (it & 1) ^ 1, abort, w.wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int q = pw + i * kProdWarps;
+      if (q >= kQuads) break;
+      const int r = 4 * q + rq;
+      const int32_t row = ahead[it % 3][r];
+      cp_async_16_zfill(kv0 + C::ROPE_OFF + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4),
+                        a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + C::ROPE_AT + ch * 16, row >= 0 ? 16u : 0u);
+    }
+    cp_async_arrive_noinc(smem_u32(&ms.rope_full));
+  };
+  // of the tile that is expanded, and of the one behind it: row of key ptid, whether the tile opens a segment, word of its unit
+  int32_t row = -1, row_next = -1, word = 0, word_next = 0;
+  bool opens = true, opens_next = false;
+  auto step = [&](int tile) {  // the walk to the given tile
+    if (tile >= rg.n_it) return;
+    opens_next = cur.advance(w, ptid);
+    word_next = cur.word;
+    look_up();
+  };
+  look_up();
+  row = resolve(0);
+  step(1);
+  named_bar_sync(kProdBar, kProdThreads);
+  request_tail(0, row);
+  load(0, 0, 0);
+  load(1, 0, 1);
+  rope(0);
+  for (int it = 0; it < rg.n_it; ++it) {
+    const int m = it % kMeta;
+    const bool more = it + 1 < rg.n_it;
+    if (more) row_next = resolve(it + 1);
+    cp_async_wait_all();
+    acquire();
+    const uint8_t* tail = tails + (it & 1) * kTile * 32;
+    if (ptid < kTile) {
+      ms.rows[m][ptid] = row;
+      *reinterpret_cast<uint4*>(sm + C::SC_OFF + (m * kTile + ptid) * 16) = *reinterpret_cast<const uint4*>(tail + ptid * 32);
+    }
+    // no unit is published once a wait has given up (as in producer_role)
+    if (opens && seg > 0) ok = __all_sync(0xffffffffu, ok && *abort == 0);
+    const bool opened = opens;
+    if (opens) {
+      if (ok && seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = word;
+      ++seg;
+    }
+    const bool whole = named_bar_red_or(kProdBar, kProdThreads, ptid < kTile && row < 0) == 0;
+    if (ptid == 0 && ok) {
+      ms.clean[m] = whole;
+      mbar_arrive(smem_u32(&ms.meta_full[m]));
+      if (opened && seg > 1) prefetch_queries(a, ms.unit[(seg - 1) % kSegs]);
+    }
+    if (more) {
+      request_tail(it + 1, row_next);
+      row = row_next;
+      opens = opens_next;
+      word = word_next;
+      step(it + 2);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k > 0) acquire();
+      if (ok) {
+        uint8_t* block = sm + slot * kBlock;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int q = pw + i * kProdWarps;
+          if (q >= kQuads) break;
+          const int r = 4 * q + rq;
+          const uint32_t e = *reinterpret_cast<const uint32_t*>(tail + r * 32 + 16 + 4 * k) >> 4 * ch & 15;
+          const Fp4Lut lut(e);
+          uint4 x;
+          fp4_expand8(code[k & 1][i].x, lut, x.x, x.y);
+          fp4_expand8(code[k & 1][i].y, lut, x.z, x.w);
+          *reinterpret_cast<uint4*>(block + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4)) = x;
+        }
+        fence_proxy_async_smem();
+        warp_arrive(smem_u32(&ms.full[slot]));
+      }
+      if (k < 2) load(k & 1, it, k + 2);
+      else if (more) load(k & 1, it + 1, k - 2);
+      if (++slot == C::NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+    if (more) rope(it + 1);
   }
   cp_async_wait_all();
 }
@@ -1201,10 +1386,10 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(smem_u32(&ms.full[s]), kTma ? 1 : 32 * C::GW);
+      mbar_init(smem_u32(&ms.full[s]), C::FULL_ARRIVALS);
       mbar_init(smem_u32(&ms.empty[s]), 1);
     }
-    for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), 1 + (C::kScaled && !kTma ? kProdThreads : 0));
+    for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), 1 + (C::kScaled && !kTma && !C::kFp4 ? kProdThreads : 0));
     for (int s = 0; s < C::SBUF; ++s) {
       mbar_init(smem_u32(&ms.s_full[s]), 1);
       mbar_init(smem_u32(&ms.s_free[s]), kSmxWarps);
@@ -1245,6 +1430,7 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
       regs_dec<C::OTHER_REGS>();
       if (warp == kQkWarp) qk_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
       else if (warp == kPvWarp) pv_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
+      else if constexpr (C::kFp4) expand_role<NC, kLayout>(w, sm, ms, rg);
       else if constexpr (!kTma) producer_role<NC, kLayout, kTma>(w, sm, ms, rg);
       else if (warp == kProdWarp0) tma_role<NC, kLayout, kTma>(w, maps, sm, ms, rg);
     }
@@ -1325,7 +1511,9 @@ template <int NC>
 bool launch_nc(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
   if (w.a.layout == DSA_KV_RAW512) return launch_layout<NC, DSA_KV_RAW512>(w, maps, stream);
   if (w.a.layout == DSA_KV_SCALED528) return launch_layout<NC, DSA_KV_SCALED528>(w, maps, stream);
-  return launch_layout<NC, DSA_KV_ROPE656>(w, maps, stream);
+  if (w.a.layout == DSA_KV_ROPE656) return launch_layout<NC, DSA_KV_ROPE656>(w, maps, stream);
+  if (w.a.layout == DSA_KV_FP4_288) return launch<NC, DSA_KV_FP4_288, false>(w, maps, stream);
+  return launch<NC, DSA_KV_FP4_416, false>(w, maps, stream);
 }
 
 }  // namespace
@@ -1348,13 +1536,14 @@ bool launch_chunk_attn(const ChunkWork& work, cudaStream_t stream) {
   const int page = w.a.page_size;
   int shift = 0;
   while (shift < 7 && page % (2 << shift) == 0) ++shift;
-  w.box_shift = shift >= 5 ? shift : 0;
+  const bool fp4 = w.a.layout == DSA_KV_FP4_288 || w.a.layout == DSA_KV_FP4_416;
+  w.box_shift = shift >= 5 && !fp4 ? shift : 0;
   w.unit_cost = chunk_unit_cost(w.a.layout);
   ChunkMaps maps{};
   if (w.box_shift > 0) {
-    const int row_bytes = w.a.layout == DSA_KV_RAW512 ? kRawRow : w.a.layout == DSA_KV_SCALED528 ? kScaledRow : kRopeRow;
-    if (!encode_rows(&maps.rows, w.a, row_bytes, 128, 1 << w.box_shift, true)) return false;
-    if (w.a.layout != DSA_KV_RAW512 && !encode_rows(&maps.scales, w.a, row_bytes, 16, 1 << w.box_shift, false)) return false;
+    const int bytes = row_bytes(w.a.layout);
+    if (!encode_rows(&maps.rows, w.a, bytes, 128, 1 << w.box_shift, true)) return false;
+    if (w.a.layout != DSA_KV_RAW512 && !encode_rows(&maps.scales, w.a, bytes, 16, 1 << w.box_shift, false)) return false;
   }
   return w.nc == 16 ? launch_nc<16>(w, maps, stream) : launch_nc<32>(w, maps, stream);
 }

@@ -64,3 +64,29 @@ def decode(rows):
     exps = np.stack([rows[:, 272:288] & 15, rows[:, 272:288] >> 4], -1).reshape(n, 32).astype(np.int64)
     val = val.reshape(n, 32, 16) * 2.0 ** (exps[..., None] - 5)
     return val.reshape(n, 512), np.ascontiguousarray(rows[:, 256:272]).view("<f4").astype(np.float64)
+
+
+def expand(rows):
+    """The 528- (656-) byte rows of the same values, as a CPU uint8 tensor."""
+    import torch
+    rows = np.asarray(rows)
+    code, _ = decode(rows)
+    e4m3 = torch.from_numpy(code).to(torch.float8_e4m3fn)
+    assert (e4m3.double() == torch.from_numpy(code)).all()       # nothing is rounded
+    parts = [e4m3.view(torch.uint8), torch.from_numpy(np.ascontiguousarray(rows[:, 256:272]))]
+    if rows.shape[1] == 416:
+        parts.append(torch.from_numpy(np.ascontiguousarray(rows[:, 288:])))
+    return torch.cat(parts, 1)
+
+
+def make_pool(rows, layout, gen, amp=1.0):
+    """Random 4-bit rows as a CPU uint8 tensor: every code, exponents a few steps apart, a magnitude for each row."""
+    import torch
+    pool = torch.randint(0, 256, (rows, ROW_BYTES[layout]), generator=gen, dtype=torch.uint8)
+    e = torch.randint(6, 12, (rows, 16, 2), generator=gen)
+    pool[:, 272:288] = (e[..., 0] | e[..., 1] << 4).to(torch.uint8)
+    s = amp * (0.1 + 3.9 * torch.rand(rows, 1, generator=gen)) * (0.5 + torch.rand(rows, 4, generator=gen)) / 100.0
+    pool[:, 256:272] = s.view(torch.uint8)
+    if layout == "fp4_416":
+        pool[:, 288:] = torch.randn(rows, 64, generator=gen).to(torch.bfloat16).view(torch.uint8)
+    return pool
