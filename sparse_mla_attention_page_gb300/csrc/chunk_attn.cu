@@ -55,8 +55,8 @@
 // nothing is rounded but P itself.)  RoPE dims are one more pass, BF16, with
 // the row's power of two in the query.
 //
-// 4-bit rows expand to the bytes and scales of the 528-byte rows before they
-// reach the ring (expand_role), and everything behind it is as for those.
+// 4-bit rows expand to the bytes and scales of the 528-byte rows in the ring
+// (fp4_expand_role), and everything behind it is as for those.
 //
 // Warp roles: 16 softmax warps (warp w: TMEM lane quarter w % 4 = 32 keys of
 // the tile, column quarter w / 4), one issuing thread for each product, and
@@ -106,10 +106,14 @@ constexpr int kSegs = 6;                     // segments whose units are kept
 constexpr int kMaxSBuf = 4;                  // score buffers
 constexpr int kProdBar = 8;                  // named barriers: 1 + column quarter, producers
 constexpr int kMaxBlocks = 12;
+constexpr int kCopyWarps = 2, kCopyThreads = 32 * kCopyWarps;    // of 4-bit rows
+constexpr int kExpandWarps = kProdWarps - kCopyWarps;
+constexpr int kMaxStage = 5, kHalf = kBlock / 2;
 constexpr int kSmemLimit = 232448;
 
 struct Misc {
   uint64_t full[kMaxBlocks], empty[kMaxBlocks];
+  uint64_t raw_full[kMaxStage], raw_empty[kMaxStage];   // codes of a block of 4-bit rows
   uint64_t rope_full, rope_empty;  // the tile's RoPE block (a buffer of its own: it is free long before the others)
   uint64_t meta_full[kMeta];       // rows (and scales) of a tile are in place
   uint64_t s_full[kMaxSBuf], s_free[kMaxSBuf];
@@ -178,11 +182,13 @@ struct Cfg {
   static constexpr int GROUPS = kRope || kFp4 ? 1 : 3;
   static constexpr int GW = kProdWarps / GROUPS, QW = (kQuads + GW - 1) / GW;
   static_assert(kProdWarps % GROUPS == 0 && GW % 2 == 0, "rows of a thread share their place in the swizzle");
-  // Of the producers that expand 4-bit rows: scales and exponents of two tiles
-  // (32 bytes a key), rows of three.
-  static constexpr int TAIL_BYTES = kFp4 ? 2 * kTile * 32 : 0, AHEAD_BYTES = kFp4 ? 3 * kTile * 4 : 0;
-  static constexpr int FULL_ARRIVALS = kTma ? 1 : kFp4 ? kProdWarps : 32 * GW;
-  static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES + ROPE_BYTES + TAIL_BYTES + AHEAD_BYTES;
+  static constexpr int EX_BYTES = kFp4 ? 2 * kTile * 16 : 0;          // exponents of 4-bit rows, of two tiles
+  static constexpr int NST = kFp4 ? 4 : 0;                    // staging buffers of their codes
+  static constexpr int ST_BYTES = NST * kHalf;
+  static constexpr int FULL_ARRIVALS = kTma ? 1 : kFp4 ? kExpandWarps : 32 * GW;
+  static constexpr int ROPE_ARRIVALS = kTma ? 1 : kFp4 ? kCopyThreads : 32 * GW;
+  static constexpr int META_ARRIVALS = 1 + (!kScaled || kTma ? 0 : kFp4 ? kCopyThreads : kProdThreads);
+  static constexpr int FIXED = kMiscBytes + 1024 + Q_BYTES + QR_BYTES + SC_BYTES + ROPE_BYTES + EX_BYTES + ST_BYTES;
   static constexpr int NS_FIT = (kSmemLimit - FIXED - NPB * P_BYTES) / kBlock;
   static constexpr int NS = NS_FIT < kMaxBlocks ? NS_FIT : kMaxBlocks;
   static constexpr int ROPE_OFF = NS * kBlock;
@@ -190,14 +196,17 @@ struct Cfg {
   static constexpr int QR_OFF = Q_OFF + Q_BYTES;
   static constexpr int P_OFF = QR_OFF + QR_BYTES;
   static constexpr int SC_OFF = P_OFF + NPB * P_BYTES;
-  static constexpr int TAIL_OFF = SC_OFF + SC_BYTES;
-  static constexpr int AHEAD_OFF = TAIL_OFF + TAIL_BYTES;
-  static constexpr int MISC_OFF = AHEAD_OFF + AHEAD_BYTES;
+  static constexpr int EX_OFF = SC_OFF + SC_BYTES;
+  static constexpr int ST_OFF = EX_OFF + EX_BYTES;
+  static constexpr int MISC_OFF = ST_OFF + ST_BYTES;
   static constexpr int SMEM = MISC_OFF + kMiscBytes + 1024;
   static_assert(NS > 4, "a tile's blocks and one more");
   static_assert(NS * kBlock >= kPlanScratch, "the plan's scratch lies in the ring");
   // a tile's rows are replaced kMeta tiles later, when its blocks are gone from the ring
   static_assert((NS - 1) / 4 + 1 < kMeta, "rows of a tile in use");
+  // (4-bit rows: when tile t's first codes are requested, block 4 t - NST is expanded, the last of tile t - 2 or
+  // a later one, so that 4 t - NST - NS is gone)
+  static_assert(NST + NS <= 4 * kMeta - 3 && NST <= kMaxStage, "rows of a tile in use");
   static_assert(SMEM <= kSmemLimit && TMEM_USED <= 512 && P_GROUP % 1024 == 0 && QR_BYTES % 1024 == 0, "budgets");
 };
 
@@ -526,171 +535,173 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
   cp_async_wait_all();
 }
 
-// The producers of 4-bit rows: they expand them to the E4M3 bytes of a 528-byte
-// row (fp4_rows.cuh) on their way into the ring.  A warp takes four rows at a
-// time (lane: 16 dims of one of them), six of them a block at most.  Codes come
-// two blocks ahead into registers, 24 of them, from lines that were requested
-// into the L2 cache a tile ahead; scales and exponents a tile ahead into shared
-// memory.  (Codes staged in shared memory as well would take two of the ring's
-// blocks.)  About 30 instructions for 16 dims of four rows, 960 issue cycles of a
-// tile's 3000 to 4000.
+// 4-bit rows, by two warps that copy and four that expand.  The copies bring the
+// codes of a block (64 bytes of every row) into one of NST staging buffers; the
+// expanding warps turn them into the E4M3 bytes of a 528-byte row (fp4_rows.cuh)
+// in a slot of the ring.  So what is on its way from memory takes half the room,
+// and a ring block the shorter way through expansion, scores, softmax and values.
+// us, 1024 tokens of 32 heads over 8192 (288 / 416 bytes) and 64 single tokens of
+// 16 heads over up to 8192 (288): 1280 / 1670 and 64.6 (528-byte rows one by one
+// 968 and 60.5, by TMA 853 and 58.5).  Tried before: six warps that load codes
+// into registers two blocks ahead and expand those 1990 / 2110 and 95; codes of two
+// blocks copied into the ring and expanded in place 1671 / 2255 and 75.  Staging
+// buffers 2 / 3 / 4 / 5, at 288 bytes: 1275 / 1296 / 1279 / 1345, 74.9 / 68.7 / 64.6
+// / 64.6.  Without the expansion's arithmetic: 1138 / 1609 and 61.6.
 template <int NC, int kLayout>
-__device__ void expand_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const Range& rg) {
+__device__ void fp4_copy_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const Range& rg) {
   using C = Cfg<NC, kLayout, false>;
-  constexpr int kMine = (kQuads + kProdWarps - 1) / kProdWarps;     // quads of rows of a warp
+  constexpr int kKeys = kTile / kCopyThreads;      // of a thread
   const ChunkArgs& a = w.a;
   const int ptid = threadIdx.x - kProdWarp0 * 32, pw = ptid >> 5, lane = ptid & 31;
-  const int rq = lane >> 3, ch = lane & 7;
   volatile int* abort = &ms.abort;
-  const uint32_t kv0 = smem_u32(sm);
-  int32_t (*ahead)[kTile] = reinterpret_cast<int32_t(*)[kTile]>(sm + C::AHEAD_OFF);   // pool rows of tile t in ahead[t % 3]
-  uint8_t* tails = sm + C::TAIL_OFF;                                                  // tile t's in half t % 2
   Walk cur(w, ms, ptid);
-  int32_t entry = -1, off = 0;
-  bool seen = false;
-  auto look_up = [&]() {       // thread -> key ptid of the walk's tile
-    const int j = cur.tile * kTile + ptid;
-    seen = ptid < kTile && j < cur.last;
-    if (seen) {
-      const int page = j / a.page_size;
-      off = j - page * a.page_size;
-      entry = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
-    }
-  };
-  // the looked-up key's row; its codes are requested into L2
-  auto resolve = [&](int tile) -> int32_t {
-    int32_t row = -1;
-    if (seen) {
-      const int64_t r = (int64_t)entry * a.page_size + off;
-      if (entry < 0 || r >= a.pool_rows) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
-      else row = (int32_t)r;
-    }
-    if (ptid < kTile) ahead[tile % 3][ptid] = row;
-    if (row >= 0) {
-      const uint8_t* p = a.pool + (int64_t)row * C::R;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 128));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + C::R - 1));
-    }
-    return row;
-  };
-  // scales and exponents of key ptid of a tile
-  auto request_tail = [&](int tile, int32_t row) {
-    if (ptid >= kTile) return;
-    const uint8_t* p = a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + kFp4Scales;
-    const uint32_t dst = smem_u32(tails + ((tile & 1) * kTile + ptid) * 32), n = row >= 0 ? 16u : 0u;
-    cp_async_16_zfill(dst, p, n);
-    cp_async_16_zfill(dst + 16, p + 16, n);
-  };
-  uint2 code[2][kMine];
-  auto load = [&](int buf, int tile, int k) {
+  int32_t entry[kKeys], off[kKeys];
+  bool seen[kKeys];
+  auto look_up = [&]() {       // keys ptid, ptid + kCopyThreads, ... of the walk's tile
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int q = pw + i * kProdWarps;
-      const int32_t row = q < kQuads ? ahead[tile % 3][4 * q + rq] : -1;
-      code[buf][i] = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.pool + (int64_t)row * C::R + k * 64) + ch) : make_uint2(0, 0);
+    for (int i = 0; i < kKeys; ++i) {
+      const int j = cur.tile * kTile + ptid + i * kCopyThreads;
+      seen[i] = j < cur.last;
+      if (seen[i]) {
+        const int page = j / a.page_size;
+        off[i] = j - page * a.page_size;
+        entry[i] = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
+      }
     }
-  };
-  int slot = 0, phase = 0, seg = 0;
-  bool ok = true;              // false once a wait gave up: keep going through every barrier
-  auto acquire = [&]() {
-    ok = ok && mbar_wait(smem_u32(&ms.empty[slot]), phase ^ 1, abort, w.wait_ns);
-    ok = __all_sync(0xffffffffu, ok);
-  };
-  auto rope = [&](int it) {    // RoPE dims of tile it, once the score product has read the ones before
-    if (!C::kRope) return;
-    ok = ok && mbar_wait(smem_u32(&ms.rope_empty), (it & 1) ^ 1, abort, w.wait_ns);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return;
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int q = pw + i * kProdWarps;
-      if (q >= kQuads) break;
-      const int r = 4 * q + rq;
-      const int32_t row = ahead[it % 3][r];
-      cp_async_16_zfill(kv0 + C::ROPE_OFF + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4),
-                        a.pool + (int64_t)(row >= 0 ? row : 0) * C::R + C::ROPE_AT + ch * 16, row >= 0 ? 16u : 0u);
-    }
-    cp_async_arrive_noinc(smem_u32(&ms.rope_full));
-  };
-  // of the tile that is expanded, and of the one behind it: row of key ptid, whether the tile opens a segment, word of its unit
-  int32_t row = -1, row_next = -1, word = 0, word_next = 0;
-  bool opens = true, opens_next = false;
-  auto step = [&](int tile) {  // the walk to the given tile
-    if (tile >= rg.n_it) return;
-    opens_next = cur.advance(w, ptid);
-    word_next = cur.word;
-    look_up();
   };
   look_up();
-  row = resolve(0);
-  step(1);
-  named_bar_sync(kProdBar, kProdThreads);
-  request_tail(0, row);
-  load(0, 0, 0);
-  load(1, 0, 1);
-  rope(0);
+  int slot = 0, phase = 0, seg = 0;
+  bool ok = true;      // false once a wait gave up: keep going through every barrier
+  bool opens = true;   // the tile starts a segment
+  auto acquire = [&]() {
+    ok = ok && mbar_wait(smem_u32(&ms.raw_empty[slot]), phase ^ 1, abort, w.wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+  };
   for (int it = 0; it < rg.n_it; ++it) {
     const int m = it % kMeta;
-    const bool more = it + 1 < rg.n_it;
-    if (more) row_next = resolve(it + 1);
-    cp_async_wait_all();
     acquire();
-    const uint8_t* tail = tails + (it & 1) * kTile * 32;
-    if (ptid < kTile) {
-      ms.rows[m][ptid] = row;
-      *reinterpret_cast<uint4*>(sm + C::SC_OFF + (m * kTile + ptid) * 16) = *reinterpret_cast<const uint4*>(tail + ptid * 32);
+    bool none = false;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int key = ptid + i * kCopyThreads;
+      int32_t row = -1;
+      if (seen[i]) {
+        const int64_t r = (int64_t)entry[i] * a.page_size + off[i];
+        if (entry[i] < 0 || r >= a.pool_rows) set_err(a.err, DSA_DEV_ERR_PAGE_RANGE);
+        else row = (int32_t)r;
+      }
+      ms.rows[m][key] = row;
+      none |= row < 0;
+      const uint8_t* src = a.pool + (int64_t)max(row, 0) * C::R + kFp4Scales;
+      cp_async_16_zfill(smem_u32(sm + C::SC_OFF + (m * kTile + key) * 16), src, row >= 0 ? 16u : 0u);
+      cp_async_16_zfill(smem_u32(sm + C::EX_OFF + ((it & 1) * kTile + key) * 16), src + 16, row >= 0 ? 16u : 0u);
     }
     // no unit is published once a wait has given up (as in producer_role)
     if (opens && seg > 0) ok = __all_sync(0xffffffffu, ok && *abort == 0);
+    if (ok) cp_async_arrive_noinc(smem_u32(&ms.meta_full[m]));
     const bool opened = opens;
     if (opens) {
-      if (ok && seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = word;
+      if (ok && seg > 0 && ptid < Walk::kWords) reinterpret_cast<int32_t*>(&ms.unit[seg % kSegs])[ptid] = cur.word;
       ++seg;
     }
-    const bool whole = named_bar_red_or(kProdBar, kProdThreads, ptid < kTile && row < 0) == 0;
+    opens = cur.advance(w, ptid);
+    if (it + 1 < rg.n_it) look_up();
+    const bool whole = named_bar_red_or(kProdBar, kCopyThreads, none) == 0;
     if (ptid == 0 && ok) {
       ms.clean[m] = whole;
       mbar_arrive(smem_u32(&ms.meta_full[m]));
       if (opened && seg > 1) prefetch_queries(a, ms.unit[(seg - 1) % kSegs]);
     }
-    if (more) {
-      request_tail(it + 1, row_next);
-      row = row_next;
-      opens = opens_next;
-      word = word_next;
-      step(it + 2);
+    if (C::kRope) {    // eight lanes a row, into the swizzled block
+      ok = ok && mbar_wait(smem_u32(&ms.rope_empty), (it & 1) ^ 1, abort, w.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        const int r0 = 4 * pw + (lane >> 3), ch = lane & 7;
+        const uint32_t dst = smem_u32(sm + C::ROPE_OFF) + (r0 >> 3) * 1024 + (r0 & 7) * 128 + ((ch ^ (r0 & 7)) << 4);
+#pragma unroll 8
+        for (int i = 0; i < kTile / (4 * kCopyWarps); ++i) {
+          const int32_t pr = ms.rows[m][r0 + 4 * kCopyWarps * i];
+          cp_async_16_zfill(dst + i * kCopyWarps * 512, a.pool + (int64_t)max(pr, 0) * C::R + kFp4Row + ch * 16, pr >= 0 ? 16u : 0u);
+        }
+        cp_async_arrive_noinc(smem_u32(&ms.rope_full));
+      }
     }
+    constexpr int kMine = kTile / (8 * kCopyWarps);      // of a thread, four lanes a row
+    const int r0 = 8 * pw + (lane >> 2), ch = lane & 3;
+    int32_t pr[kMine];
 #pragma unroll
+    for (int i = 0; i < kMine; ++i) pr[i] = ms.rows[m][r0 + 8 * kCopyWarps * i];
+#pragma unroll 1
     for (int k = 0; k < 4; ++k) {
       if (k > 0) acquire();
       if (ok) {
-        uint8_t* block = sm + slot * kBlock;
+        const uint32_t dst = smem_u32(sm + C::ST_OFF + slot * kHalf) + r0 * 64 + ch * 16;
+        const uint8_t* src = a.pool + k * 64 + ch * 16;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int q = pw + i * kProdWarps;
-          if (q >= kQuads) break;
-          const int r = 4 * q + rq;
-          const uint32_t e = *reinterpret_cast<const uint32_t*>(tail + r * 32 + 16 + 4 * k) >> 4 * ch & 15;
-          const Fp4Lut lut(e);
-          uint4 x;
-          fp4_expand8(code[k & 1][i].x, lut, x.x, x.y);
-          fp4_expand8(code[k & 1][i].y, lut, x.z, x.w);
-          *reinterpret_cast<uint4*>(block + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4)) = x;
-        }
-        fence_proxy_async_smem();
-        warp_arrive(smem_u32(&ms.full[slot]));
+        for (int i = 0; i < kMine; ++i)
+          cp_async_16_zfill(dst + i * kCopyWarps * 512, src + (int64_t)max(pr[i], 0) * C::R, pr[i] >= 0 ? 16u : 0u);
+        cp_async_arrive_noinc(smem_u32(&ms.raw_full[slot]));
       }
-      if (k < 2) load(k & 1, it, k + 2);
-      else if (more) load(k & 1, it + 1, k - 2);
+      if (++slot == C::NST) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  cp_async_wait_all();
+}
+
+template <int NC, int kLayout>
+__device__ void fp4_expand_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const Range& rg) {
+  using C = Cfg<NC, kLayout, false>;
+  constexpr int kMine = kTile / (8 * kExpandWarps);    // rows of a thread: r0, r0 + 8 kExpandWarps, ...
+  const int pw = (threadIdx.x >> 5) - kProdWarp0 - kCopyWarps, lane = threadIdx.x & 31;
+  const int ch = lane & 3, r0 = 8 * pw + (lane >> 2);  // dims [32 ch, 32 ch + 32) of the block
+  volatile int* abort = &ms.abort;
+  const uint32_t x7 = r0 & 7, row0 = (r0 >> 3) * 1024 + x7 * 128;
+  const uint32_t to0 = row0 + (((2 * ch) ^ x7) << 4), to1 = row0 + (((2 * ch + 1) ^ x7) << 4);
+  int slot = 0, phase = 0, raw = 0, raw_phase = 0;
+  for (int it = 0; it < rg.n_it; ++it) {
+    const uint8_t* exps = sm + C::EX_OFF + ((it & 1) * kTile + r0) * 16 + ch;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      bool ok = mbar_wait(smem_u32(&ms.raw_full[raw]), raw_phase, abort, w.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const uint8_t* codes = sm + C::ST_OFF + raw * kHalf + r0 * 64 + ch * 16;
+      uint4 c[kMine];
+      uint32_t e[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        c[i] = *reinterpret_cast<const uint4*>(codes + i * kExpandWarps * 512);
+        e[i] = exps[4 * k + i * kExpandWarps * 128];
+      }
+      warp_arrive(smem_u32(&ms.raw_empty[raw]));
+      if (++raw == C::NST) {
+        raw = 0;
+        raw_phase ^= 1;
+      }
+      ok = mbar_wait(smem_u32(&ms.empty[slot]), phase ^ 1, abort, w.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      uint8_t* to = sm + slot * kBlock;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const Fp4Lut lo(e[i] & 15), hi(e[i] >> 4);
+        uint4 x, y;
+        fp4_expand8(c[i].x, lo, x.x, x.y);
+        fp4_expand8(c[i].y, lo, x.z, x.w);
+        fp4_expand8(c[i].z, hi, y.x, y.y);
+        fp4_expand8(c[i].w, hi, y.z, y.w);
+        *reinterpret_cast<uint4*>(to + to0 + i * kExpandWarps * 1024) = x;
+        *reinterpret_cast<uint4*>(to + to1 + i * kExpandWarps * 1024) = y;
+      }
+      fence_proxy_async_smem();
+      warp_arrive(smem_u32(&ms.full[slot]));
       if (++slot == C::NS) {
         slot = 0;
         phase ^= 1;
       }
     }
-    if (more) rope(it + 1);
   }
-  cp_async_wait_all();
 }
 
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
@@ -1389,7 +1400,11 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
       mbar_init(smem_u32(&ms.full[s]), C::FULL_ARRIVALS);
       mbar_init(smem_u32(&ms.empty[s]), 1);
     }
-    for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), 1 + (C::kScaled && !kTma && !C::kFp4 ? kProdThreads : 0));
+    for (int s = 0; s < kMeta; ++s) mbar_init(smem_u32(&ms.meta_full[s]), C::META_ARRIVALS);
+    for (int s = 0; s < kMaxStage; ++s) {
+      mbar_init(smem_u32(&ms.raw_full[s]), kCopyThreads);
+      mbar_init(smem_u32(&ms.raw_empty[s]), kExpandWarps);
+    }
     for (int s = 0; s < C::SBUF; ++s) {
       mbar_init(smem_u32(&ms.s_full[s]), 1);
       mbar_init(smem_u32(&ms.s_free[s]), kSmxWarps);
@@ -1399,7 +1414,7 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
       mbar_init(smem_u32(&ms.p_free[s]), 1);
       mbar_init(smem_u32(&ms.final[s]), 1);
     }
-    mbar_init(smem_u32(&ms.rope_full), kTma ? 1 : 32 * C::GW);
+    mbar_init(smem_u32(&ms.rope_full), C::ROPE_ARRIVALS);
     mbar_init(smem_u32(&ms.rope_empty), 1);
     mbar_init(smem_u32(&ms.q_full), kSmxWarps);
     ms.abort = 0;
@@ -1430,7 +1445,10 @@ __global__ void __launch_bounds__(Cfg<NC, kLayout, kTma>::THREADS, 1)
       regs_dec<C::OTHER_REGS>();
       if (warp == kQkWarp) qk_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
       else if (warp == kPvWarp) pv_role<NC, kLayout, kTma>(w, sm, ms, tmem, rg);
-      else if constexpr (C::kFp4) expand_role<NC, kLayout>(w, sm, ms, rg);
+      else if constexpr (C::kFp4) {
+        if (warp < kProdWarp0 + kCopyWarps) fp4_copy_role<NC, kLayout>(w, sm, ms, rg);
+        else fp4_expand_role<NC, kLayout>(w, sm, ms, rg);
+      }
       else if constexpr (!kTma) producer_role<NC, kLayout, kTma>(w, sm, ms, rg);
       else if (warp == kProdWarp0) tma_role<NC, kLayout, kTma>(w, maps, sm, ms, rg);
     }
