@@ -560,6 +560,42 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
                    float sm_scale, void* o_bf16_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes,
                    int32_t* err_flag_dev, void* stream);
 
+/* ------------------------------- dense attention behind shared prefixes */
+
+/* Largest number of requests of dsa_prefix_attn. */
+#define DSA_MAX_PREFIX_REQUESTS 4096
+
+/* Workspace bytes of dsa_prefix_attn: as dsa_chunk_attn_workspace_bytes, and 4 KB
+ * for each query row, 256 rows a request at most. */
+size_t dsa_prefix_attn_workspace_bytes(int T, int H, int B, int layout);
+
+/* dsa_chunk_attn for batches whose requests begin with common rows.  Group g is
+ * the requests [group_cu[g], group_cu[g + 1]); their first prefix_lens[g] keys
+ * are the same rows, held in the same pages of the pool, or copies of them: they
+ * are read once for all of the group's query rows, through the page-table row of
+ * the group's first request that has new tokens.  Results are those of
+ * dsa_chunk_attn (two partial softmaxes are joined in FP32; a result is off by
+ * no more, but need not have the same bits).
+ * Prefixes are used as far as it pays and holds for the whole group: rounded down
+ * to 128 keys, at most what the first new token of each of the group's requests
+ * sees, and only where packing the rows of several requests into tiles of 32 takes
+ * less work than each request's own pass (few query rows a request: at most 32 of
+ * the last tile's rows are saved each).  Requests outside every group, and those of
+ * a group of one, attend alone.  With more than 256 query rows (tokens x heads) a
+ * request on average nothing is shared.
+ *   group_cu_dev     [G + 1] int32 ascending within [0, B], prefix_lens_dev [G]
+ *                    int32, at least 0, read on the GPU; otherwise
+ *                    (DSA_DEV_ERR_LENGTH) the call's requests attend alone.
+ *   G                0 (pointers may be NULL) to B;  B <= DSA_MAX_PREFIX_REQUESTS.
+ *   workspace_dev    ws_bytes >= dsa_prefix_attn_workspace_bytes(T, H, B, layout).
+ * Everything else as dsa_chunk_attn. */
+int dsa_prefix_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool_dev, int64_t pool_rows,
+                    int layout, int kv_row_dim, const int32_t* page_table_dev, int B, int max_pages,
+                    int page_size, const int32_t* cu_q_dev, const int32_t* kv_lens_dev,
+                    const int32_t* group_cu_dev, const int32_t* prefix_lens_dev, int G, int causal,
+                    float sm_scale, void* o_bf16_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes,
+                    int32_t* err_flag_dev, void* stream);
+
 #if defined(__GNUC__)
 #pragma GCC visibility pop
 #endif

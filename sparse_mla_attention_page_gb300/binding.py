@@ -43,7 +43,7 @@ EXPORTS = (
     "dsa_sparse_attn_prefill_q8", "dsa_gather_dequant_workspace_bytes", "dsa_gather_dequant",
     "dsa_sparse_attn_decode_noalloc", "dsa_set_wait_limit_ns",
     "dsa_pages_extend", "dsa_pages_release", "dsa_rope_qkv656", "dsa_chunk_attn_workspace_bytes", "dsa_chunk_attn",
-    "dsa_kv_write_fp4", "dsa_kv_read", "dsa_pages_release_own",
+    "dsa_kv_write_fp4", "dsa_kv_read", "dsa_pages_release_own", "dsa_prefix_attn_workspace_bytes", "dsa_prefix_attn",
 )
 
 
@@ -123,6 +123,11 @@ def lib() -> ctypes.CDLL:
             L.dsa_kv_read.argtypes = [vp, i64, i32, vp, i32, i32, i32, vp, vp, vp, i64, i64, vp, vp]
             L.dsa_pages_release_own.restype = i32
             L.dsa_pages_release_own.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+            L.dsa_prefix_attn_workspace_bytes.restype = c.c_size_t
+            L.dsa_prefix_attn_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.dsa_prefix_attn.restype = i32
+            L.dsa_prefix_attn.argtypes = [vp, i32, i32, i32, vp, i64, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32,
+                                          c.c_float, vp, vp, vp, c.c_size_t, vp, vp]
             _lib = L
     return _lib
 
@@ -552,3 +557,32 @@ def dsa_chunk_attn(q_bf16, pool, layout, page_table, page_size, cu_q, kv_lens, s
         _arg(cu_q, "cu_q", i32, (B + 1,), dev), _arg(kv_lens, "kv_lens", i32, (B,), dev), int(causal), sm_scale,
         _arg(o, "o", torch.bfloat16, (T, H, 512), dev), _arg(lse, "lse", torch.float32, (T, H), dev),
         _arg(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _flag(err_flag, dev), s), "dsa_chunk_attn")
+
+
+def dsa_prefix_attn_workspace_bytes(T: int, H: int, B: int, layout) -> int:
+    return int(lib().dsa_prefix_attn_workspace_bytes(T, H, B, LAYOUTS.get(layout, layout)))
+
+
+def prefix_workspace_for(T: int, H: int, B: int, layout, device=None) -> torch.Tensor:
+    """A device workspace for dsa_prefix_attn of up to T tokens of up to B requests, with up to H heads."""
+    return torch.empty(dsa_prefix_attn_workspace_bytes(T, H, B, layout), dtype=torch.uint8, device=device or "cuda")
+
+
+def dsa_prefix_attn(q_bf16, pool, layout, page_table, page_size, cu_q, kv_lens, group_cu, prefix_lens, sm_scale, o, lse,
+                    workspace, causal=True, err_flag=None, stream=None) -> None:
+    """dsa_chunk_attn for requests that begin with common rows: group g's requests group_cu[g]:group_cu[g + 1] share their
+    first prefix_lens[g] keys, which are read once for all of them (see include/dsa.h)."""
+    dev, s = _call_device(stream)
+    lay = LAYOUTS.get(layout, layout)
+    T, H, D = _dims(q_bf16, "q_bf16", 3)
+    B, W = _dims(page_table, "page_table", 2)
+    rows, _ = _dims(pool, "pool", 2)
+    G, = _dims(prefix_lens, "prefix_lens", 1)
+    i32 = torch.int32
+    _check((_lib or lib()).dsa_prefix_attn(
+        _arg(q_bf16, "q_bf16", torch.bfloat16, None, dev), T, H, D, _arg(pool, "pool", torch.uint8, None, dev), rows, lay,
+        _kv_row_dim(pool, lay), _arg(page_table, "page_table", i32, None, dev), B, W, page_size,
+        _arg(cu_q, "cu_q", i32, (B + 1,), dev), _arg(kv_lens, "kv_lens", i32, (B,), dev),
+        _arg(group_cu, "group_cu", i32, (G + 1,), dev), _arg(prefix_lens, "prefix_lens", i32, (G,), dev), G, int(causal), sm_scale,
+        _arg(o, "o", torch.bfloat16, (T, H, 512), dev), _arg(lse, "lse", torch.float32, (T, H), dev),
+        _arg(workspace, "workspace", torch.uint8, None, dev), workspace.numel(), _flag(err_flag, dev), s), "dsa_prefix_attn")

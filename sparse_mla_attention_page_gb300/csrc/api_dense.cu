@@ -2,6 +2,7 @@
 // tables, rotary positions and the attention of new tokens.  Host-side
 // validation, then one launch sequence; on a non-zero status other than
 // DSA_ERR_CUDA nothing was launched.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -39,11 +40,14 @@ bool table_ok(int B, int max_pages, int page_size) {
 // Where the parts of the attention's workspace begin (pointers from base on).
 // Its size grows with T, H and B alone, not with the rows of a unit that they
 // lead to, so that it serves every smaller call too.
-size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, char* base) {
-  w.nc = dsa::chunk_columns(T, H, B);
-  w.max_units = (int64_t)T * H / w.nc + B;     // full units, and the last of each request
+// shared: with room for requests that share prefixes (a.G may still be 0).
+size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool shared, char* base) {
+  // shared prefixes pack rows of several requests: 16 rows only where there are no more
+  w.nc = dsa::chunk_columns(T, H, w.a.G > 0 ? 1 : B);
+  w.rows = (int64_t)T * H;
+  w.max_units = (w.rows / w.nc) * (w.a.G > 0 ? 2 : 1) + B + w.a.G;     // full units, and the last of each request and group
   w.grid = sms;
-  const size_t units = (size_t)((int64_t)T * H / dsa::kFewestRows + B);
+  const size_t units = (size_t)((w.rows / dsa::kFewestRows) * (shared ? 2 : 1) + B * (shared ? 2 : 1));
   const size_t rows = (size_t)sms * 2 * dsa::chunk_columns(T, H, 1);
   size_t end = 0;
   auto take = [&](size_t bytes) {
@@ -55,6 +59,12 @@ size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, char* base
   w.splits = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
   w.part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
   w.part_o = reinterpret_cast<float*>(take(rows * 512 * sizeof(float)));
+  if (shared) {
+    const size_t joined = (size_t)std::min(w.rows, (int64_t)B * dsa::kSharedRows) * 2;
+    w.n_units = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
+    w.row_lse = reinterpret_cast<float*>(take(joined * sizeof(float)));
+    w.row_o = reinterpret_cast<float*>(take(joined * 512 * sizeof(float)));
+  }
   return end;
 }
 
@@ -88,6 +98,42 @@ int release_pages(const dsa::ReleaseArgs& a, void* stream) {
 
 bool chunk_sizes_ok(int T, int H, int B) {
   return T >= 0 && H >= 1 && H <= 1024 && (int64_t)T * H <= INT32_MAX / 2 && B >= 1 && B <= DSA_MAX_REQUESTS;
+}
+
+size_t chunk_bytes(int T, int H, int B, int layout, bool shared) {
+  if (!chunk_sizes_ok(T, H, B) || dsa_kv_row_bytes(layout) == 0) return 0;
+  int sms = 0;
+  if (dsa::current_device_sms(&sms) != DSA_OK) sms = 152;
+  dsa::ChunkWork w{};
+  return lay_out_chunk(w, T, H, B, sms, shared, nullptr);
+}
+
+// Dense attention, checked and launched; shared: of dsa_prefix_attn.
+int attend(const dsa::ChunkArgs& a, int kv_row_dim, bool shared, void* workspace, size_t ws_bytes, void* stream) {
+  if (a.T < 0 || a.pool_rows < 0) return DSA_ERR_SHAPE;
+  if (dsa_kv_row_bytes(a.layout) == 0) return DSA_ERR_LAYOUT;
+  const int width = a.layout == DSA_KV_ROPE656 || a.layout == DSA_KV_FP4_416 ? 576 : 512;
+  if (a.q_row != width || kv_row_dim != width) return DSA_ERR_ROW_WIDTH;
+  if (a.H < 1 || a.H > 1024) return DSA_ERR_HEADS;
+  if (a.T == 0) return DSA_OK;
+  if (any_null(a.page_table, a.cu_q, a.kv_lens) || any_null(a.q, a.o) || any_null(a.pool) || any_null(a.lse)) return DSA_ERR_NULL;
+  if (!table_ok(a.B, a.max_pages, a.page_size) || !chunk_sizes_ok(a.T, a.H, a.B) || a.pool_rows < 1 || a.pool_rows > INT32_MAX)
+    return DSA_ERR_SHAPE;
+  if (!aligned(a.q, 16) || !aligned(a.pool, 16) || !aligned(a.o, 16) || !aligned(a.lse, 4) || !aligned(a.page_table, 4) ||
+      !aligned(a.cu_q, 4) || !aligned(a.kv_lens, 4) || !aligned(a.err, 4))
+    return DSA_ERR_ALIGN;
+  if (workspace == nullptr || ws_bytes < chunk_bytes(a.T, a.H, a.B, a.layout, shared)) return DSA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return DSA_ERR_ALIGN;
+  int sms = 0;
+  const int st = dsa::current_device_sms(&sms);
+  if (st != DSA_OK) return st;
+  dsa::ChunkWork w{};
+  w.a = a;
+  if ((int64_t)a.T * a.H > (int64_t)a.B * dsa::kSharedRows) w.a.G = 0;
+  lay_out_chunk(w, a.T, a.H, a.B, sms, shared, static_cast<char*>(workspace));
+  w.wait_ns = dsa::wait_limit_ns();
+  cudaGetLastError();
+  return launch_status(dsa::launch_chunk_attn(w, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -207,12 +253,10 @@ int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t 
   return launch_status(true);
 }
 
-size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout) {
-  if (!chunk_sizes_ok(T, H, B) || dsa_kv_row_bytes(layout) == 0) return 0;
-  int sms = 0;
-  if (dsa::current_device_sms(&sms) != DSA_OK) sms = 152;
-  dsa::ChunkWork w{};
-  return lay_out_chunk(w, T, H, B, sms, nullptr);
+size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout) { return chunk_bytes(T, H, B, layout, false); }
+
+size_t dsa_prefix_attn_workspace_bytes(int T, int H, int B, int layout) {
+  return B > DSA_MAX_PREFIX_REQUESTS ? 0 : chunk_bytes(T, H, B, layout, true);
 }
 
 int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool_dev, int64_t pool_rows,
@@ -220,49 +264,25 @@ int dsa_chunk_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool
                    const int32_t* cu_q_dev, const int32_t* kv_lens_dev, int causal, float sm_scale,
                    void* o_bf16_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes, int32_t* err_flag_dev,
                    void* stream) {
-  if (T < 0 || pool_rows < 0) return DSA_ERR_SHAPE;
-  if (dsa_kv_row_bytes(layout) == 0) return DSA_ERR_LAYOUT;
-  const int width = layout == DSA_KV_ROPE656 || layout == DSA_KV_FP4_416 ? 576 : 512;
-  if (D != width || kv_row_dim != width) return DSA_ERR_ROW_WIDTH;
-  if (H < 1 || H > 1024) return DSA_ERR_HEADS;
-  if (T == 0) return DSA_OK;
-  if (any_null(page_table_dev, cu_q_dev, kv_lens_dev) || q_bf16_dev == nullptr || pool_dev == nullptr ||
-      o_bf16_dev == nullptr || lse_dev == nullptr)
-    return DSA_ERR_NULL;
-  if (!table_ok(B, max_pages, page_size) || !chunk_sizes_ok(T, H, B) || pool_rows < 1 || pool_rows > INT32_MAX)
-    return DSA_ERR_SHAPE;
-  if (!aligned(q_bf16_dev, 16) || !aligned(pool_dev, 16) || !aligned(o_bf16_dev, 16) || !aligned(lse_dev, 4) ||
-      !aligned(page_table_dev, 4) || !aligned(cu_q_dev, 4) || !aligned(kv_lens_dev, 4) || !aligned(err_flag_dev, 4))
-    return DSA_ERR_ALIGN;
-  if (workspace_dev == nullptr || ws_bytes < dsa_chunk_attn_workspace_bytes(T, H, B, layout)) return DSA_ERR_WORKSPACE;
-  if (!aligned(workspace_dev, 256)) return DSA_ERR_ALIGN;
-  int sms = 0;
-  const int st = dsa::current_device_sms(&sms);
-  if (st != DSA_OK) return st;
-  dsa::ChunkWork w{};
-  lay_out_chunk(w, T, H, B, sms, static_cast<char*>(workspace_dev));
-  w.wait_ns = dsa::wait_limit_ns();
-  dsa::ChunkArgs& a = w.a;
-  a.q = static_cast<const uint16_t*>(q_bf16_dev);
-  a.T = T;
-  a.H = H;
-  a.q_row = width;
-  a.pool = static_cast<const uint8_t*>(pool_dev);
-  a.pool_rows = pool_rows;
-  a.layout = layout;
-  a.page_table = page_table_dev;
-  a.B = B;
-  a.max_pages = max_pages;
-  a.page_size = page_size;
-  a.cu_q = cu_q_dev;
-  a.kv_lens = kv_lens_dev;
-  a.causal = causal != 0;
-  a.sm_scale = sm_scale;
-  a.o = static_cast<uint16_t*>(o_bf16_dev);
-  a.lse = lse_dev;
-  a.err = err_flag_dev;
-  cudaGetLastError();
-  return launch_status(dsa::launch_chunk_attn(w, static_cast<cudaStream_t>(stream)));
+  const dsa::ChunkArgs a{static_cast<const uint16_t*>(q_bf16_dev), T, H, D, static_cast<const uint8_t*>(pool_dev), pool_rows,
+                         layout, page_table_dev, B, max_pages, page_size, cu_q_dev, kv_lens_dev, causal != 0, sm_scale,
+                         static_cast<uint16_t*>(o_bf16_dev), lse_dev, err_flag_dev, nullptr, nullptr, 0};
+  return attend(a, kv_row_dim, false, workspace_dev, ws_bytes, stream);
+}
+
+int dsa_prefix_attn(const void* q_bf16_dev, int T, int H, int D, const void* pool_dev, int64_t pool_rows,
+                    int layout, int kv_row_dim, const int32_t* page_table_dev, int B, int max_pages,
+                    int page_size, const int32_t* cu_q_dev, const int32_t* kv_lens_dev,
+                    const int32_t* group_cu_dev, const int32_t* prefix_lens_dev, int G, int causal,
+                    float sm_scale, void* o_bf16_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes,
+                    int32_t* err_flag_dev, void* stream) {
+  if (G < 0 || G > B || B > DSA_MAX_PREFIX_REQUESTS) return DSA_ERR_SHAPE;
+  if (G > 0 && T > 0 && any_null(group_cu_dev, prefix_lens_dev)) return DSA_ERR_NULL;
+  if (!aligned(group_cu_dev, 4) || !aligned(prefix_lens_dev, 4)) return DSA_ERR_ALIGN;
+  const dsa::ChunkArgs a{static_cast<const uint16_t*>(q_bf16_dev), T, H, D, static_cast<const uint8_t*>(pool_dev), pool_rows,
+                         layout, page_table_dev, B, max_pages, page_size, cu_q_dev, kv_lens_dev, causal != 0, sm_scale,
+                         static_cast<uint16_t*>(o_bf16_dev), lse_dev, err_flag_dev, group_cu_dev, prefix_lens_dev, G};
+  return attend(a, kv_row_dim, true, workspace_dev, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -10,6 +10,11 @@
 // chunk_unit_cost more than its tiles, for its query operand and its output.
 // Lengths live on the GPU: every CTA of the attention kernel forms the list's
 // prefix sums for itself.
+//
+// Shared prefixes.  The requests of a group begin with common rows.  Where that
+// takes fewer tiles, their query rows are packed into units of the prefix alone,
+// and each request keeps units over its own keys; the two results of a row are
+// joined as those of split units are.
 #pragma once
 #include <cstdint>
 
@@ -36,8 +41,16 @@ struct __align__(16) ChunkUnit {
   int32_t tiles;     // at least 1
   int32_t kv;        // the request's keys
   int32_t last;      // keys that the unit's last row sees
-  int32_t pad;
+  int32_t key0;      // the request's key that the unit's first one is
+  int32_t mate;      // of a kOwn unit: the unit that holds its first row's part over the prefix,
+  int16_t slot0;     // parts > 0: spread over CTAs, its parts in the slots slot0, then as of ChunkSplit
+  int16_t parts;
+  uint8_t side;      // ChunkSide
+  uint8_t mate_col;  // and that row's column there
+  int16_t pad[3];
 };
+static_assert(sizeof(ChunkUnit) == 64, "sixteen words");
+enum ChunkSide { kAlone = 0, kPrefix = 1, kOwn = 2 };   // all of a row's keys; those it shares; the others
 
 // A unit spread over CTAs c0 ..: its parts lie in the slots slot0, 2 (c0 + 1), 2 (c0 + 2), ...
 struct __align__(16) ChunkSplit {
@@ -63,15 +76,24 @@ struct ChunkWork {
   ChunkSplit* splits;      // [grid] by the CTA in which the unit begins
   float* part_lse;         // [2 grid][nc]
   float* part_o;           // [2 grid][nc][512] normalised
+  // with shared prefixes (a.G > 0), else nullptr:
+  int32_t* n_units;
+  int64_t rows;            // T H
+  float* row_lse;          // [2][rows] of kPrefix and kOwn units that are not spread over CTAs
+  float* row_o;            // [2][rows][512]
 };
+// Sharing is for batches of few query rows a request; at most so many on average
+// (eight units each: packing rows could save one of them at most).
+constexpr int kSharedRows = 256;
 
 // Keys that row r of a unit's request sees.
 __device__ __forceinline__ int chunk_visible(const ChunkArgs& a, const ChunkUnit& u, int col) {
-  if (!a.causal) return u.kv;
+  if (!a.causal || u.side == kPrefix) return u.kv;
   const int64_t v = (int64_t)u.vis0 + (u.r0 + col) / a.H;
   return v < 0 ? 0 : v > u.kv ? u.kv : (int)v;
 }
 
 bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream);
+bool launch_prefix_merge(const ChunkWork& w, cudaStream_t stream);
 
 }  // namespace dsa

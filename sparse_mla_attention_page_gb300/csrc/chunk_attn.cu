@@ -201,7 +201,7 @@ struct Cfg {
   static constexpr int MISC_OFF = ST_OFF + ST_BYTES;
   static constexpr int SMEM = MISC_OFF + kMiscBytes + 1024;
   static_assert(NS > 4, "a tile's blocks and one more");
-  static_assert(NS * kBlock >= kPlanScratch, "the plan's scratch lies in the ring");
+  static_assert(MISC_OFF >= kPlanScratch, "the plan's scratch lies in front");
   // a tile's rows are replaced kMeta tiles later, when its blocks are gone from the ring
   static_assert((NS - 1) / 4 + 1 < kMeta, "rows of a tile in use");
   // (4-bit rows: when tile t's first codes are requested, block 4 t - NST is expanded, the last of tile t - 2 or
@@ -367,10 +367,10 @@ struct Range {
 // The producers' walk through a CTA's tiles.  A segment is the part of a unit
 // inside the CTA's range.  What they need of the next unit is fetched while the
 // current one is worked on: its request and lengths by every thread, one word
-// of its entry by each of the first twelve (for the other roles).
+// of its entry by each of the first sixteen (for the other roles).
 struct Walk {
-  int unit, tile, tiles, b, last;
-  int next_tiles, next_b, next_last;
+  int unit, tile, tiles, b, last, key0;
+  int next_tiles, next_b, next_last, next_key0;
   int32_t word = 0, next_word = 0;
   static constexpr int kWords = sizeof(ChunkUnit) / 4;
   __device__ __forceinline__ void fetch_next(const ChunkWork& w, int ptid) {
@@ -378,6 +378,7 @@ struct Walk {
     next_tiles = __ldcg(&u->tiles);
     next_b = __ldcg(&u->b);
     next_last = __ldcg(&u->last);
+    next_key0 = __ldcg(&u->key0);
     if (ptid < kWords) next_word = __ldcg(reinterpret_cast<const int32_t*>(u) + ptid);
   }
   __device__ __forceinline__ Walk(const ChunkWork& w, const Misc& ms, int ptid) {
@@ -386,6 +387,7 @@ struct Walk {
     tiles = u.tiles;
     b = u.b;
     last = u.last;
+    key0 = u.key0;
     tile = (int)(ms.range.t0 - u.tile0);
     fetch_next(w, ptid);
   }
@@ -396,6 +398,7 @@ struct Walk {
     tiles = next_tiles;
     b = next_b;
     last = next_last;
+    key0 = next_key0;
     word = next_word;
     ++unit;
     fetch_next(w, ptid);
@@ -447,9 +450,10 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
   int32_t entry = -1, off = 0;
   bool seen = false;
   auto look_up = [&]() {
-    const int j = cur.tile * kTile + ptid;
+    int j = cur.tile * kTile + ptid;
     seen = ptid < kTile && j < cur.last;
     if (seen) {
+      j += cur.key0;
       const int page = j / a.page_size;
       off = j - page * a.page_size;
       entry = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
@@ -560,9 +564,10 @@ __device__ void fp4_copy_role(const ChunkWork& w, uint8_t* sm, Misc& ms, const R
   auto look_up = [&]() {       // keys ptid, ptid + kCopyThreads, ... of the walk's tile
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      const int j = cur.tile * kTile + ptid + i * kCopyThreads;
+      int j = cur.tile * kTile + ptid + i * kCopyThreads;
       seen[i] = j < cur.last;
       if (seen[i]) {
+        j += cur.key0;
         const int page = j / a.page_size;
         off[i] = j - page * a.page_size;
         entry[i] = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
@@ -731,9 +736,10 @@ __device__ void tma_role(const ChunkWork& w, const ChunkMaps& maps, uint8_t* sm,
   Walk cur(w, ms, lane);
   int32_t entry = -1, off = 0, want = 0;     // the next tile's: page-table entry, row in the page, keys seen of the box
   auto look_up = [&]() {
-    const int j = cur.tile * kTile + (lane << w.box_shift);
+    int j = cur.tile * kTile + (lane << w.box_shift);
     want = mine ? min(box, cur.last - j) : 0;
     if (want > 0) {
+      j += cur.key0;
       const int page = j / a.page_size;
       off = j - page * a.page_size;
       entry = __ldg(a.page_table + (int64_t)cur.b * a.max_pages + page);
@@ -1337,6 +1343,8 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     const int64_t part = ((int64_t)blockIdx.x * 2 + (rg.t0 >= u.tile0 ? 0 : 1)) * NC;
     const int cols = u.cols - c0;                        // of this thread's columns
     const int64_t row0 = u.row0;
+    const bool final = whole && u.side == kAlone;        // else FP32, to be joined
+    const int64_t to = whole ? (u.side - kPrefix) * w.rows + row0 : part;
     float li[CPT];
     ld_row<CPT>(&ms.by[c0], li);
     // block db's outputs of this thread's columns, normalised
@@ -1350,7 +1358,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       for (int k = 0; k < CPT; ++k)
         y[k] = li[k] == 0.f ? 0.f : fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(v[k])) * (li[k] * unlift);
     };
-    if (whole) {
+    if (final) {
       __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + (row0 + c0) * kD + row;
 #pragma unroll
       for (int db = 0; db < 4; ++db) {
@@ -1361,7 +1369,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
           if (k < cols) o[k * kD + db * 128] = __float2bfloat16_rn(y[k]);
       }
     } else {
-      float* o = w.part_o + (part + c0) * kD + row;
+      float* o = (whole ? w.row_o : w.part_o) + (to + c0) * kD + row;
 #pragma unroll
       for (int db = 0; db < 4; ++db) {
         float y[CPT];
@@ -1372,8 +1380,8 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
       }
     }
     if (quarter == 0 && lane < CPT && lane < cols) {
-      if (whole) a.lse[row0 + c0 + lane] = ms.alpha[c0 + lane];
-      else w.part_lse[part + c0 + lane] = ms.alpha[c0 + lane];
+      if (final) a.lse[row0 + c0 + lane] = ms.alpha[c0 + lane];
+      else (whole ? w.row_lse : w.part_lse)[to + c0 + lane] = ms.alpha[c0 + lane];
     }
   }
 }
@@ -1490,6 +1498,7 @@ bool launch(const ChunkWork& w, const ChunkMaps& maps, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, chunk_attn_kernel<NC, kLayout, kTma>, w, maps) != cudaSuccess) return false;
+  if (w.a.G > 0) return launch_prefix_merge(w, stream);
   // units of one tile are not spread over CTAs
   return (int64_t)w.a.max_pages * w.a.page_size <= kTile || launch_chunk_merge(w, stream);
 }

@@ -177,11 +177,212 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
     }
 }
 
-}  // namespace
+// ---- rows that share a prefix
 
-bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
+// Where the parts of a unit's rows over the prefix lie: those of its first rows,
+// and from column brk on those of the next unit of the prefix.
+struct Join {
+  int64_t row0;
+  int cols, own_slot, own_parts;       // parts 0: one part, in row_o
+  int brk, col0, slot[2], parts[2];    // column of its first row there
+  int kind;                            // 0: nothing to do, 1: up to kFewParts parts, 2: more
+};
+
+__device__ __forceinline__ Join join_of(const ChunkWork& w, int u) {
+  union {
+    ChunkUnit u;
+    int4 v[4];
+  } x;
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x.v[k] = __ldcg(reinterpret_cast<const int4*>(w.units + i) + k);
+  };
+  fetch(u);
+  Join j{};
+  if (x.u.side == kPrefix || (x.u.side == kAlone && x.u.parts == 0)) return j;
+  j.row0 = x.u.row0;
+  j.cols = x.u.cols;
+  j.own_slot = x.u.slot0;
+  j.own_parts = x.u.parts;
+  j.brk = j.cols;
+  int parts = max(j.own_parts, 1);
+  if (x.u.side == kOwn) {
+    const int mate = x.u.mate;
+    j.col0 = x.u.mate_col;
+    j.brk = min(j.cols, w.nc - j.col0);
+    fetch(mate);
+    j.slot[0] = x.u.slot0;
+    j.parts[0] = max((int)x.u.parts, 0);
+    int most = max(j.parts[0], 1);
+    if (j.brk < j.cols) {
+      fetch(mate + 1);
+      j.slot[1] = x.u.slot0;
+      j.parts[1] = max((int)x.u.parts, 0);
+      most = max(most, j.parts[1]);
+    }
+    parts += most;
+  } else {
+    j.parts[0] = -1;                   // no prefix
+  }
+  j.kind = parts <= kFewParts ? 1 : 2;
+  return j;
+}
+
+// The parts of one row: its own keys' first, then the prefix's.
+struct RowParts {
+  const ChunkWork& w;
+  int64_t row, own_at, pre_at;         // rows of part_o (or of row_o, where there is one part)
+  int own, pre;                        // parts
+  bool own_whole, pre_whole;
+  int own_next, pre_next, col, pre_col;
+  __device__ __forceinline__ RowParts(const ChunkWork& work, const Join& j, int c) : w(work), row(j.row0 + c), col(c) {
+    own_whole = j.own_parts == 0;
+    own = own_whole ? 1 : j.own_parts;
+    own_at = own_whole ? w.rows + row : (int64_t)j.own_slot * w.nc + c;
+    own_next = (j.own_slot / 2 + 1) * 2;
+    const int second = c >= j.brk;
+    const int n = second ? j.parts[1] : j.parts[0], slot = second ? j.slot[1] : j.slot[0];
+    pre_col = (j.col0 + c) % w.nc;
+    pre_whole = n == 0;
+    pre = n < 0 ? 0 : pre_whole ? 1 : n;
+    pre_at = pre_whole ? row : (int64_t)slot * w.nc + pre_col;
+    pre_next = (slot / 2 + 1) * 2;
+  }
+  __device__ __forceinline__ int count() const { return own + pre; }
+  // part p's LSE and row of 512
+  __device__ __forceinline__ void at(int p, const float*& lse, const float4*& o) const {
+    const bool mine = p < own;
+    const int q = mine ? p : p - own;
+    const bool whole = mine ? own_whole : pre_whole;
+    const int64_t r = q == 0 ? (mine ? own_at : pre_at)
+                             : (int64_t)((mine ? own_next : pre_next) + 2 * (q - 1)) * w.nc + (mine ? col : pre_col);
+    lse = (whole ? w.row_lse : w.part_lse) + r;
+    o = reinterpret_cast<const float4*>((whole ? w.row_o : w.part_o) + r * kD);
+  }
+};
+
+// Parts p0, p0 + step, ... of a row, kInFlight of them at once: running maximum,
+// sum and V float4 of the dims, d4 + 32 i for i < V.
+template <int V, int kInFlight>
+__device__ __forceinline__ void fold_parts(const RowParts& rp, int p0, int step, int d4, float& m, float& sum, float4 (&acc)[V]) {
+  const int n = rp.count();
+  m = -INFINITY;
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (; p0 < n; p0 += step * kInFlight) {
+    float ls[kInFlight];
+    float4 v[kInFlight][V];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      const int p = p0 + k * step;
+      ls[k] = -INFINITY;
+      if (p >= n) continue;
+      const float* lse;
+      const float4* o;
+      rp.at(p, lse, o);
+      ls[k] = __ldcg(lse);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = __ldcg(o + d4 + 32 * i);
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) top = fmaxf(top, ls[k]);
+    if (top != m && m != -INFINITY) {
+      const float f = expf(m - top);
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
+    }
+    m = top;
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      if (ls[k] == -INFINITY) continue;            // no such part, or one without a visible key
+      const float e = expf(ls[k] - m);             // (NaN where it is: fmaxf passes it over)
+      sum += e;
+#pragma unroll
+      for (int i = 0; i < V; ++i) fold(acc[i], e, v[k][i]);
+    }
+  }
+}
+
+constexpr int kJoinLanes = kMergeThreads / 32;     // many parts: a warp for every eighth part of a row
+constexpr int kJoinAll = 1024;                     // units up to which every block looks at all of them
+
+// Few units (and so perhaps many parts): every block knows all of them, takes
+// its share of the rows of few parts, a pair at a time, and of those of many,
+// one at a time.  Many units: a block takes runs of 32 for itself.
+__global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const __grid_constant__ ChunkWork w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");               // every part is written
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ Join joins[kMergeThreads];
+  __shared__ float lane_m[kJoinLanes], lane_sum[kJoinLanes];
+  __shared__ float4 lane_o[kJoinLanes][kD / 4];
+  const int tid = threadIdx.x, n_units = __ldcg(w.n_units);
+  const bool all = n_units <= kJoinAll;
+  const int run = all ? kMergeThreads : 32;
+  const int pairs = w.nc / kFewRows;
+  for (int u0 = all ? 0 : blockIdx.x * run; u0 < n_units; u0 += all ? run : run * (int)gridDim.x) {
+    const int here = min(run, n_units - u0);
+    __syncthreads();                               // the entries before are done with
+    if (tid < here) joins[tid] = join_of(w, u0 + tid);
+    __syncthreads();
+    for (int item = all ? blockIdx.x : 0; item < here * pairs; item += all ? gridDim.x : 1) {
+      const Join& j = joins[item / pairs];
+      const int col = item % pairs * kFewRows + tid / kFewThreads, d4 = tid % kFewThreads;
+      if ((j.kind == 0 || (j.kind == 2 && all)) || col >= j.cols) continue;
+      const RowParts rp(w, j, col);
+      float m, sum;
+      float4 acc[1];
+      fold_parts<1, 4>(rp, 0, 1, d4, m, sum, acc);
+      store_row(w.a, rp.row, d4, acc[0], sum == 0.f ? 0.f : 1.f / sum);
+      if (d4 == 0) w.a.lse[rp.row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    }
+    if (!all) continue;
+    int item = blockIdx.x;                         // from the unit's first row on
+    for (int i = 0; i < here; ++i) {
+      const Join& j = joins[i];
+      if (j.kind != 2) continue;
+      for (; item < j.cols; item += gridDim.x) {
+        const RowParts rp(w, j, item);
+        const int lane = tid & 31, warp = tid >> 5;
+        float m, sum;
+        float4 acc[4];
+        fold_parts<4, 2>(rp, warp, kJoinLanes, lane, m, sum, acc);
+        if (lane == 0) {
+          lane_m[warp] = m;
+          lane_sum[warp] = sum;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lane_o[warp][lane + 32 * k] = acc[k];
+        __syncthreads();
+        if (tid < kD / 4) {
+          float top = -INFINITY, total = 0.f;
+#pragma unroll
+          for (int k = 0; k < kJoinLanes; ++k) top = fmaxf(top, lane_m[k]);
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kJoinLanes; ++k) {
+            if (lane_sum[k] == 0.f) continue;      // none of its parts has a visible key
+            const float e = expf(lane_m[k] - top);
+            total = fmaf(e, lane_sum[k], total);
+            fold(o, e, lane_o[k][tid]);
+          }
+          store_row(w.a, rp.row, tid, o, total == 0.f ? 0.f : 1.f / total);
+          if (tid == 0) w.a.lse[rp.row] = total == 0.f ? -INFINITY : top + logf(total);
+        }
+        __syncthreads();
+      }
+      item -= j.cols;
+    }
+  }
+}
+
+template <class Kernel>
+bool launch_merge(Kernel kernel, dim3 grid, const ChunkWork& w, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(w.grid, kFewBlocks);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -189,7 +390,17 @@ bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, w) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, kernel, w) == cudaSuccess;
+}
+
+}  // namespace
+
+bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
+  return launch_merge(chunk_merge_kernel, dim3(w.grid, kFewBlocks), w, stream);
+}
+
+bool launch_prefix_merge(const ChunkWork& w, cudaStream_t stream) {
+  return launch_merge(prefix_merge_kernel, dim3(w.grid * 4), w, stream);
 }
 
 }  // namespace dsa

@@ -40,25 +40,100 @@ __device__ __forceinline__ Request request_of(const ChunkArgs& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ int units_of(const ChunkArgs& a, const Request& r, int nc) {
-  return (int)(((int64_t)r.n * a.H + nc - 1) / nc);
-}
+__device__ __forceinline__ int units_of(const ChunkArgs& a, int n, int nc) { return (int)(((int64_t)n * a.H + nc - 1) / nc); }
 
-// Entry of the i-th unit of request b (tile0 is filled in later).
-__device__ __forceinline__ ChunkUnit unit_of(const ChunkArgs& a, const Request& r, int b, int i, int nc) {
-  ChunkUnit u;
+// Keys that the first new token of a request sees.
+__device__ __forceinline__ int first_visible(const ChunkArgs& a, const Request& r) { return a.causal ? r.kv - r.n + 1 : r.kv; }
+
+// Rows and keys that units are cut from: a request, its own keys, or a group's
+// rows over their prefix.
+struct Part {
+  int t0, n, kv, vis0, key0, b, side;
+  int64_t group_row0;      // kOwn: the group's first query row and first unit
+  int group_unit;
+};
+
+// Entry of the i-th unit of a part (tile0 is filled in later).
+__device__ __forceinline__ ChunkUnit unit_of(const ChunkArgs& a, const Part& r, int i, int nc) {
+  ChunkUnit u{};
   const int64_t rows = (int64_t)r.n * a.H, r0 = (int64_t)i * nc;
-  u.tile0 = 0;
   u.row0 = (int64_t)r.t0 * a.H + r0;
-  u.b = b;
+  u.b = r.b;
   u.cols = (int)(rows - r0 < nc ? rows - r0 : nc);
   u.r0 = (int)r0;
-  u.vis0 = a.causal ? r.kv - r.n + 1 : r.kv;
+  u.vis0 = r.vis0;
   u.kv = r.kv;
+  u.key0 = r.key0;
+  u.side = (uint8_t)r.side;
+  if (r.side == kOwn) {
+    const int64_t at = u.row0 - r.group_row0;
+    u.mate = r.group_unit + (int)(at / nc);
+    u.mate_col = (uint8_t)(at % nc);
+  }
   u.last = chunk_visible(a, u, u.cols - 1);
   u.tiles = u.last <= kChunkTile ? 1 : (u.last - 1) / kChunkTile + 1;
-  u.pad = 0;
   return u;
+}
+
+// The groups of requests, in shared memory.
+struct Groups {
+  const int32_t* cu;       // [G + 1]
+  int32_t* keys;           // [G] shared keys (while they are found: what every row sees)
+  int32_t* first;          // [G] the first request with new tokens
+  int32_t* units;          // [G] units of the requests
+};
+
+// A group shares a whole number of tiles of its prefix, at most what its first
+// tokens all see, and only where packing its rows takes less than each request
+// reading those tiles for itself (the cost of a unit counted as the ranges do).
+// Requests with lengths out of range end the sharing of their group, offsets out
+// of order that of all.
+template <int THREADS>
+__device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch) {
+  const ChunkArgs& a = w.a;
+  const int tid = threadIdx.x, G = a.G;
+  int32_t* cu = scratch;
+  const Groups g{cu, cu + G + 1, cu + 2 * G + 1, cu + 3 * G + 1};
+  bool bad = false;
+  for (int i = tid; i <= G; i += THREADS) {
+    const int x = __ldg(a.group_cu + i);
+    bad |= x < 0 || x > a.B || (i < G && (x > __ldg(a.group_cu + i + 1) || __ldg(a.prefix_lens + i) < 0));
+    cu[i] = x;
+    if (i == G) break;
+    g.keys[i] = INT32_MAX;
+    g.first[i] = INT32_MAX;
+    g.units[i] = 0;
+  }
+  bad = __syncthreads_or(bad) != 0;
+  if (bad) {
+    if (blockIdx.x == 0 && tid == 0) set_err(a.err, DSA_DEV_ERR_LENGTH);
+    for (int i = tid; i <= G; i += THREADS) cu[i] = 0;      // nobody belongs to a group
+    __syncthreads();
+  } else {
+    for (int b = cu[0] + tid; b < cu[G]; b += THREADS) {
+      const int i = scan_owner(cu, G, b);
+      const Request r = request_of(a, b);
+      if (r.err) atomicMin(g.keys + i, 0);
+      if (r.n <= 0) continue;
+      atomicMin(g.keys + i, max(first_visible(a, r), 0));
+      atomicMin(g.first + i, b);
+      atomicAdd(g.units + i, units_of(a, r.n, w.nc));
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < G; i += THREADS) {
+    const int tiles = g.first[i] == INT32_MAX ? 0 : min(g.keys[i], __ldg(a.prefix_lens + i)) / kChunkTile;
+    int keys = 0;
+    if (tiles > 0) {
+      const int n = __ldg(a.cu_q + cu[i + 1]) - __ldg(a.cu_q + cu[i]);
+      const int64_t apart = (int64_t)g.units[i] * tiles * kTileCost;
+      const int64_t packed = (int64_t)units_of(a, n, w.nc) * (tiles * kTileCost + w.unit_cost);
+      if (packed < apart) keys = tiles * kChunkTile;
+    }
+    g.keys[i] = keys;
+  }
+  __syncthreads();
+  return g;
 }
 
 // A CTA's part of the tile list.
@@ -75,25 +150,62 @@ struct ChunkRange {
 // 13.7, rope 16.2 / 16.4.
 constexpr int kWholeTiles = 2;
 
-constexpr int kPlanScratch = DSA_MAX_REQUESTS * 4 + 256;   // bytes of shared memory
+// Bytes of shared memory: 32-bit words of the requests, or of the requests and
+// five of each group, and the scans' sums.
+constexpr int kPlanWords = DSA_MAX_REQUESTS > 6 * DSA_MAX_PREFIX_REQUESTS + 1 ? DSA_MAX_REQUESTS : 6 * DSA_MAX_PREFIX_REQUESTS + 1;
+constexpr int kPlanScratch = (kPlanWords * 4 + 7) / 8 * 8 + 256;
 
 // By all THREADS threads; mine and start (the range's first unit) lie in
 // shared memory and hold after the caller's next barrier.
 template <int THREADS>
 __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch, ChunkRange& mine, ChunkUnit& start) {
-  int32_t* first_unit = reinterpret_cast<int32_t*>(scratch);                             // [B]
-  int64_t* sums = reinterpret_cast<int64_t*>(scratch + DSA_MAX_REQUESTS * 4);
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch + kPlanScratch - 256);
+  int32_t* first_unit = reinterpret_cast<int32_t*>(scratch);                             // [N]
   const ChunkArgs& a = w.a;
   const int tid = threadIdx.x, cta = blockIdx.x;
+  const int N = a.G + a.B;         // parts: the groups' prefixes, then the requests
+  Groups groups{};
+  if (a.G > 0) groups = find_groups<THREADS>(w, first_unit + N);
   int err = 0;
-  const int per = (a.B + THREADS - 1) / THREADS;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  auto part = [&](int p) -> Part {
+    Part x{};
+    if (p < a.G) {
+      x.side = kPrefix;
+      x.kv = x.vis0 = groups.keys[p];
+      if (x.kv > 0) {
+        x.b = groups.first[p];
+        x.t0 = __ldg(a.cu_q + groups.cu[p]);
+        x.n = __ldg(a.cu_q + groups.cu[p + 1]) - x.t0;
+      }
+      return x;
+    }
+    const int b = p - a.G;
+    const Request r = request_of(a, b);
+    err |= r.err;
+    x.t0 = r.t0;
+    x.n = r.n;
+    x.b = b;
+    x.kv = r.kv;
+    x.vis0 = first_visible(a, r);
+    if (a.G > 0 && r.n > 0 && b >= groups.cu[0] && b < groups.cu[a.G]) {
+      const int g = scan_owner(groups.cu, a.G, b);
+      if (groups.keys[g] > 0) {
+        x.side = kOwn;
+        x.key0 = groups.keys[g];
+        x.kv -= x.key0;
+        x.vis0 -= x.key0;
+        x.group_row0 = (int64_t)__ldg(a.cu_q + groups.cu[g]) * a.H;
+        x.group_unit = first_unit[g];      // (once the sums are there)
+      }
+    }
+    return x;
+  };
+  const int per = (N + THREADS - 1) / THREADS;
+  const int b0 = min(tid * per, N), b1 = min(b0 + per, N);
   int64_t here = 0;
   int last_units = 0;
   for (int b = b0; b < b1; ++b) {
-    const Request r = request_of(a, b);
-    err |= r.err;
-    last_units = units_of(a, r, w.nc);
+    last_units = units_of(a, part(b).n, w.nc);
     here += last_units;
   }
   int64_t total;
@@ -104,31 +216,32 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   }
   if (err && cta == 0) set_err(a.err, err);
   const int n_units = (int)total;
+  if (a.G > 0 && cta == 0 && tid == 0) *w.n_units = n_units;
   for (int b = b0; b < b1; ++b) {
     first_unit[b] = (int)min(at, (int64_t)INT32_MAX);
-    at += b + 1 == b1 ? last_units : units_of(a, request_of(a, b), w.nc);
+    at += b + 1 == b1 ? last_units : units_of(a, part(b).n, w.nc);
   }
   __syncthreads();
 
   // thread -> a run of consecutive units
   const int uper = (n_units + THREADS - 1) / THREADS;
   const int u0 = (int)min((int64_t)tid * uper, (int64_t)n_units), u1 = min(u0 + uper, n_units);
-  const int first_b = u0 < u1 ? scan_owner(first_unit, a.B, u0) : 0;
+  const int first_b = u0 < u1 ? scan_owner(first_unit, N, u0) : 0;
   int64_t tiles = 0;
   ChunkUnit only{};              // of a thread that has one unit: worked out once
   auto walk = [&](auto&& visit) {
     if (u1 - u0 == 1 && tiles > 0) return visit(u0, only);
     int b = first_b;
-    Request r{};
+    Part r{};
     bool have = false;
     for (int u = u0; u < u1; ++u) {
-      while (b + 1 < a.B && first_unit[b + 1] <= u) {
+      while (b + 1 < N && first_unit[b + 1] <= u) {
         ++b;
         have = false;
       }
-      if (!have) r = request_of(a, b);
+      if (!have) r = part(b);
       have = true;
-      visit(u, unit_of(a, r, b, u - first_unit[b], w.nc));
+      visit(u, unit_of(a, r, u - first_unit[b], w.nc));
     }
   };
   walk([&](int, const ChunkUnit& e) {
@@ -147,6 +260,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
       if (u1 > u0 && u0 == cta) {
         start = only;
         start.tile0 = tile0;
+        w.units[u0] = start;
         mine.unit = u0;
         mine.t0 = tile0;
         mine.t1 = tile0 + only.tiles;
@@ -171,7 +285,8 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
     e.tile0 = tile0;
     const int64_t body = v0 + w.unit_cost, end = body + (int64_t)e.tiles * kTileCost;
     auto tile_at = [&](int64_t v) { return v < body ? 0 : (v - body) / kTileCost; };
-    if (v0 > va && v0 < vb) w.units[u] = e;
+    // the unit's first tile lies in this range (a border may lie in front of it, in the unit's own cost)
+    const bool begins = v0 < vb && va < end && tile_at(va) == 0 && (ends || vb >= end || tile_at(vb) > 0);
     if (va >= v0 && va < end) {
       start = e;
       mine.unit = u;
@@ -183,15 +298,18 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
       // in CTAs cta .. ceil(end grid / V) - 1: in slot 0 of a CTA whose range
       // starts with the unit, in slot 1 where another one is in front.
       ChunkSplit sp{};
-      if (tile_at(vb) > 0 && tile_at(va) == 0) {
+      if (begins) {
         sp.row0 = e.row0;
         sp.cols = e.cols;
         sp.parts = (int)min((end * grid + V - 1) / V, (int64_t)grid) - cta;
         sp.slot0 = 2 * cta + (va < v0 ? 1 : 0);
         sp.next = 2 * (cta + 1);
+        e.slot0 = (int16_t)sp.slot0;
+        e.parts = (int16_t)sp.parts;
       }
       w.splits[cta] = sp;
     }
+    if (begins) w.units[u] = e;
     tile0 += e.tiles;
     v0 = end;
   });

@@ -86,6 +86,9 @@ struct ChunkArgs {
   uint16_t* o;
   float* lse;
   int32_t* err;
+  const int32_t* group_cu;      // [G + 1] requests that share a prefix, nullptr without groups
+  const int32_t* prefix_lens;   // [G]
+  int G;
 };
 // Query rows of a unit of the work list, 16 or 32.
 constexpr int kFewestRows = 16;
