@@ -44,11 +44,12 @@ bool table_ok(int B, int max_pages, int page_size) {
 size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool shared, char* base) {
   // shared prefixes pack rows of several requests: 16 rows only where there are no more
   w.nc = dsa::chunk_columns(T, H, w.a.G > 0 ? 1 : B);
-  w.rows = (int64_t)T * H;
-  w.max_units = (w.rows / w.nc) * (w.a.G > 0 ? 2 : 1) + B + w.a.G;     // full units, and the last of each request and group
+  const int64_t all = (int64_t)T * H;
+  w.max_units = (all / w.nc) * (w.a.G > 0 ? 2 : 1) + B + w.a.G;     // full units, and the last of each request and group
   w.grid = sms;
-  const size_t units = (size_t)((w.rows / dsa::kFewestRows) * (shared ? 2 : 1) + B * (shared ? 2 : 1));
-  const size_t rows = (size_t)sms * 2 * dsa::chunk_columns(T, H, 1);
+  const size_t units = (size_t)((all / dsa::kFewestRows + B) * (shared ? 2 : 1));
+  w.joined0 = (int64_t)sms * 2 * dsa::chunk_columns(T, H, 1);
+  const size_t rows = (size_t)(w.joined0 + (shared ? 2 * std::min(all, (int64_t)B * dsa::kSharedRows) : 0));
   size_t end = 0;
   auto take = [&](size_t bytes) {
     char* p = base + end;
@@ -59,12 +60,7 @@ size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool share
   w.splits = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
   w.part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
   w.part_o = reinterpret_cast<float*>(take(rows * 512 * sizeof(float)));
-  if (shared) {
-    const size_t joined = (size_t)std::min(w.rows, (int64_t)B * dsa::kSharedRows) * 2;
-    w.n_units = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
-    w.row_lse = reinterpret_cast<float*>(take(joined * sizeof(float)));
-    w.row_o = reinterpret_cast<float*>(take(joined * 512 * sizeof(float)));
-  }
+  if (shared) w.n_units = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
   return end;
 }
 

@@ -76,11 +76,10 @@ struct ChunkWork {
   ChunkSplit* splits;      // [grid] by the CTA in which the unit begins
   float* part_lse;         // [2 grid][nc]
   float* part_o;           // [2 grid][nc][512] normalised
-  // with shared prefixes (a.G > 0), else nullptr:
-  int32_t* n_units;
-  int64_t rows;            // T H
-  float* row_lse;          // [2][rows] of kPrefix and kOwn units that are not spread over CTAs
-  float* row_o;            // [2][rows][512]
+  // With shared prefixes (a.G > 0) the parts are followed by rows of kPrefix and
+  // kOwn units that are not spread over CTAs: part joined0 + (side - 1) T H + row.
+  int64_t joined0;
+  int32_t* n_units;        // all of them; those of requests, which come first
 };
 // Sharing is for batches of few query rows a request; at most so many on average
 // (eight units each: packing rows could save one of them at most).

@@ -1344,7 +1344,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     const int cols = u.cols - c0;                        // of this thread's columns
     const int64_t row0 = u.row0;
     const bool final = whole && u.side == kAlone;        // else FP32, to be joined
-    const int64_t to = whole ? (u.side - kPrefix) * w.rows + row0 : part;
+    const int64_t to = whole ? w.joined0 + (int64_t)(u.side - kPrefix) * a.T * a.H + row0 : part;
     float li[CPT];
     ld_row<CPT>(&ms.by[c0], li);
     // block db's outputs of this thread's columns, normalised
@@ -1369,7 +1369,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
           if (k < cols) o[k * kD + db * 128] = __float2bfloat16_rn(y[k]);
       }
     } else {
-      float* o = (whole ? w.row_o : w.part_o) + (to + c0) * kD + row;
+      float* o = w.part_o + (to + c0) * kD + row;
 #pragma unroll
       for (int db = 0; db < 4; ++db) {
         float y[CPT];
@@ -1381,7 +1381,7 @@ __device__ void softmax_role(const ChunkWork& w, uint8_t* sm, Misc& ms, uint32_t
     }
     if (quarter == 0 && lane < CPT && lane < cols) {
       if (final) a.lse[row0 + c0 + lane] = ms.alpha[c0 + lane];
-      else (whole ? w.row_lse : w.part_lse)[to + c0 + lane] = ms.alpha[c0 + lane];
+      else w.part_lse[to + c0 + lane] = ms.alpha[c0 + lane];
     }
   }
 }

@@ -12,6 +12,7 @@
 // flight, 34.6 with 128 whose loads came after the weights; 81.8 us for 32
 // requests of 4096 rows and two tokens of 128 heads with four blocks of rows a
 // unit, 85 with sixteen.
+#include <cstddef>
 #include <cuda_bf16.h>
 
 #include "chunk.cuh"
@@ -57,13 +58,14 @@ __device__ __forceinline__ ChunkSplit split_of(const ChunkSplit* s) {
   return x.s;
 }
 
-// One slice of one row of a unit of many parts, by the whole block.
-__device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit& sp, int col, int slice) {
-  __shared__ float wt[kMaxCtas];
+// One slice of a row of many parts, part p of which lies at `slot(p)`, by the
+// whole block.
+template <class Slot>
+__device__ __forceinline__ void merge_many(const ChunkWork& w, int parts, int64_t row, int slice, Slot&& slot) {
+  __shared__ float wt[2 * kMaxCtas];
   __shared__ float red[kMergeThreads / 32], red2[kMergeThreads / 32];
   __shared__ float4 acc_s[kLanes][kSlice4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto slot = [&](int p) { return (int64_t)(p == 0 ? sp.slot0 : sp.next + 2 * (p - 1)) * w.nc + col; };
   const int pl = tid / kDimThreads, dt = tid % kDimThreads;
   float4 v[kBatch][kVec];
   auto load = [&](int p0) {
@@ -72,14 +74,14 @@ __device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit&
       const int p = p0 + q * kLanes;
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
-        v[q][i] = p < sp.parts ? __ldcg(reinterpret_cast<const float4*>(w.part_o + slot(p) * kD) + slice * kSlice4 + dt + i * kDimThreads)
+        v[q][i] = p < parts ? __ldcg(reinterpret_cast<const float4*>(w.part_o + slot(p) * kD) + slice * kSlice4 + dt + i * kDimThreads)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   load(pl);
   float m = -INFINITY;
   bool nan = false;
-  for (int p = tid; p < sp.parts; p += kMergeThreads) {
+  for (int p = tid; p < parts; p += kMergeThreads) {
     const float x = __ldcg(w.part_lse + slot(p));
     wt[p] = x;
     m = fmaxf(m, x);
@@ -91,7 +93,7 @@ __device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit&
 #pragma unroll
   for (int i = 0; i < kMergeThreads / 32; ++i) m = fmaxf(m, red[i]);
   float sum = 0.f;
-  for (int p = tid; p < sp.parts; p += kMergeThreads) {
+  for (int p = tid; p < parts; p += kMergeThreads) {
     wt[p] = nan ? __int_as_float(0x7FC00000) : m == -INFINITY ? 0.f : expf(wt[p] - m);
     sum += wt[p];
   }
@@ -102,12 +104,12 @@ __device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit&
 #pragma unroll
   for (int i = 0; i < kMergeThreads / 32; ++i) sum += red2[i];
   float4 acc[kVec] = {};
-  for (int p0 = pl; p0 < sp.parts; p0 += kLanes * kBatch) {
+  for (int p0 = pl; p0 < parts; p0 += kLanes * kBatch) {
     if (p0 != pl) load(p0);
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       const int p = p0 + q * kLanes;
-      if (p >= sp.parts) break;
+      if (p >= parts) break;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) fold(acc[i], wt[p], v[q][i]);
     }
@@ -119,8 +121,8 @@ __device__ __forceinline__ void merge_many(const ChunkWork& w, const ChunkSplit&
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kLanes; ++i) fold(o, 1.f, acc_s[i][tid]);
-    store_row(w.a, sp.row0 + col, slice * kSlice4 + tid, o, sum == 0.f ? 0.f : 1.f / sum);
-    if (tid == 0 && slice == 0) w.a.lse[sp.row0 + col] = sum == 0.f ? -INFINITY : m + logf(sum);
+    store_row(w.a, row, slice * kSlice4 + tid, o, sum == 0.f ? 0.f : 1.f / sum);
+    if (tid == 0 && slice == 0) w.a.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
   }
   __syncthreads();   // acc_s, wt and the sums are free for the next row
 }
@@ -172,209 +174,168 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
   for (int i = 0; i < (w.grid + 31) / 32; ++i)
     for (uint32_t bits = many[i]; bits != 0; bits &= bits - 1) {
       const ChunkSplit& u = big[(32 * i + __ffs(bits) - 1) / kFewParts];
-      for (; item < kSlices * u.cols; item += blocks) merge_many(w, u, item / kSlices, item % kSlices);
+      for (; item < kSlices * u.cols; item += blocks) {
+        const int col = item / kSlices;
+        merge_many(w, u.parts, u.row0 + col, item % kSlices,
+                   [&](int p) { return (int64_t)(p == 0 ? u.slot0 : u.next + 2 * (p - 1)) * w.nc + col; });
+      }
       item -= kSlices * u.cols;
     }
 }
 
 // ---- rows that share a prefix
 
-// Where the parts of a unit's rows over the prefix lie: those of its first rows,
-// and from column brk on those of the next unit of the prefix.
+// A unit of a request, and where its rows' parts over the prefix lie: those of
+// its first rows, and from column brk on those of the prefix's next unit.
 struct Join {
   int64_t row0;
-  int cols, own_slot, own_parts;       // parts 0: one part, in row_o
-  int brk, col0, slot[2], parts[2];    // column of its first row there
+  int cols, brk, col0;                 // col0: column of the first row in the prefix's unit
+  int16_t own_slot, own_parts;         // parts 0: one part, behind joined0
+  int16_t slot[2], parts[2];           // -1: no prefix
   int kind;                            // 0: nothing to do, 1: up to kFewParts parts, 2: more
 };
 
-__device__ __forceinline__ Join join_of(const ChunkWork& w, int u) {
-  union {
-    ChunkUnit u;
-    int4 v[4];
-  } x;
-  auto fetch = [&](int i) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x.v[k] = __ldcg(reinterpret_cast<const int4*>(w.units + i) + k);
-  };
-  fetch(u);
-  Join j{};
-  if (x.u.side == kPrefix || (x.u.side == kAlone && x.u.parts == 0)) return j;
-  j.row0 = x.u.row0;
-  j.cols = x.u.cols;
-  j.own_slot = x.u.slot0;
-  j.own_parts = x.u.parts;
-  j.brk = j.cols;
-  int parts = max(j.own_parts, 1);
-  if (x.u.side == kOwn) {
-    const int mate = x.u.mate;
-    j.col0 = x.u.mate_col;
-    j.brk = min(j.cols, w.nc - j.col0);
-    fetch(mate);
-    j.slot[0] = x.u.slot0;
-    j.parts[0] = max((int)x.u.parts, 0);
-    int most = max(j.parts[0], 1);
-    if (j.brk < j.cols) {
-      fetch(mate + 1);
-      j.slot[1] = x.u.slot0;
-      j.parts[1] = max((int)x.u.parts, 0);
-      most = max(most, j.parts[1]);
-    }
-    parts += most;
-  } else {
-    j.parts[0] = -1;                   // no prefix
+// The words of a unit's entry that a join needs.
+struct JoinUnit {
+  int64_t row0;
+  int cols;
+  int4 last;      // mate; slot0 and parts; side and mate_col
+  __device__ __forceinline__ void fetch(const ChunkUnit* u) {
+    row0 = __ldcg(reinterpret_cast<const long long*>(&u->row0));
+    cols = __ldcg(&u->cols);
+    last = __ldcg(reinterpret_cast<const int4*>(&u->mate));
   }
-  j.kind = parts <= kFewParts ? 1 : 2;
+};
+static_assert(offsetof(ChunkUnit, mate) == 48 && offsetof(ChunkUnit, slot0) == 52 && offsetof(ChunkUnit, parts) == 54 &&
+              offsetof(ChunkUnit, side) == 56 && offsetof(ChunkUnit, mate_col) == 57, "entry");
+
+__device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, int n_units) {
+  Join j{};
+  j.row0 = u.row0;
+  j.cols = j.brk = u.cols;
+  j.own_slot = (int16_t)u.last.y;
+  j.own_parts = (int16_t)(u.last.y >> 16);
+  j.parts[0] = -1;
+  if ((u.last.z & 0xFF) == kAlone) {
+    j.kind = j.own_parts == 0 ? 0 : j.own_parts <= kFewParts ? 1 : 2;
+    return j;
+  }
+  const int m0 = __ldcg(reinterpret_cast<const int*>(&w.units[u.last.x].slot0));
+  const int m1 = __ldcg(reinterpret_cast<const int*>(&w.units[min(u.last.x + 1, n_units - 1)].slot0));
+  j.col0 = u.last.z >> 8 & 0xFF;
+  j.brk = min(j.cols, w.nc - j.col0);
+  j.slot[0] = (int16_t)m0;
+  j.parts[0] = (int16_t)(m0 >> 16);
+  j.slot[1] = (int16_t)m1;
+  j.parts[1] = (int16_t)(m1 >> 16);
+  const int most = max((int)j.parts[0], j.brk < j.cols ? (int)j.parts[1] : 0);
+  j.kind = max((int)j.own_parts, 1) + max(most, 1) <= kFewParts ? 1 : 2;
   return j;
 }
 
 // The parts of one row: its own keys' first, then the prefix's.
 struct RowParts {
-  const ChunkWork& w;
-  int64_t row, own_at, pre_at;         // rows of part_o (or of row_o, where there is one part)
-  int own, pre;                        // parts
-  bool own_whole, pre_whole;
-  int own_next, pre_next, col, pre_col;
-  __device__ __forceinline__ RowParts(const ChunkWork& work, const Join& j, int c) : w(work), row(j.row0 + c), col(c) {
-    own_whole = j.own_parts == 0;
-    own = own_whole ? 1 : j.own_parts;
-    own_at = own_whole ? w.rows + row : (int64_t)j.own_slot * w.nc + c;
-    own_next = (j.own_slot / 2 + 1) * 2;
-    const int second = c >= j.brk;
-    const int n = second ? j.parts[1] : j.parts[0], slot = second ? j.slot[1] : j.slot[0];
-    pre_col = (j.col0 + c) % w.nc;
-    pre_whole = n == 0;
-    pre = n < 0 ? 0 : pre_whole ? 1 : n;
-    pre_at = pre_whole ? row : (int64_t)slot * w.nc + pre_col;
-    pre_next = (slot / 2 + 1) * 2;
+  int64_t row;
+  int own, n;                          // parts over its own keys, all
+  int own0, own1, pre0, pre1, step;    // where the first ones lie, and (but for the step) the others
+  __device__ __forceinline__ RowParts(const ChunkWork& w, const Join& j, int c) : row(j.row0 + c), step(2 * w.nc) {
+    const int64_t rows = (int64_t)w.a.T * w.a.H;
+    auto others = [&](int slot, int col) { return (slot / 2 * 2) * w.nc + col; };   // the k-th part: + k step
+    own = max((int)j.own_parts, 1);
+    own0 = j.own_parts == 0 ? (int)(w.joined0 + rows + row) : j.own_slot * w.nc + c;
+    own1 = others(j.own_slot, c);
+    const bool second = c >= j.brk;
+    const int parts = second ? j.parts[1] : j.parts[0], slot = second ? j.slot[1] : j.slot[0];
+    const int col = second ? c - j.brk : j.col0 + c;
+    n = own + (parts < 0 ? 0 : max(parts, 1));
+    pre0 = parts == 0 ? (int)(w.joined0 + row) : slot * w.nc + col;
+    pre1 = others(slot, col);
   }
-  __device__ __forceinline__ int count() const { return own + pre; }
-  // part p's LSE and row of 512
-  __device__ __forceinline__ void at(int p, const float*& lse, const float4*& o) const {
+  __device__ __forceinline__ int64_t at(int p) const {
     const bool mine = p < own;
     const int q = mine ? p : p - own;
-    const bool whole = mine ? own_whole : pre_whole;
-    const int64_t r = q == 0 ? (mine ? own_at : pre_at)
-                             : (int64_t)((mine ? own_next : pre_next) + 2 * (q - 1)) * w.nc + (mine ? col : pre_col);
-    lse = (whole ? w.row_lse : w.part_lse) + r;
-    o = reinterpret_cast<const float4*>((whole ? w.row_o : w.part_o) + r * kD);
+    return q == 0 ? (mine ? own0 : pre0) : (mine ? own1 : pre1) + q * step;
   }
 };
 
-// Parts p0, p0 + step, ... of a row, kInFlight of them at once: running maximum,
-// sum and V float4 of the dims, d4 + 32 i for i < V.
-template <int V, int kInFlight>
-__device__ __forceinline__ void fold_parts(const RowParts& rp, int p0, int step, int d4, float& m, float& sum, float4 (&acc)[V]) {
-  const int n = rp.count();
-  m = -INFINITY;
-  sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+// d4: the thread's four dims.
+__device__ __forceinline__ void join_few(const ChunkWork& w, const RowParts& rp, int d4) {
+  float m = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (; p0 < n; p0 += step * kInFlight) {
-    float ls[kInFlight];
-    float4 v[kInFlight][V];
+  for (int p0 = 0; p0 < rp.n; p0 += kFewParts) {
+    float ls[kFewParts];
+    float4 v[kFewParts];
 #pragma unroll
-    for (int k = 0; k < kInFlight; ++k) {
-      const int p = p0 + k * step;
-      ls[k] = -INFINITY;
-      if (p >= n) continue;
-      const float* lse;
-      const float4* o;
-      rp.at(p, lse, o);
-      ls[k] = __ldcg(lse);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] = __ldcg(o + d4 + 32 * i);
+    for (int k = 0; k < kFewParts; ++k) {
+      const bool there = p0 + k < rp.n;
+      const int64_t at = there ? rp.at(p0 + k) : 0;
+      ls[k] = there ? __ldcg(w.part_lse + at) : -INFINITY;
+      v[k] = there ? __ldcg(reinterpret_cast<const float4*>(w.part_o + at * kD) + d4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float top = m;
 #pragma unroll
-    for (int k = 0; k < kInFlight; ++k) top = fmaxf(top, ls[k]);
-    if (top != m && m != -INFINITY) {
+    for (int k = 0; k < kFewParts; ++k) top = fmaxf(top, ls[k]);
+    if (p0 > 0 && top != m) {
       const float f = expf(m - top);
       sum *= f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     }
     m = top;
 #pragma unroll
-    for (int k = 0; k < kInFlight; ++k) {
+    for (int k = 0; k < kFewParts; ++k) {
       if (ls[k] == -INFINITY) continue;            // no such part, or one without a visible key
-      const float e = expf(ls[k] - m);             // (NaN where it is: fmaxf passes it over)
+      const float e = expf(ls[k] - m);             // (NaN where one of them is: fmaxf passes it over)
       sum += e;
-#pragma unroll
-      for (int i = 0; i < V; ++i) fold(acc[i], e, v[k][i]);
+      fold(acc, e, v[k]);
     }
   }
+  store_row(w.a, rp.row, d4, acc, sum == 0.f ? 0.f : 1.f / sum);
+  if (d4 == 0) w.a.lse[rp.row] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
-constexpr int kJoinLanes = kMergeThreads / 32;     // many parts: a warp for every eighth part of a row
-constexpr int kJoinAll = 1024;                     // units up to which every block looks at all of them
+constexpr int kJoinAll = 512;                      // units of requests up to which every block looks at all of them
+constexpr int kJoinRun = 8;
 
-// Few units (and so perhaps many parts): every block knows all of them, takes
-// its share of the rows of few parts, a pair at a time, and of those of many,
-// one at a time.  Many units: a block takes runs of 32 for itself.
+// Up to kJoinAll units of requests, whose rows may have many parts: every block
+// knows all units and takes its share of the rows of few parts (a pair at a time)
+// and of the slices of those of many.  More units: a block takes runs of them.
 __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const __grid_constant__ ChunkWork w) {
   asm volatile("griddepcontrol.wait;" ::: "memory");               // every part is written
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Join joins[kMergeThreads];
-  __shared__ float lane_m[kJoinLanes], lane_sum[kJoinLanes];
-  __shared__ float4 lane_o[kJoinLanes][kD / 4];
-  const int tid = threadIdx.x, n_units = __ldcg(w.n_units);
-  const bool all = n_units <= kJoinAll;
-  const int run = all ? kMergeThreads : 32;
+  const int tid = threadIdx.x, blocks = gridDim.x;
+  JoinUnit u;
+  if (tid < w.max_units) u.fetch(w.units + tid);                   // (while the counts are on their way)
+  const int n_units = __ldcg(w.n_units), n = __ldcg(w.n_units + 1);
+  const bool all = n <= kJoinAll;
+  const int run = all ? kMergeThreads : kJoinRun;
   const int pairs = w.nc / kFewRows;
-  for (int u0 = all ? 0 : blockIdx.x * run; u0 < n_units; u0 += all ? run : run * (int)gridDim.x) {
-    const int here = min(run, n_units - u0);
+  for (int u0 = all ? 0 : blockIdx.x * run; u0 < n; u0 += all ? run : run * blocks) {
+    const int here = min(run, n - u0);
     __syncthreads();                               // the entries before are done with
-    if (tid < here) joins[tid] = join_of(w, u0 + tid);
+    if (tid < here) {
+      if (u0 > 0) u.fetch(w.units + u0 + tid);
+      joins[tid] = join_of(w, u, n_units);
+    }
     __syncthreads();
-    for (int item = all ? blockIdx.x : 0; item < here * pairs; item += all ? gridDim.x : 1) {
-      const Join& j = joins[item / pairs];
-      const int col = item % pairs * kFewRows + tid / kFewThreads, d4 = tid % kFewThreads;
-      if ((j.kind == 0 || (j.kind == 2 && all)) || col >= j.cols) continue;
-      const RowParts rp(w, j, col);
-      float m, sum;
-      float4 acc[1];
-      fold_parts<1, 4>(rp, 0, 1, d4, m, sum, acc);
-      store_row(w.a, rp.row, d4, acc[0], sum == 0.f ? 0.f : 1.f / sum);
-      if (d4 == 0) w.a.lse[rp.row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    // rows of few parts; units first, as units may have fewer rows than others
+    for (int item = all ? blockIdx.x : 0; item < here * pairs; item += all ? blocks : 1) {
+      const Join& j = joins[item % here];
+      const int col = item / here * kFewRows + tid / kFewThreads;
+      if (j.kind == 0 || (j.kind == 2 && all) || col >= j.cols) continue;
+      join_few(w, RowParts(w, j, col), tid % kFewThreads);
     }
     if (!all) continue;
     int item = blockIdx.x;                         // from the unit's first row on
     for (int i = 0; i < here; ++i) {
       const Join& j = joins[i];
       if (j.kind != 2) continue;
-      for (; item < j.cols; item += gridDim.x) {
-        const RowParts rp(w, j, item);
-        const int lane = tid & 31, warp = tid >> 5;
-        float m, sum;
-        float4 acc[4];
-        fold_parts<4, 2>(rp, warp, kJoinLanes, lane, m, sum, acc);
-        if (lane == 0) {
-          lane_m[warp] = m;
-          lane_sum[warp] = sum;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) lane_o[warp][lane + 32 * k] = acc[k];
-        __syncthreads();
-        if (tid < kD / 4) {
-          float top = -INFINITY, total = 0.f;
-#pragma unroll
-          for (int k = 0; k < kJoinLanes; ++k) top = fmaxf(top, lane_m[k]);
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < kJoinLanes; ++k) {
-            if (lane_sum[k] == 0.f) continue;      // none of its parts has a visible key
-            const float e = expf(lane_m[k] - top);
-            total = fmaf(e, lane_sum[k], total);
-            fold(o, e, lane_o[k][tid]);
-          }
-          store_row(w.a, rp.row, tid, o, total == 0.f ? 0.f : 1.f / total);
-          if (tid == 0) w.a.lse[rp.row] = total == 0.f ? -INFINITY : top + logf(total);
-        }
-        __syncthreads();
+      for (; item < kSlices * j.cols; item += blocks) {
+        const RowParts rp(w, j, item / kSlices);
+        merge_many(w, rp.n, rp.row, item % kSlices, [&](int p) { return rp.at(p); });
       }
-      item -= j.cols;
+      item -= kSlices * j.cols;
     }
   }
 }

@@ -86,10 +86,13 @@ struct Groups {
 // A group shares a whole number of tiles of its prefix, at most what its first
 // tokens all see, and only where packing its rows takes less than each request
 // reading those tiles for itself (the cost of a unit counted as the ranges do).
-// Requests with lengths out of range end the sharing of their group, offsets out
+// All groups together have to save what joining the rows takes, about two tiles
+// of every CTA.  Requests with lengths out of range end the sharing of their group, offsets out
 // of order that of all.
+constexpr int kJoinCost = 2 * kTileCost;
+
 template <int THREADS>
-__device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch) {
+__device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch, int64_t* sums) {
   const ChunkArgs& a = w.a;
   const int tid = threadIdx.x, G = a.G;
   int32_t* cu = scratch;
@@ -121,6 +124,7 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
     }
     __syncthreads();
   }
+  int64_t saved = 0;
   for (int i = tid; i < G; i += THREADS) {
     const int tiles = g.first[i] == INT32_MAX ? 0 : min(g.keys[i], __ldg(a.prefix_lens + i)) / kChunkTile;
     int keys = 0;
@@ -128,10 +132,17 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
       const int n = __ldg(a.cu_q + cu[i + 1]) - __ldg(a.cu_q + cu[i]);
       const int64_t apart = (int64_t)g.units[i] * tiles * kTileCost;
       const int64_t packed = (int64_t)units_of(a, n, w.nc) * (tiles * kTileCost + w.unit_cost);
-      if (packed < apart) keys = tiles * kChunkTile;
+      if (packed < apart) {
+        keys = tiles * kChunkTile;
+        saved += apart - packed;
+      }
     }
     g.keys[i] = keys;
   }
+  int64_t all;
+  block_scan<THREADS>(saved, &all, sums);
+  if (all < (int64_t)w.grid * kJoinCost)
+    for (int i = tid; i < G; i += THREADS) g.keys[i] = 0;
   __syncthreads();
   return g;
 }
@@ -163,39 +174,39 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   int32_t* first_unit = reinterpret_cast<int32_t*>(scratch);                             // [N]
   const ChunkArgs& a = w.a;
   const int tid = threadIdx.x, cta = blockIdx.x;
-  const int N = a.G + a.B;         // parts: the groups' prefixes, then the requests
+  const int N = a.B + a.G;         // parts: the requests, then the groups' prefixes
   Groups groups{};
-  if (a.G > 0) groups = find_groups<THREADS>(w, first_unit + N);
+  if (a.G > 0) groups = find_groups<THREADS>(w, first_unit + N, sums);
   int err = 0;
   auto part = [&](int p) -> Part {
     Part x{};
-    if (p < a.G) {
+    if (p >= a.B) {
+      const int g = p - a.B;
       x.side = kPrefix;
-      x.kv = x.vis0 = groups.keys[p];
+      x.kv = x.vis0 = groups.keys[g];
       if (x.kv > 0) {
-        x.b = groups.first[p];
-        x.t0 = __ldg(a.cu_q + groups.cu[p]);
-        x.n = __ldg(a.cu_q + groups.cu[p + 1]) - x.t0;
+        x.b = groups.first[g];
+        x.t0 = __ldg(a.cu_q + groups.cu[g]);
+        x.n = __ldg(a.cu_q + groups.cu[g + 1]) - x.t0;
       }
       return x;
     }
-    const int b = p - a.G;
-    const Request r = request_of(a, b);
+    const Request r = request_of(a, p);
     err |= r.err;
     x.t0 = r.t0;
     x.n = r.n;
-    x.b = b;
+    x.b = p;
     x.kv = r.kv;
     x.vis0 = first_visible(a, r);
-    if (a.G > 0 && r.n > 0 && b >= groups.cu[0] && b < groups.cu[a.G]) {
-      const int g = scan_owner(groups.cu, a.G, b);
+    if (a.G > 0 && r.n > 0 && p >= groups.cu[0] && p < groups.cu[a.G]) {
+      const int g = scan_owner(groups.cu, a.G, p);
       if (groups.keys[g] > 0) {
         x.side = kOwn;
         x.key0 = groups.keys[g];
         x.kv -= x.key0;
         x.vis0 -= x.key0;
         x.group_row0 = (int64_t)__ldg(a.cu_q + groups.cu[g]) * a.H;
-        x.group_unit = first_unit[g];      // (once the sums are there)
+        x.group_unit = first_unit[a.B + g];      // (once the sums are there)
       }
     }
     return x;
@@ -216,12 +227,15 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   }
   if (err && cta == 0) set_err(a.err, err);
   const int n_units = (int)total;
-  if (a.G > 0 && cta == 0 && tid == 0) *w.n_units = n_units;
   for (int b = b0; b < b1; ++b) {
     first_unit[b] = (int)min(at, (int64_t)INT32_MAX);
     at += b + 1 == b1 ? last_units : units_of(a, part(b).n, w.nc);
   }
   __syncthreads();
+  if (a.G > 0 && cta == 0 && tid == 0) {
+    w.n_units[0] = n_units;
+    w.n_units[1] = min(first_unit[a.B], n_units);
+  }
 
   // thread -> a run of consecutive units
   const int uper = (n_units + THREADS - 1) / THREADS;

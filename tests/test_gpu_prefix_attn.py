@@ -60,6 +60,13 @@ def make(groups, H, layout, page=64, seed=0, alone=((), ()), lead=0, tail=0, qam
                 causal=causal)
 
 
+def enough(H, news, sms=152):
+    """Keys of a prefix that pays for news[b] new tokens of the group's requests: packing their rows saves a unit's tiles
+    as often as units get fewer, and has to save two tiles a CTA, beside what a packed unit costs (below three tiles)."""
+    units, packed = sum(-(-n * H // 32) for n in news), -(-sum(news) * H // 32)
+    return 128 * -(-(2 * sms + 3 * packed) // (units - packed))
+
+
 def hide_shared(w, keys):
     """Takes the first keys[g] keys' whole pages out of the rows of every request of group g but the first."""
     t = w["table"].clone()
@@ -115,15 +122,20 @@ def check(w, err_want=0, hidden=None, only=None, **kw):
     return whole_o, whole_lse
 
 
-ONE = [(1, c) for c in (0, 1, 60, 127, 128, 129, 300, 5)]
+ONE = [(1, c) for c in (0, 1, 60, 127, 128, 129, 300, 5, 9, 200, 31, 2, 70, 400, 33, 8)]
+MIXED = [(1, 3), (2, 200), (1, 0), (3, 50), (1, 129), (1, 9), (2, 0), (1, 64), (1, 300), (2, 5), (1, 1), (1, 90)]
+
+
+def common(H, members=ONE):
+    return enough(H, [m[0] for m in members])
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("H", [1, 4, 8, 16, 20])
 def test_single_tokens(layout, H):
-    """Eight requests of one token behind five tiles: their rows are packed."""
-    w = make([(640, ONE)], H, layout, seed=H)
-    check(w, hidden=[640])
+    """Requests of one token: their rows are packed."""
+    w = make([(common(H), ONE)], H, layout, seed=H)
+    check(w, hidden=[common(H)])
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
@@ -137,60 +149,67 @@ def test_heads_that_fill_the_tiles(layout, H):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
-@pytest.mark.parametrize("prefix", [1, 127, 128, 129, 500, 1024])
-def test_prefix_lengths(layout, prefix):
-    """Prefixes that end inside a tile, and inside a page; none that fills a tile."""
-    check(make([(prefix, [(1, 3), (2, 200), (1, 0), (3, 50), (1, 129)])], 8, layout, seed=prefix))
+@pytest.mark.parametrize("more", [-1, 0, 1, 63, 127])
+def test_prefix_lengths(layout, more):
+    """Prefixes that end inside a tile, and inside a page; one that is a key too short to pay; hardly any."""
+    p = common(8, MIXED) + more
+    check(make([(p, MIXED)], 8, layout, seed=p), hidden=[p // 128 * 128] if more >= 0 else None)
+    check(make([(1 + more // 2, MIXED[:5])], 8, layout, seed=p) if more > 0 else make([(500, MIXED[:5])], 8, layout, seed=p))
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("page", [1, 3, 16, 48, 256, 1000])
 def test_page_sizes(layout, page):
-    w = make([(700, [(1, 30), (2, 140), (1, 0), (1, 300), (1, 7)])], 8, layout, page=page, seed=page)
-    check(w, hidden=[640])
+    p = common(8, MIXED)
+    w = make([(p + 60, MIXED)], 8, layout, page=page, seed=page)
+    check(w, hidden=[p])
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_groups_and_requests_alone(layout):
     """Groups of several sizes, one of a single request, an empty one; requests of none in front and behind; rows of no
     request; requests without new tokens, a group that begins with one."""
-    groups = [(512, [(1, 9), (1, 100), (2, 0), (1, 33), (1, 1)]), (300, [(2, 10)]), (200, []),
-              (900, [(0, 5), (1, 70), (1, 3), (0, 0), (3, 200), (1, 1), (1, 2)])]
+    groups = [(2000, MIXED), (300, [(2, 10)]), (200, []), (1500, [(0, 5), (1, 70), (1, 3), (0, 0), (3, 200)] + ONE)]
     w = make(groups, 8, layout, page=16, seed=3, alone=([(1, 50), (40, 0)], [(0, 7), (2, 400), (1, 0)]), lead=3, tail=5)
+    w["table"][int(w["gcu"][3])] = -1                      # of the request without new tokens: nothing is read through it
     check(w)
 
 
 @pytest.mark.parametrize("layout", ["raw512", "fp4_416"])
 def test_chunks_behind_a_prefix(layout):
     """Drafted tokens and chunks: rows of a request over several tiles, and over two tiles of the packed rows."""
-    check(make([(1300, [(n, c) for n, c in zip((5, 3, 7, 1, 6, 2), (0, 90, 4, 300, 128, 1))])], 5, layout, seed=4))
-    check(make([(600, [(40, 10), (33, 0), (21, 77)])], 3, layout, seed=5))
+    m = [(n, c) for n, c in zip((5, 3, 7, 1, 6, 2, 5, 3, 9, 1, 8, 4), (0, 90, 4, 300, 128, 1, 2, 60, 11, 0, 31, 200))]
+    check(make([(common(5, m), m)], 5, layout, seed=4), hidden=[common(5, m)])
+    m = [(12, 10), (23, 0), (21, 77), (13, 5), (2, 0), (34, 1), (1, 0), (12, 3)]
+    check(make([(common(3, m), m)], 3, layout, seed=5), hidden=[common(3, m)])
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_not_causal_and_large_queries(layout):
-    check(make([(640, ONE[:6])], 8, layout, seed=6, causal=False))
+    p = common(8)
+    check(make([(p, ONE)], 8, layout, seed=6, causal=False), hidden=[p])
     check(make([(640, [(3, 0), (2, 40), (4, 300)])], 4, layout, seed=7, causal=False))
-    check(make([(640, ONE[:6])], 8, layout, seed=8, qamp=40.0))
+    check(make([(p, ONE)], 8, layout, seed=8, qamp=40.0), hidden=[p])
 
 
 @pytest.mark.parametrize("layout", ["raw512", "rope656"])
 def test_copies_of_the_prefix(layout):
     """Each request holds the rows in pages of its own."""
-    check(make([(640, ONE[:5])], 8, layout, seed=9, copies=True))
+    check(make([(common(8), ONE)], 8, layout, seed=9, copies=True))
 
 
 @pytest.mark.parametrize("layout", ["raw512", "scaled528", "fp4_416"])
 def test_requests_shorter_than_the_prefix(layout):
     """What is shared ends with what every first token sees."""
-    w = make([(640, ONE[:5])], 8, layout, seed=10)
-    w["kv"][2] = 300
-    check(w, hidden=[256])
+    p = common(8)
+    w = make([(p + 900, ONE)], 8, layout, seed=10)
+    w["kv"][2] = p + 44
+    check(w, hidden=[p])
     w["kv"][2] = 100                                       # below a tile: nobody shares
     check(w)
     w["kv"][3] = 1
     check(w)
-    w = make([(640, [(5, 0), (1, 3), (1, 9)])], 8, layout, seed=11)
+    w = make([(p, [(5, 0)] + ONE)], 8, layout, seed=11)
     w["kv"][0] = 3                                         # more new tokens than keys: the first see none
     check(w)
 
@@ -214,27 +233,31 @@ def test_many_requests(layout):
 
 def test_most_requests():
     r = random.Random(14)
-    w = make([(256, [(1, r.randint(0, 9)) for _ in range(4096)])], 4, "raw512", seed=14)
-    check(w, only=[0, 1, 2000, 4095])
-    w = make([(256, [(1, 3), (1, 5)]) for _ in range(2048)], 4, "raw512", seed=15)     # as many groups as pairs
-    check(w, only=[0, 1, 2000, 2001, 4095])
+    w = make([(256, [(1, r.randint(0, 9)) for _ in range(4096)])], 4, "raw512", page=16, seed=14)
+    check(w, hidden=[256], only=[0, 1, 2000, 4095])
+    w = make([(640, [(1, 3), (1, 5)]) for _ in range(300)], 4, "raw512", page=16, seed=15)
+    check(w, hidden=[640] * 300, only=[0, 1, 301, 598, 599])
+    w = make([], 4, "raw512", page=16, seed=15, alone=([(1, 5)] * 4096, []))           # as many groups as requests
+    w["gcu"], w["plens"] = torch.arange(4097, dtype=torch.int32), torch.full((4096,), 128, dtype=torch.int32)
+    check(w, only=[0, 1, 4095])
 
 
 @pytest.mark.parametrize("gcu,plens", [([0, 3, 2, 5], [640, 640, 640]), ([-1, 2, 3, 5], [640] * 3), ([0, 2, 3, 6], [640] * 3),
                                        ([0, 2, 4, 5], [640, -1, 640]), ([5, 3, 1, 0], [640] * 3)])
 def test_bad_groups(gcu, plens):
     """Flagged; every request attends alone, so the results are right."""
-    w = make([(640, ONE[:5])], 8, "raw512", seed=16)
+    w = make([(common(8), ONE[:5])], 8, "raw512", seed=16)
     w["gcu"], w["plens"] = torch.tensor(gcu, dtype=torch.int32), torch.tensor(plens, dtype=torch.int32)
     check(w, err_want=binding.DSA_DEV_ERR_LENGTH)
 
 
 def test_prefix_longer_than_anything():
-    w = make([(640, ONE[:5])], 8, "raw512", seed=17)
+    p = common(8)
+    w = make([(p, ONE)], 8, "raw512", seed=17)
     w["plens"][0] = 2 ** 31 - 1
     # every request's keys but its last one are taken for common rows: only those of the first are read
-    w["kv"][:] = 641
-    check(w, hidden=[640])
+    w["kv"][:] = p + 1
+    check(w, hidden=[p])
 
 
 def test_no_groups():
@@ -248,31 +271,33 @@ def test_no_groups():
 def test_bad_lengths_and_pages(layout):
     """A request with offsets out of order or a length beyond the table ends its group's sharing and is flagged, a bad page
     in the first request's row masks its keys for the group."""
-    w = make([(640, ONE[:5])], 8, layout, seed=19, tail=3)
+    p, n = common(8), len(ONE)
+    w = make([(p, ONE)], 8, layout, seed=19, tail=3)
     wide, name = (fp4_ref.expand(w["pool"].numpy()), WIDE[layout]) if layout in WIDE else (w["pool"], layout)
     bound = (lambda table: ref.chunk_attn(w["q"], wide, name, table, 64, w["cu"], w["kv"], SCALE))
+    kv1 = int(w["kv"][1])
     w["kv"][1] = 10 ** 6
     o, lse, err = run(w)
     assert err & binding.DSA_DEV_ERR_LENGTH
     ro, rl, otol, ltol, _ = bound(w["table"])
-    for t in (0, 2, 3, 4):
+    for t in (0, 2, 3, n - 1):
         assert ((o[t].double() - ro[t]).abs() <= otol[t]).all() and ((lse[t].double() - rl[t]).abs() <= ltol[t]).all()
-    w["kv"][1] = w["kv"][0]
+    w["kv"][1] = kv1
+    shown = w["table"].clone()
     w["table"][0, 3] = -7
     o, lse, err = run(w)
     assert err == binding.DSA_DEV_ERR_PAGE_RANGE
-    masked = w["table"].clone()
-    masked[:, 3] = -7
-    want = bound(masked)
-    n = 5
-    assert ((o[:n].double() - want[0][:n]).abs() <= want[2][:n]).all() and ((lse[:n].double() - want[1][:n]).abs() <= want[3][:n]).all()
+    shown[:, 3] = -7
+    ro, rl, otol, ltol, _ = bound(shown)
+    assert ((o[:n].double() - ro[:n]).abs() <= otol[:n]).all() and ((lse[:n].double() - rl[:n]).abs() <= ltol[:n]).all()
     assert (o[n:] == 7.0).all()
 
 
 @pytest.mark.parametrize("layout", ["raw512", "scaled528", "fp4_288"])
 def test_nan_rows(layout):
     """In the prefix: every result is NaN; behind one request's own rows: its results alone."""
-    w = make([(640, ONE[:5])], 8, layout, seed=20)
+    p = common(8)
+    w = make([(p, ONE)], 8, layout, seed=20)
     row = (lambda b, j: int(w["table"][b, j // 64]) * 64 + j % 64)
     clean = w["pool"].clone()
     at = slice(0, 1) if layout == "raw512" else slice(512, 516) if layout == "scaled528" else slice(256, 260)
@@ -281,18 +306,21 @@ def test_nan_rows(layout):
     o, lse, err = run(w)
     assert err == 0 and o.isnan().any(-1).all() and lse.isnan().all()
     w["pool"] = clean.clone()
-    w["pool"][row(2, 660), at] = nan
+    w["pool"][row(2, p + 20), at] = nan
     o, lse, err = run(w)
-    assert err == 0 and lse[2].isnan().all() and torch.isfinite(lse[[0, 1, 3, 4]]).all() and torch.isfinite(o[[0, 1, 3, 4]]).all()
+    rest = [t for t in range(len(ONE)) if t != 2]
+    assert err == 0 and lse[2].isnan().all() and torch.isfinite(lse[rest]).all() and torch.isfinite(o[rest].float()).all()
 
 
 def test_captured_steps():
     """A captured call serves other lengths, groups and prefixes, with a workspace that eager calls use as well."""
-    w = make([(640, ONE)], 8, "rope656", seed=21)
+    p, B = common(8), len(ONE)
+    w = make([(p, ONE)], 8, "rope656", seed=21)
+    most = w["kv"].clone()
     d = {k: v.cuda() for k, v in w.items() if isinstance(v, torch.Tensor)}
-    T, H = 8, 8
+    T, H = B, 8
     o, lse = torch.zeros(T, H, 512, dtype=BF, device="cuda"), torch.zeros(T, H, device="cuda")
-    ws = binding.prefix_workspace_for(T, H, 8, "rope656")
+    ws = binding.prefix_workspace_for(T, H, B, "rope656")
 
     def step():
         binding.dsa_prefix_attn(d["q"], d["pool"], "rope656", d["table"], 64, d["cu"], d["kv"], d["gcu"], d["plens"], SCALE, o, lse, ws)
@@ -301,8 +329,8 @@ def test_captured_steps():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
-    for kv0, gcu, plen in ((640, [0, 8], 640), (300, [0, 5], 200), (641, [2, 3], 640), (130, [0, 0], 0), (640, [1, 8], 512)):
-        w["kv"] = torch.tensor([kv0 + i for i in range(8)], dtype=torch.int32).clamp(max=641)
+    for kv0, gcu, plen in ((p, [0, B], p), (300, [0, 5], 200), (p + 1, [2, 3], 640), (130, [0, 0], 0), (p + 9, [1, B], p)):
+        w["kv"] = torch.minimum(torch.tensor([kv0 + 1 + 7 * i for i in range(B)], dtype=torch.int32), most)
         w["gcu"], w["plens"] = torch.tensor(gcu, dtype=torch.int32), torch.tensor([plen], dtype=torch.int32)
         for k in ("kv", "gcu", "plens"):
             d[k].copy_(w[k])
@@ -316,7 +344,7 @@ def test_captured_steps():
 
 def test_streams_and_repeats():
     """Calls on two streams with a workspace each, over and over: the same bits."""
-    ws = [make([(1280, [(1, 9 * i) for i in range(20)])], 8, lay, seed=22) for lay in ("raw512", "fp4_416")]
+    ws = [make([(3200, [(1, 9 * i) for i in range(20)])], 8, lay, seed=22) for lay in ("raw512", "fp4_416")]
     want = [check(w, only=[0, 7, 19]) for w in ws]
     streams = [torch.cuda.Stream() for _ in ws]
     dev, outs = [], []
@@ -339,7 +367,7 @@ def test_streams_and_repeats():
 @pytest.mark.parametrize("layout", ["raw512", "rope656", "fp4_416"])
 def test_wait_that_runs_out(layout):
     """A limit of zero: the call returns, reports the timeout, leaves rows of no request alone, and the next is right."""
-    w = make([(2000, [(1, 9 * i) for i in range(20)])], 8, layout, seed=23, lead=2, tail=3)
+    w = make([(3200, [(1, 9 * i) for i in range(20)])], 8, layout, seed=23, lead=2, tail=3)
     old = binding.dsa_set_wait_limit_ns(0)
     try:
         o, lse, err = run(w)
@@ -354,7 +382,7 @@ def test_wait_that_runs_out(layout):
 def test_workspace_of_larger_calls():
     """One workspace for every smaller call."""
     ws = binding.prefix_workspace_for(64, 16, 32, "rope656")
-    check(make([(640, ONE)], 8, "rope656", seed=24), ws=ws)
+    check(make([(common(8), ONE)], 8, "rope656", seed=24), ws=ws)
     check(make([(640, ONE[:3])], 16, "rope656", seed=25), ws=ws)
     check(make([(640, [(9, 0), (20, 5)])], 16, "rope656", seed=26), ws=ws)
 
