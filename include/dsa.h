@@ -576,13 +576,15 @@ size_t dsa_prefix_attn_workspace_bytes(int T, int H, int B, int layout);
  * the group's first request that has new tokens.  Results are those of
  * dsa_chunk_attn (two partial softmaxes are joined in FP32; a result is off by
  * no more, but need not have the same bits).
- * Prefixes are used as far as it pays and holds for the whole group: rounded down
- * to 128 keys, at most what the first new token of each of the group's requests
- * sees, and only where packing the rows of several requests into tiles of 32 takes
- * less work than each request's own pass (few query rows a request: at most 32 of
- * the last tile's rows are saved each).  Requests outside every group, and those of
- * a group of one, attend alone.  With more than 256 query rows (tokens x heads) a
- * request on average nothing is shared.
+ * A prefix is used as far as it holds for the whole group: rounded down to 128
+ * keys, at most what the first new token of each of its requests sees; and where
+ * it pays: query rows (tokens x heads) are worked on 32 at a time, so that there is
+ * something to save where requests have few of them (single or drafted tokens of a
+ * few heads), and all groups together have to save about two passes over 128 keys a
+ * multiprocessor.  Otherwise, and for requests outside every group or in a group of
+ * one, this is dsa_chunk_attn.  A call that could not share by its sizes (more than
+ * 256 query rows a request on average, or a page table without room for enough
+ * common keys) does not look at the groups.
  *   group_cu_dev     [G + 1] int32 ascending within [0, B], prefix_lens_dev [G]
  *                    int32, at least 0, read on the GPU; otherwise
  *                    (DSA_DEV_ERR_LENGTH) the call's requests attend alone.

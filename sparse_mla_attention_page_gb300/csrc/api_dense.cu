@@ -125,7 +125,7 @@ int attend(const dsa::ChunkArgs& a, int kv_row_dim, bool shared, void* workspace
   if (st != DSA_OK) return st;
   dsa::ChunkWork w{};
   w.a = a;
-  if ((int64_t)a.T * a.H > (int64_t)a.B * dsa::kSharedRows) w.a.G = 0;
+  if (!dsa::sharing_possible(a, sms)) w.a.G = 0;
   lay_out_chunk(w, a.T, a.H, a.B, sms, shared, static_cast<char*>(workspace));
   w.wait_ns = dsa::wait_limit_ns();
   cudaGetLastError();

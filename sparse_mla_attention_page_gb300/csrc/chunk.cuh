@@ -84,6 +84,14 @@ struct ChunkWork {
 // Sharing is for batches of few query rows a request; at most so many on average
 // (eight units each: packing rows could save one of them at most).
 constexpr int kSharedRows = 256;
+// What all groups together have to save, a CTA: about two tiles, for the join.
+constexpr int kJoinCost = 2 * kTileCost;
+// Whether the groups could: packing rows saves less than a unit a request, of
+// the tiles that the page table has room for.
+inline bool sharing_possible(const ChunkArgs& a, int ctas) {
+  return (int64_t)a.T * a.H <= (int64_t)a.B * kSharedRows &&
+         (int64_t)(a.B - 1) * ((int64_t)a.max_pages * a.page_size / kChunkTile) * kTileCost >= (int64_t)ctas * kJoinCost;
+}
 
 // Keys that row r of a unit's request sees.
 __device__ __forceinline__ int chunk_visible(const ChunkArgs& a, const ChunkUnit& u, int col) {

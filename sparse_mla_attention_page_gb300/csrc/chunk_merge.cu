@@ -185,6 +185,10 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
 
 // ---- rows that share a prefix
 
+// Rows of up to so many parts are joined by a thread for each 4 dims, kFewParts
+// parts at a time; with more, which only few rows have, by slices.
+constexpr int kLoopParts = 24;
+
 // A unit of a request, and where its rows' parts over the prefix lie: those of
 // its first rows, and from column brk on those of the prefix's next unit.
 struct Join {
@@ -192,7 +196,7 @@ struct Join {
   int cols, brk, col0;                 // col0: column of the first row in the prefix's unit
   int16_t own_slot, own_parts;         // parts 0: one part, behind joined0
   int16_t slot[2], parts[2];           // -1: no prefix
-  int kind;                            // 0: nothing to do, 1: up to kFewParts parts, 2: more
+  int kind;                            // 0: nothing to do, 1: up to kLoopParts parts, 2: more
 };
 
 // The words of a unit's entry that a join needs.
@@ -217,7 +221,7 @@ __device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, i
   j.own_parts = (int16_t)(u.last.y >> 16);
   j.parts[0] = -1;
   if ((u.last.z & 0xFF) == kAlone) {
-    j.kind = j.own_parts == 0 ? 0 : j.own_parts <= kFewParts ? 1 : 2;
+    j.kind = j.own_parts == 0 ? 0 : j.own_parts <= kLoopParts ? 1 : 2;
     return j;
   }
   const int m0 = __ldcg(reinterpret_cast<const int*>(&w.units[u.last.x].slot0));
@@ -229,7 +233,7 @@ __device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, i
   j.slot[1] = (int16_t)m1;
   j.parts[1] = (int16_t)(m1 >> 16);
   const int most = max((int)j.parts[0], j.brk < j.cols ? (int)j.parts[1] : 0);
-  j.kind = max((int)j.own_parts, 1) + max(most, 1) <= kFewParts ? 1 : 2;
+  j.kind = max((int)j.own_parts, 1) + max(most, 1) <= kLoopParts ? 1 : 2;
   return j;
 }
 

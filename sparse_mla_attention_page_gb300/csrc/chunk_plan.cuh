@@ -89,8 +89,6 @@ struct Groups {
 // All groups together have to save what joining the rows takes, about two tiles
 // of every CTA.  Requests with lengths out of range end the sharing of their group, offsets out
 // of order that of all.
-constexpr int kJoinCost = 2 * kTileCost;
-
 template <int THREADS>
 __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch, int64_t* sums) {
   const ChunkArgs& a = w.a;

@@ -248,6 +248,8 @@ def test_bad_groups(gcu, plens):
     """Flagged; every request attends alone, so the results are right."""
     w = make([(common(8), ONE[:5])], 8, "raw512", seed=16)
     w["gcu"], w["plens"] = torch.tensor(gcu, dtype=torch.int32), torch.tensor(plens, dtype=torch.int32)
+    check(w)                                               # (too small a call to share: the groups are not looked at)
+    w["table"] = torch.cat([w["table"], torch.full((5, 200), -1, dtype=torch.int32)], 1)
     check(w, err_want=binding.DSA_DEV_ERR_LENGTH)
 
 
