@@ -318,11 +318,14 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const __
   for (int u0 = all ? 0 : blockIdx.x * run; u0 < n; u0 += all ? run : run * blocks) {
     const int here = min(run, n - u0);
     __syncthreads();                               // the entries before are done with
+    bool many = false;
     if (tid < here) {
       if (u0 > 0) u.fetch(w.units + u0 + tid);
-      joins[tid] = join_of(w, u, n_units);
+      const Join j = join_of(w, u, n_units);
+      many = j.kind == 2;
+      joins[tid] = j;
     }
-    __syncthreads();
+    many = __syncthreads_or(many) != 0;
     // rows of few parts; units first, as units may have fewer rows than others
     for (int item = all ? blockIdx.x : 0; item < here * pairs; item += all ? blocks : 1) {
       const Join& j = joins[item % here];
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const __
       if (j.kind == 0 || (j.kind == 2 && all) || col >= j.cols) continue;
       join_few(w, RowParts(w, j, col), tid % kFewThreads);
     }
-    if (!all) continue;
+    if (!all || !many) continue;
     int item = blockIdx.x;                         // from the unit's first row on
     for (int i = 0; i < here; ++i) {
       const Join& j = joins[i];
