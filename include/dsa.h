@@ -580,7 +580,7 @@ size_t dsa_prefix_attn_workspace_bytes(int T, int H, int B, int layout);
  * keys, at most what the first new token of each of its requests sees; and where
  * it pays: query rows (tokens x heads) are worked on 32 at a time, so that there is
  * something to save where requests have few of them (single or drafted tokens of a
- * few heads), and all groups together have to save about two passes over 128 keys a
+ * few heads), and all groups together have to save about four passes over 128 keys a
  * multiprocessor.  Otherwise, and for requests outside every group or in a group of
  * one, this is dsa_chunk_attn.  A call that could not share by its sizes (more than
  * 256 query rows a request on average, or a page table without room for enough

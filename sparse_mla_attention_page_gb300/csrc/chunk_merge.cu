@@ -213,7 +213,9 @@ struct JoinUnit {
 static_assert(offsetof(ChunkUnit, mate) == 48 && offsetof(ChunkUnit, slot0) == 52 && offsetof(ChunkUnit, parts) == 54 &&
               offsetof(ChunkUnit, side) == 56 && offsetof(ChunkUnit, mate_col) == 57, "entry");
 
-__device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, int n_units) {
+// parts_of(m): the word of unit m that holds its slot0 and parts.
+template <class PartsOf>
+__device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, int n_units, PartsOf&& parts_of) {
   Join j{};
   j.row0 = u.row0;
   j.cols = j.brk = u.cols;
@@ -224,8 +226,7 @@ __device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, i
     j.kind = j.own_parts == 0 ? 0 : j.own_parts <= kLoopParts ? 1 : 2;
     return j;
   }
-  const int m0 = __ldcg(reinterpret_cast<const int*>(&w.units[u.last.x].slot0));
-  const int m1 = __ldcg(reinterpret_cast<const int*>(&w.units[min(u.last.x + 1, n_units - 1)].slot0));
+  const int m0 = parts_of(u.last.x), m1 = parts_of(min(u.last.x + 1, n_units - 1));
   j.col0 = u.last.z >> 8 & 0xFF;
   j.brk = min(j.cols, w.nc - j.col0);
   j.slot[0] = (int16_t)m0;
@@ -304,14 +305,16 @@ constexpr int kJoinRun = 8;
 // Up to kJoinAll units of requests, whose rows may have many parts: every block
 // knows all units and takes its share of the rows of few parts (a pair at a time)
 // and of the slices of those of many.  More units: a block takes runs of them.
-__global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const __grid_constant__ ChunkWork w) {
+__global__ void __launch_bounds__(kMergeThreads, 3) prefix_merge_kernel(const __grid_constant__ ChunkWork w) {
   asm volatile("griddepcontrol.wait;" ::: "memory");               // every part is written
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Join joins[kMergeThreads];
+  __shared__ int near[kMergeThreads];              // slot0 and parts of the first units
   const int tid = threadIdx.x, blocks = gridDim.x;
-  JoinUnit u;
+  JoinUnit u{};
   if (tid < w.max_units) u.fetch(w.units + tid);                   // (while the counts are on their way)
   const int n_units = __ldcg(w.n_units), n = __ldcg(w.n_units + 1);
+  near[tid] = u.last.y;
   const bool all = n <= kJoinAll;
   const int run = all ? kMergeThreads : kJoinRun;
   const int pairs = w.nc / kFewRows;
@@ -321,7 +324,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const __
     bool many = false;
     if (tid < here) {
       if (u0 > 0) u.fetch(w.units + u0 + tid);
-      const Join j = join_of(w, u, n_units);
+      const Join j = join_of(w, u, n_units, [&](int m) {
+        return m < kMergeThreads ? near[m] : __ldcg(reinterpret_cast<const int*>(&w.units[m].slot0));
+      });
       many = j.kind == 2;
       joins[tid] = j;
     }
@@ -368,7 +373,7 @@ bool launch_chunk_merge(const ChunkWork& w, cudaStream_t stream) {
 }
 
 bool launch_prefix_merge(const ChunkWork& w, cudaStream_t stream) {
-  return launch_merge(prefix_merge_kernel, dim3(w.grid * 4), w, stream);
+  return launch_merge(prefix_merge_kernel, dim3(w.grid * 3), w, stream);
 }
 
 }  // namespace dsa

@@ -86,8 +86,7 @@ struct Groups {
 // A group shares a whole number of tiles of its prefix, at most what its first
 // tokens all see, and only where packing its rows takes less than each request
 // reading those tiles for itself (the cost of a unit counted as the ranges do).
-// All groups together have to save what joining the rows takes, about two tiles
-// of every CTA.  Requests with lengths out of range end the sharing of their group, offsets out
+// All groups together have to save what joining the rows takes (kJoinCost).  Requests with lengths out of range end the sharing of their group, offsets out
 // of order that of all.
 template <int THREADS>
 __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch, int64_t* sums) {

@@ -62,9 +62,9 @@ def make(groups, H, layout, page=64, seed=0, alone=((), ()), lead=0, tail=0, qam
 
 def enough(H, news, sms=152):
     """Keys of a prefix that pays for news[b] new tokens of the group's requests: packing their rows saves a unit's tiles
-    as often as units get fewer, and has to save two tiles a CTA, beside what a packed unit costs (below three tiles)."""
+    as often as units get fewer, and has to save four tiles a CTA, beside what a packed unit costs (below three tiles)."""
     units, packed = sum(-(-n * H // 32) for n in news), -(-sum(news) * H // 32)
-    return 128 * -(-(2 * sms + 3 * packed) // (units - packed))
+    return 128 * -(-(4 * sms + 3 * packed) // (units - packed))
 
 
 def hide_shared(w, keys):
@@ -169,7 +169,7 @@ def test_page_sizes(layout, page):
 def test_groups_and_requests_alone(layout):
     """Groups of several sizes, one of a single request, an empty one; requests of none in front and behind; rows of no
     request; requests without new tokens, a group that begins with one."""
-    groups = [(2000, MIXED), (300, [(2, 10)]), (200, []), (1500, [(0, 5), (1, 70), (1, 3), (0, 0), (3, 200)] + ONE)]
+    groups = [(8000, MIXED), (300, [(2, 10)]), (200, []), (6000, [(0, 5), (1, 70), (1, 3), (0, 0), (3, 200)] + ONE)]
     w = make(groups, 8, layout, page=16, seed=3, alone=([(1, 50), (40, 0)], [(0, 7), (2, 400), (1, 0)]), lead=3, tail=5)
     w["table"][int(w["gcu"][3])] = -1                      # of the request without new tokens: nothing is read through it
     check(w)
@@ -346,7 +346,7 @@ def test_captured_steps():
 
 def test_streams_and_repeats():
     """Calls on two streams with a workspace each, over and over: the same bits."""
-    ws = [make([(3200, [(1, 9 * i) for i in range(20)])], 8, lay, seed=22) for lay in ("raw512", "fp4_416")]
+    ws = [make([(5504, [(1, 9 * i) for i in range(20)])], 8, lay, seed=22) for lay in ("raw512", "fp4_416")]
     want = [check(w, only=[0, 7, 19]) for w in ws]
     streams = [torch.cuda.Stream() for _ in ws]
     dev, outs = [], []
@@ -369,7 +369,7 @@ def test_streams_and_repeats():
 @pytest.mark.parametrize("layout", ["raw512", "rope656", "fp4_416"])
 def test_wait_that_runs_out(layout):
     """A limit of zero: the call returns, reports the timeout, leaves rows of no request alone, and the next is right."""
-    w = make([(3200, [(1, 9 * i) for i in range(20)])], 8, layout, seed=23, lead=2, tail=3)
+    w = make([(5504, [(1, 9 * i) for i in range(20)])], 8, layout, seed=23, lead=2, tail=3)
     old = binding.dsa_set_wait_limit_ns(0)
     try:
         o, lse, err = run(w)
