@@ -42,13 +42,12 @@ bool table_ok(int B, int max_pages, int page_size) {
 // lead to, so that it serves every smaller call too.
 // shared: with room for requests that share prefixes (a.G may still be 0).
 size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool shared, char* base) {
-  // shared prefixes pack rows of several requests: 16 rows only where there are no more
-  w.nc = dsa::chunk_columns(T, H, w.a.G > 0 ? 1 : B);
+  w.nc = w.a.G > 0 ? 32 : dsa::chunk_columns(T, H, B);     // shared prefixes: rows of several requests together
   const int64_t all = (int64_t)T * H;
   w.max_units = (all / w.nc) * (w.a.G > 0 ? 2 : 1) + B + w.a.G;     // full units, and the last of each request and group
   w.grid = sms;
   const size_t units = (size_t)((all / dsa::kFewestRows + B) * (shared ? 2 : 1));
-  w.joined0 = (int64_t)sms * 2 * dsa::chunk_columns(T, H, 1);
+  w.joined0 = (int64_t)sms * 2 * (shared ? 32 : dsa::chunk_columns(T, H, 1));
   const size_t rows = (size_t)(w.joined0 + (shared ? 2 * std::min(all, (int64_t)B * dsa::kSharedRows) : 0));
   size_t end = 0;
   auto take = [&](size_t bytes) {
@@ -56,7 +55,7 @@ size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool share
     end += (bytes + 255) / 256 * 256;
     return p;
   };
-  w.units = reinterpret_cast<dsa::ChunkUnit*>(take((units + 1) * sizeof(dsa::ChunkUnit)));
+  w.units = take((units + 1) * (shared ? sizeof(dsa::SharedUnit) : sizeof(dsa::ChunkUnit)));
   w.splits = reinterpret_cast<dsa::ChunkSplit*>(take((size_t)sms * sizeof(dsa::ChunkSplit)));
   w.part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
   w.part_o = reinterpret_cast<float*>(take(rows * 512 * sizeof(float)));
@@ -129,7 +128,8 @@ int attend(const dsa::ChunkArgs& a, int kv_row_dim, bool shared, void* workspace
   lay_out_chunk(w, a.T, a.H, a.B, sms, shared, static_cast<char*>(workspace));
   w.wait_ns = dsa::wait_limit_ns();
   cudaGetLastError();
-  return launch_status(dsa::launch_chunk_attn(w, static_cast<cudaStream_t>(stream)));
+  const auto launch = w.a.G > 0 ? dsa::launch_prefix_attn : dsa::launch_chunk_attn;
+  return launch_status(launch(w, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

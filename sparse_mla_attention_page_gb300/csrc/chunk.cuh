@@ -41,16 +41,31 @@ struct __align__(16) ChunkUnit {
   int32_t tiles;     // at least 1
   int32_t kv;        // the request's keys
   int32_t last;      // keys that the unit's last row sees
+  int32_t pad;
+};
+enum ChunkSide { kAlone = 0, kPrefix = 1, kOwn = 2 };   // all of a row's keys; those it shares; the others
+struct __align__(16) SharedUnit : ChunkUnit {
   int32_t key0;      // the request's key that the unit's first one is
   int32_t mate;      // of a kOwn unit: the unit that holds its first row's part over the prefix,
-  int16_t slot0;     // parts > 0: spread over CTAs, its parts in the slots slot0, then as of ChunkSplit
-  int16_t parts;
   uint8_t side;      // ChunkSide
   uint8_t mate_col;  // and that row's column there
-  int16_t pad[3];
+  int16_t pad2;
+  int16_t slot0;     // parts > 0: spread over CTAs, its parts in the slots slot0, then as of ChunkSplit
+  int16_t parts;
 };
-static_assert(sizeof(ChunkUnit) == 64, "sixteen words");
-enum ChunkSide { kAlone = 0, kPrefix = 1, kOwn = 2 };   // all of a row's keys; those it shares; the others
+static_assert(sizeof(ChunkUnit) == 48 && sizeof(SharedUnit) == 64, "whole 16-byte words");
+// The kernels with groups of requests (kShared) are built apart from those
+// without: these ran up to 6 % slower with the other's code in them.
+template <bool kShared>
+struct UnitOf {
+  using type = ChunkUnit;
+};
+template <>
+struct UnitOf<true> {
+  using type = SharedUnit;
+};
+template <bool kShared>
+using Unit = typename UnitOf<kShared>::type;
 
 // A unit spread over CTAs c0 ..: its parts lie in the slots slot0, 2 (c0 + 1), 2 (c0 + 2), ...
 struct __align__(16) ChunkSplit {
@@ -72,7 +87,7 @@ struct ChunkWork {
   int box_shift;           // log2 of the rows of a TMA box; 0: rows are copied one by one
   int unit_cost;
   uint64_t wait_ns;
-  ChunkUnit* units;        // [max_units + 1]; those that begin inside a CTA's range
+  void* units;             // Unit<kShared>[max_units + 1]; those that begin inside a CTA's range
   ChunkSplit* splits;      // [grid] by the CTA in which the unit begins
   float* part_lse;         // [2 grid][nc]
   float* part_o;           // [2 grid][nc][512] normalised
@@ -96,9 +111,18 @@ inline bool sharing_possible(const ChunkArgs& a, int ctas) {
          (int64_t)(a.B - 1) * ((int64_t)a.max_pages * a.page_size / kChunkTile) * kTileCost >= (int64_t)ctas * kJoinCost;
 }
 
+template <bool kShared>
+__device__ __forceinline__ Unit<kShared>* units_of(const ChunkWork& w) {
+  return static_cast<Unit<kShared>*>(w.units);
+}
+
 // Keys that row r of a unit's request sees.
-__device__ __forceinline__ int chunk_visible(const ChunkArgs& a, const ChunkUnit& u, int col) {
-  if (!a.causal || u.side == kPrefix) return u.kv;
+template <class U>
+__device__ __forceinline__ int chunk_visible(const ChunkArgs& a, const U& u, int col) {
+  if (!a.causal) return u.kv;
+  if constexpr (sizeof(U) == sizeof(SharedUnit)) {
+    if (u.side == kPrefix) return u.kv;
+  }
   const int64_t v = (int64_t)u.vis0 + (u.r0 + col) / a.H;
   return v < 0 ? 0 : v > u.kv ? u.kv : (int)v;
 }

@@ -203,15 +203,16 @@ struct Join {
 struct JoinUnit {
   int64_t row0;
   int cols;
-  int4 last;      // mate; slot0 and parts; side and mate_col
-  __device__ __forceinline__ void fetch(const ChunkUnit* u) {
+  int4 last;      // key0; mate; side and mate_col; slot0 and parts
+  __device__ __forceinline__ void fetch(const SharedUnit* u) {
     row0 = __ldcg(reinterpret_cast<const long long*>(&u->row0));
     cols = __ldcg(&u->cols);
-    last = __ldcg(reinterpret_cast<const int4*>(&u->mate));
+    last = __ldcg(reinterpret_cast<const int4*>(&u->key0));
   }
 };
-static_assert(offsetof(ChunkUnit, mate) == 48 && offsetof(ChunkUnit, slot0) == 52 && offsetof(ChunkUnit, parts) == 54 &&
-              offsetof(ChunkUnit, side) == 56 && offsetof(ChunkUnit, mate_col) == 57, "entry");
+static_assert(offsetof(SharedUnit, key0) == 48 && offsetof(SharedUnit, mate) == 52 && offsetof(SharedUnit, side) == 56 &&
+              offsetof(SharedUnit, mate_col) == 57 && offsetof(SharedUnit, slot0) == 60 && offsetof(SharedUnit, parts) == 62,
+              "entry");
 
 // parts_of(m): the word of unit m that holds its slot0 and parts.
 template <class PartsOf>
@@ -219,14 +220,14 @@ __device__ __forceinline__ Join join_of(const ChunkWork& w, const JoinUnit& u, i
   Join j{};
   j.row0 = u.row0;
   j.cols = j.brk = u.cols;
-  j.own_slot = (int16_t)u.last.y;
-  j.own_parts = (int16_t)(u.last.y >> 16);
+  j.own_slot = (int16_t)u.last.w;
+  j.own_parts = (int16_t)(u.last.w >> 16);
   j.parts[0] = -1;
   if ((u.last.z & 0xFF) == kAlone) {
     j.kind = j.own_parts == 0 ? 0 : j.own_parts <= kLoopParts ? 1 : 2;
     return j;
   }
-  const int m0 = parts_of(u.last.x), m1 = parts_of(min(u.last.x + 1, n_units - 1));
+  const int m0 = parts_of(u.last.y), m1 = parts_of(min(u.last.y + 1, n_units - 1));
   j.col0 = u.last.z >> 8 & 0xFF;
   j.brk = min(j.cols, w.nc - j.col0);
   j.slot[0] = (int16_t)m0;
@@ -311,10 +312,11 @@ __global__ void __launch_bounds__(kMergeThreads, 3) prefix_merge_kernel(const __
   __shared__ Join joins[kMergeThreads];
   __shared__ int near[kMergeThreads];              // slot0 and parts of the first units
   const int tid = threadIdx.x, blocks = gridDim.x;
+  const SharedUnit* units = units_of<true>(w);
   JoinUnit u{};
-  if (tid < w.max_units) u.fetch(w.units + tid);                   // (while the counts are on their way)
+  if (tid < w.max_units) u.fetch(units + tid);                    // (while the counts are on their way)
   const int n_units = __ldcg(w.n_units), n = __ldcg(w.n_units + 1);
-  near[tid] = u.last.y;
+  near[tid] = u.last.w;
   const bool all = n <= kJoinAll;
   const int run = all ? kMergeThreads : kJoinRun;
   const int pairs = w.nc / kFewRows;
@@ -323,9 +325,9 @@ __global__ void __launch_bounds__(kMergeThreads, 3) prefix_merge_kernel(const __
     __syncthreads();                               // the entries before are done with
     bool many = false;
     if (tid < here) {
-      if (u0 > 0) u.fetch(w.units + u0 + tid);
+      if (u0 > 0) u.fetch(units + u0 + tid);
       const Join j = join_of(w, u, n_units, [&](int m) {
-        return m < kMergeThreads ? near[m] : __ldcg(reinterpret_cast<const int*>(&w.units[m].slot0));
+        return m < kMergeThreads ? near[m] : __ldcg(reinterpret_cast<const int*>(&units[m].slot0));
       });
       many = j.kind == 2;
       joins[tid] = j;

@@ -40,7 +40,7 @@ __device__ __forceinline__ Request request_of(const ChunkArgs& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ int units_of(const ChunkArgs& a, int n, int nc) { return (int)(((int64_t)n * a.H + nc - 1) / nc); }
+__device__ __forceinline__ int unit_count(const ChunkArgs& a, int n, int nc) { return (int)(((int64_t)n * a.H + nc - 1) / nc); }
 
 // Keys that the first new token of a request sees.
 __device__ __forceinline__ int first_visible(const ChunkArgs& a, const Request& r) { return a.causal ? r.kv - r.n + 1 : r.kv; }
@@ -54,8 +54,9 @@ struct Part {
 };
 
 // Entry of the i-th unit of a part (tile0 is filled in later).
-__device__ __forceinline__ ChunkUnit unit_of(const ChunkArgs& a, const Part& r, int i, int nc) {
-  ChunkUnit u{};
+template <bool kShared>
+__device__ __forceinline__ Unit<kShared> unit_of(const ChunkArgs& a, const Part& r, int i, int nc) {
+  Unit<kShared> u{};
   const int64_t rows = (int64_t)r.n * a.H, r0 = (int64_t)i * nc;
   u.row0 = (int64_t)r.t0 * a.H + r0;
   u.b = r.b;
@@ -63,12 +64,14 @@ __device__ __forceinline__ ChunkUnit unit_of(const ChunkArgs& a, const Part& r, 
   u.r0 = (int)r0;
   u.vis0 = r.vis0;
   u.kv = r.kv;
-  u.key0 = r.key0;
-  u.side = (uint8_t)r.side;
-  if (r.side == kOwn) {
-    const int64_t at = u.row0 - r.group_row0;
-    u.mate = r.group_unit + (int)(at / nc);
-    u.mate_col = (uint8_t)(at % nc);
+  if constexpr (kShared) {
+    u.key0 = r.key0;
+    u.side = (uint8_t)r.side;
+    if (r.side == kOwn) {
+      const int64_t at = u.row0 - r.group_row0;
+      u.mate = r.group_unit + (int)(at / nc);
+      u.mate_col = (uint8_t)(at % nc);
+    }
   }
   u.last = chunk_visible(a, u, u.cols - 1);
   u.tiles = u.last <= kChunkTile ? 1 : (u.last - 1) / kChunkTile + 1;
@@ -117,7 +120,7 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
       if (r.n <= 0) continue;
       atomicMin(g.keys + i, max(first_visible(a, r), 0));
       atomicMin(g.first + i, b);
-      atomicAdd(g.units + i, units_of(a, r.n, w.nc));
+      atomicAdd(g.units + i, unit_count(a, r.n, w.nc));
     }
     __syncthreads();
   }
@@ -128,7 +131,7 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
     if (tiles > 0) {
       const int n = __ldg(a.cu_q + cu[i + 1]) - __ldg(a.cu_q + cu[i]);
       const int64_t apart = (int64_t)g.units[i] * tiles * kTileCost;
-      const int64_t packed = (int64_t)units_of(a, n, w.nc) * (tiles * kTileCost + w.unit_cost);
+      const int64_t packed = (int64_t)unit_count(a, n, w.nc) * (tiles * kTileCost + w.unit_cost);
       if (packed < apart) {
         keys = tiles * kChunkTile;
         saved += apart - packed;
@@ -160,24 +163,25 @@ constexpr int kWholeTiles = 2;
 
 // Bytes of shared memory: 32-bit words of the requests, or of the requests and
 // five of each group, and the scans' sums.
-constexpr int kPlanWords = DSA_MAX_REQUESTS > 6 * DSA_MAX_PREFIX_REQUESTS + 1 ? DSA_MAX_REQUESTS : 6 * DSA_MAX_PREFIX_REQUESTS + 1;
-constexpr int kPlanScratch = (kPlanWords * 4 + 7) / 8 * 8 + 256;
+constexpr int plan_words(bool shared) { return shared ? 6 * DSA_MAX_PREFIX_REQUESTS + 2 : DSA_MAX_REQUESTS; }
+constexpr int plan_scratch(bool shared) { return plan_words(shared) * 4 + 256; }
 
 // By all THREADS threads; mine and start (the range's first unit) lie in
 // shared memory and hold after the caller's next barrier.
-template <int THREADS>
-__device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch, ChunkRange& mine, ChunkUnit& start) {
-  int64_t* sums = reinterpret_cast<int64_t*>(scratch + kPlanScratch - 256);
+template <int THREADS, bool kShared>
+__device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch, ChunkRange& mine, Unit<kShared>& start) {
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch + plan_words(kShared) * 4);
   int32_t* first_unit = reinterpret_cast<int32_t*>(scratch);                             // [N]
   const ChunkArgs& a = w.a;
   const int tid = threadIdx.x, cta = blockIdx.x;
-  const int N = a.B + a.G;         // parts: the requests, then the groups' prefixes
+  Unit<kShared>* units = units_of<kShared>(w);
+  const int N = kShared ? a.B + a.G : a.B;         // parts: the requests, then the groups' prefixes
   Groups groups{};
-  if (a.G > 0) groups = find_groups<THREADS>(w, first_unit + N, sums);
+  if constexpr (kShared) groups = find_groups<THREADS>(w, first_unit + N, sums);
   int err = 0;
   auto part = [&](int p) -> Part {
     Part x{};
-    if (p >= a.B) {
+    if (kShared && p >= a.B) {
       const int g = p - a.B;
       x.side = kPrefix;
       x.kv = x.vis0 = groups.keys[g];
@@ -195,7 +199,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
     x.b = p;
     x.kv = r.kv;
     x.vis0 = first_visible(a, r);
-    if (a.G > 0 && r.n > 0 && p >= groups.cu[0] && p < groups.cu[a.G]) {
+    if (kShared && r.n > 0 && p >= groups.cu[0] && p < groups.cu[a.G]) {
       const int g = scan_owner(groups.cu, a.G, p);
       if (groups.keys[g] > 0) {
         x.side = kOwn;
@@ -213,7 +217,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   int64_t here = 0;
   int last_units = 0;
   for (int b = b0; b < b1; ++b) {
-    last_units = units_of(a, part(b).n, w.nc);
+    last_units = unit_count(a, part(b).n, w.nc);
     here += last_units;
   }
   int64_t total;
@@ -226,10 +230,10 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   const int n_units = (int)total;
   for (int b = b0; b < b1; ++b) {
     first_unit[b] = (int)min(at, (int64_t)INT32_MAX);
-    at += b + 1 == b1 ? last_units : units_of(a, part(b).n, w.nc);
+    at += b + 1 == b1 ? last_units : unit_count(a, part(b).n, w.nc);
   }
   __syncthreads();
-  if (a.G > 0 && cta == 0 && tid == 0) {
+  if (kShared && cta == 0 && tid == 0) {
     w.n_units[0] = n_units;
     w.n_units[1] = min(first_unit[a.B], n_units);
   }
@@ -239,7 +243,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   const int u0 = (int)min((int64_t)tid * uper, (int64_t)n_units), u1 = min(u0 + uper, n_units);
   const int first_b = u0 < u1 ? scan_owner(first_unit, N, u0) : 0;
   int64_t tiles = 0;
-  ChunkUnit only{};              // of a thread that has one unit: worked out once
+  Unit<kShared> only{};          // of a thread that has one unit: worked out once
   auto walk = [&](auto&& visit) {
     if (u1 - u0 == 1 && tiles > 0) return visit(u0, only);
     int b = first_b;
@@ -252,10 +256,10 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
       }
       if (!have) r = part(b);
       have = true;
-      visit(u, unit_of(a, r, u - first_unit[b], w.nc));
+      visit(u, unit_of<kShared>(a, r, u - first_unit[b], w.nc));
     }
   };
-  walk([&](int, const ChunkUnit& e) {
+  walk([&](int, const Unit<kShared>& e) {
     tiles += e.tiles;
     only = e;
   });
@@ -265,13 +269,13 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
     const int fair = (int)((n_tiles + w.grid - 1) / w.grid);       // tiles of a CTA where units are split
     if (!__syncthreads_or(u1 > u0 && only.tiles > fair + kWholeTiles)) {
       if (tid == 0) {
-        w.splits[cta].parts = 0;
+        if (!kShared) w.splits[cta].parts = 0;
         if (cta >= n_units) mine.t0 = mine.t1 = 0;
       }
       if (u1 > u0 && u0 == cta) {
         start = only;
         start.tile0 = tile0;
-        w.units[u0] = start;
+        if constexpr (kShared) units[u0] = start;
         mine.unit = u0;
         mine.t0 = tile0;
         mine.t1 = tile0 + only.tiles;
@@ -287,17 +291,19 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   if (tid == 0) {
     if (idle) mine.t0 = mine.t1 = 0;
     else if (ends) mine.t1 = n_tiles;
-    if (ends) w.splits[cta].parts = 0;
+    if (!kShared && ends) w.splits[cta].parts = 0;
   }
   if (idle) return;
   const int64_t va = cta * V / grid, vb = (cta + 1) * V / grid;
   int64_t v0 = tile0 * kTileCost + (int64_t)u0 * w.unit_cost;
-  walk([&](int u, ChunkUnit e) {
+  walk([&](int u, Unit<kShared> e) {
     e.tile0 = tile0;
     const int64_t body = v0 + w.unit_cost, end = body + (int64_t)e.tiles * kTileCost;
     auto tile_at = [&](int64_t v) { return v < body ? 0 : (v - body) / kTileCost; };
-    // the unit's first tile lies in this range (a border may lie in front of it, in the unit's own cost)
-    const bool begins = v0 < vb && va < end && tile_at(va) == 0 && (ends || vb >= end || tile_at(vb) > 0);
+    // with shared prefixes: the unit's first tile lies in this range (a border may lie in front of it, in the
+    // unit's own cost), so that each entry is written once, with its parts
+    const bool begins = kShared && v0 < vb && va < end && tile_at(va) == 0 && (ends || vb >= end || tile_at(vb) > 0);
+    if (!kShared && v0 > va && v0 < vb) units[u] = e;
     if (va >= v0 && va < end) {
       start = e;
       mine.unit = u;
@@ -309,18 +315,23 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
       // in CTAs cta .. ceil(end grid / V) - 1: in slot 0 of a CTA whose range
       // starts with the unit, in slot 1 where another one is in front.
       ChunkSplit sp{};
-      if (begins) {
+      if (tile_at(vb) > 0 && tile_at(va) == 0) {
         sp.row0 = e.row0;
         sp.cols = e.cols;
         sp.parts = (int)min((end * grid + V - 1) / V, (int64_t)grid) - cta;
         sp.slot0 = 2 * cta + (va < v0 ? 1 : 0);
         sp.next = 2 * (cta + 1);
+      }
+      if constexpr (kShared) {
         e.slot0 = (int16_t)sp.slot0;
         e.parts = (int16_t)sp.parts;
+      } else {
+        w.splits[cta] = sp;
       }
-      w.splits[cta] = sp;
     }
-    if (begins) w.units[u] = e;
+    if constexpr (kShared) {
+      if (begins) units[u] = e;
+    }
     tile0 += e.tiles;
     v0 = end;
   });

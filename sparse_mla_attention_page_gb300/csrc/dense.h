@@ -95,6 +95,7 @@ constexpr int kFewestRows = 16;
 int chunk_columns(int T, int H, int B);
 struct ChunkWork;      // chunk.cuh
 bool launch_chunk_attn(const ChunkWork& w, cudaStream_t stream);
+bool launch_prefix_attn(const ChunkWork& w, cudaStream_t stream);     // w.a.G > 0
 
 // Limit of every bounded wait inside the attention kernels (dsa_set_wait_limit_ns).
 uint64_t wait_limit_ns();
