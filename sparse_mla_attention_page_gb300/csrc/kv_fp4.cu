@@ -26,23 +26,64 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t v, int lanes) {
   return v;
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// v / s, rounded as IEEE division does: a quotient within an ulp, then its
+// remainder, which an FMA gives exactly, times the rounded reciprocal of s
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990; two steps, as the first product may be off by more).  Exact
+// where remainders do not underflow: s at least 2^-80 (a smaller quotient than
+// 2^-7 has code 0 however it is rounded), its reciprocal a normal number.  Five
+// packed operations for two quotients; dividing each took a third of the kernel.
+__device__ __forceinline__ void divide8(float* v, float s) {
+  const float r1 = __frcp_rn(s);
+  const uint64_t r = pack2(r1, r1), n = pack2(-s, -s);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const uint64_t x = pack2(v[k], v[k + 1]);
+    uint64_t q = fma2(x, r, 0ull);
+    q = fma2(fma2(n, q, x), r, q);
+    q = fma2(fma2(n, q, x), r, q);
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
+    v[k] = copysignf(a, v[k]);         // (a zero keeps its sign)
+    v[k + 1] = copysignf(b, v[k + 1]);
+  }
+}
+
 // Eight dims of this lane (one of a block's two and a group's sixteen): their
 // word, the block's exponent nibble and the group's scale.
 __device__ __forceinline__ void quantise8(float* v, uint32_t& word, uint32_t& e, float& s) {
   uint32_t top = 0;                    // as bits: a NaN is the largest
 #pragma unroll
   for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-  const uint32_t block = max_bits(top, 2), group = max_bits(block, 16);
+  const uint32_t group = max_bits(top, 16);
   const bool odd = group >= 0x7F800000u;
   s = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(__uint_as_float(group), kFp4Top);
-  const bool none = odd || s == 0.f;
-  const float y = none ? 0.f : __fdiv_rn(__uint_as_float(block), s);
-  e = 0;
+  if (__all_sync(0xffffffffu, s >= 0x1p-80f && s <= 0x1p100f)) {
+    divide8(v, s);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 11; ++k) e += y > 0.21875f * (float)(1 << k);      // 7 2^-5, 7 2^-4, ..
+    for (int k = 0; k < 8; ++k) v[k] = odd || s == 0.f ? copysignf(0.f, v[k]) : __fdiv_rn(v[k], s);
+  }
+  float y = 0.f;                       // the block's largest quotient
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y = fmaxf(y, fabsf(v[k]));
+  y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+  // y <= 1.75 2^(e - 3): its exponent, one more where its mantissa is above 1.75
+  e = (uint32_t)min(max((int)((__float_as_uint(y) + 0x1FFFFFu) >> 23) - 124, 0), 11);
   const float up = __uint_as_float((127u + 5u - e) << 23);               // 2^(5 - e)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = none ? copysignf(0.f, v[k]) : __fdiv_rn(v[k], s) * up;
+  for (int k = 0; k < 8; ++k) v[k] *= up;
   word = fp4_word(v);
 }
 

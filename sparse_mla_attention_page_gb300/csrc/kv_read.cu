@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kInFlight = 4;
 constexpr int kNearCu = 2048;        // offsets kept in shared memory; more are searched where they are
-constexpr int kBlocks = 6;           // resident on an SM
+constexpr int kBlocks = 4;           // resident on an SM: more of them spill, and are slower
 
 template <int kLayout>
 struct Format {
