@@ -98,6 +98,8 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
   int32_t* cu = scratch;
   const Groups g{cu, cu + G + 1, cu + 2 * G + 1, cu + 3 * G + 1};
   bool bad = false;
+  Request r{};
+  if (tid < a.B) r = request_of(a, tid);         // (on its way beside the groups)
   for (int i = tid; i <= G; i += THREADS) {
     const int x = __ldg(a.group_cu + i);
     bad |= x < 0 || x > a.B || (i < G && (x > __ldg(a.group_cu + i + 1) || __ldg(a.prefix_lens + i) < 0));
@@ -113,9 +115,10 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
     for (int i = tid; i <= G; i += THREADS) cu[i] = 0;      // nobody belongs to a group
     __syncthreads();
   } else {
-    for (int b = cu[0] + tid; b < cu[G]; b += THREADS) {
+    for (int b = tid; b < cu[G]; b += THREADS) {
+      if (b != tid) r = request_of(a, b);
+      if (b < cu[0]) continue;
       const int i = scan_owner(cu, G, b);
-      const Request r = request_of(a, b);
       if (r.err) atomicMin(g.keys + i, 0);
       if (r.n <= 0) continue;
       atomicMin(g.keys + i, max(first_visible(a, r), 0));
