@@ -503,7 +503,8 @@ int dsa_rope_qkv656(const dsa_rope* rope, const int32_t* positions_dev, int64_t 
 /* Workspace bytes of dsa_chunk_attn for T query tokens of B requests with H
  * heads on the current device: the work list and the partial results of
  * query groups that are spread over several SMs (20 MB on 152 SMs, and 3 bytes
- * a query row).  Enough for every call with no more tokens, heads and requests.
+ * a query row); for 4-bit rows, from 8192 query rows on, 87 MB more, into which
+ * chunks of prompts expand their requests' rows.  Enough for every call with no more tokens, heads and requests.
  * 0 for a size out of range. */
 size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
 
@@ -545,7 +546,9 @@ size_t dsa_chunk_attn_workspace_bytes(int T, int H, int B, int layout);
  * A row with an infinite or NaN scale, or a query with a NaN or an infinity,
  * scores NaN: the results that see it are NaN, no others.  Equal calls give
  * equal bits.
- *   q_bf16_dev      [T, H, 512] BF16, [T, H, 576] over 656-byte rows; 16-byte aligned.
+ *   layout          any of the five; 4-bit rows are attended as the 8-bit rows of
+ *                   the same values.
+ *   q_bf16_dev      [T, H, 512] BF16, [T, H, 576] over 656- and 416-byte rows; 16-byte aligned.
  *   H               1 to 1024; T * H < 2^30.
  *   page_table_dev  [B, max_pages] int32.
  *   cu_q_dev        [B + 1] int32;  kv_lens_dev [B] int32; B <= DSA_MAX_REQUESTS.

@@ -40,8 +40,9 @@ bool table_ok(int B, int max_pages, int page_size) {
 // Where the parts of the attention's workspace begin (pointers from base on).
 // Its size grows with T, H and B alone, not with the rows of a unit that they
 // lead to, so that it serves every smaller call too.
-// shared: with room for requests that share prefixes (a.G may still be 0).
-size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool shared, char* base) {
+// shared: with room for requests that share prefixes (a.G may still be 0).  flat:
+// of 4-bit rows, with room for expanded ones where a call is large enough for it.
+size_t lay_out_chunk(dsa::ChunkWork& w, dsa::FlatWork* flat, int T, int H, int B, int sms, bool shared, char* base) {
   w.nc = w.a.G > 0 ? 32 : dsa::chunk_columns(T, H, B);     // shared prefixes: rows of several requests together
   const int64_t all = (int64_t)T * H;
   w.max_units = (all / w.nc) * (w.a.G > 0 ? 2 : 1) + B + w.a.G;     // full units, and the last of each request and group
@@ -60,6 +61,15 @@ size_t lay_out_chunk(dsa::ChunkWork& w, int T, int H, int B, int sms, bool share
   w.part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
   w.part_o = reinterpret_cast<float*>(take(rows * 512 * sizeof(float)));
   if (shared) w.n_units = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+  if (flat != nullptr && all >= dsa::kFlatCall) {
+    const size_t requests = (size_t)std::min(B, dsa::kFlatRequests);
+    flat->rows = reinterpret_cast<uint8_t*>(take((size_t)dsa::kFlatTiles * 128 * 656));
+    flat->table = reinterpret_cast<int32_t*>(take((size_t)dsa::kFlatTable * sizeof(int32_t)));
+    flat->cu8 = reinterpret_cast<int32_t*>(take((requests + 1) * sizeof(int32_t)));
+    flat->kv8 = reinterpret_cast<int32_t*>(take(requests * sizeof(int32_t)));
+    flat->cu4 = reinterpret_cast<int32_t*>(take((requests + 1) * sizeof(int32_t)));
+    flat->kv4 = reinterpret_cast<int32_t*>(take(requests * sizeof(int32_t)));
+  }
   return end;
 }
 
@@ -95,12 +105,15 @@ bool chunk_sizes_ok(int T, int H, int B) {
   return T >= 0 && H >= 1 && H <= 1024 && (int64_t)T * H <= INT32_MAX / 2 && B >= 1 && B <= DSA_MAX_REQUESTS;
 }
 
+bool fp4(int layout) { return layout == DSA_KV_FP4_288 || layout == DSA_KV_FP4_416; }
+
 size_t chunk_bytes(int T, int H, int B, int layout, bool shared) {
   if (!chunk_sizes_ok(T, H, B) || dsa_kv_row_bytes(layout) == 0) return 0;
   int sms = 0;
   if (dsa::current_device_sms(&sms) != DSA_OK) sms = 152;
   dsa::ChunkWork w{};
-  return lay_out_chunk(w, T, H, B, sms, shared, nullptr);
+  dsa::FlatWork flat{};
+  return lay_out_chunk(w, fp4(layout) ? &flat : nullptr, T, H, B, sms, shared, nullptr);
 }
 
 // Dense attention, checked and launched; shared: of dsa_prefix_attn.
@@ -125,9 +138,31 @@ int attend(const dsa::ChunkArgs& a, int kv_row_dim, bool shared, void* workspace
   dsa::ChunkWork w{};
   w.a = a;
   if (!dsa::sharing_possible(a, sms)) w.a.G = 0;
-  lay_out_chunk(w, a.T, a.H, a.B, sms, shared, static_cast<char*>(workspace));
+  dsa::FlatWork flat{};
+  lay_out_chunk(w, fp4(a.layout) ? &flat : nullptr, a.T, a.H, a.B, sms, shared, static_cast<char*>(workspace));
   w.wait_ns = dsa::wait_limit_ns();
   cudaGetLastError();
+  const int64_t tiles = ((int64_t)a.max_pages * a.page_size + 127) / 128;       // of a page-table row
+  // (pages of fewer rows: every block of the expansion looks at all of them)
+  if (flat.rows != nullptr && w.a.G == 0 && (int64_t)a.T * a.H >= (int64_t)a.B * dsa::kFlatRows && a.B <= dsa::kFlatRequests &&
+      a.B * tiles <= dsa::kFlatTable && a.page_size >= 16) {
+    flat.a = a;
+    flat.tiles = dsa::kFlatTiles;
+    flat.width = (int)tiles;
+    dsa::ChunkWork w8 = w;
+    w8.a.layout = a.layout == DSA_KV_FP4_416 ? DSA_KV_ROPE656 : DSA_KV_SCALED528;
+    w8.a.pool = flat.rows;
+    w8.a.pool_rows = dsa::kFlatTiles * 128;
+    w8.a.page_table = flat.table;
+    w8.a.max_pages = (int)tiles;
+    w8.a.page_size = 128;
+    w8.a.cu_q = flat.cu8;
+    w8.a.kv_lens = flat.kv8;
+    w.a.cu_q = flat.cu4;
+    w.a.kv_lens = flat.kv4;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launch_status(dsa::launch_fp4_flat(flat, sms, s) && dsa::launch_chunk_attn(w8, s) && dsa::launch_chunk_attn(w, s));
+  }
   const auto launch = w.a.G > 0 ? dsa::launch_prefix_attn : dsa::launch_chunk_attn;
   return launch_status(launch(w, static_cast<cudaStream_t>(stream)));
 }

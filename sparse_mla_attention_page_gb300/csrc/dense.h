@@ -90,6 +90,26 @@ struct ChunkArgs {
   const int32_t* prefix_lens;   // [G]
   int G;
 };
+// Chunks over 4-bit rows: their requests' rows as 8-bit rows in the workspace (fp4_flat.cu).
+struct FlatWork {
+  ChunkArgs a;            // of the call
+  uint8_t* rows;          // [tiles * 128] rows of 528 or 656 bytes
+  int tiles;
+  int32_t* table;         // [B, width] pages of 128 rows
+  int width;
+  int32_t *cu8, *kv8;     // the requests that attend over those rows: all, or none where they do not fit
+  int32_t *cu4, *kv4;     // the others, over the 4-bit rows
+};
+constexpr int kFlatTiles = 1024;          // 131072 rows, 86 MB
+constexpr int kFlatTable = 1 << 18;       // entries
+constexpr int kFlatRequests = 1024;
+// Query rows of a call, and of a request on average, from which it is worth three
+// launches more.  us with / without (32 heads: 416-byte rows): 2048 tokens over 8192
+// 2165 / 3465, 256 over 8192 287 / 425; 16 heads: 64 over 8192 66 / 72, 32 over 8192
+// 64 / 62, prompts of 512 50 / 47, of 4 x up to 1000 117 / 137.
+constexpr int kFlatCall = 8192, kFlatRows = 1024;
+bool launch_fp4_flat(const FlatWork& f, int sms, cudaStream_t stream);
+
 // Query rows of a unit of the work list, 16 or 32.
 constexpr int kFewestRows = 16;
 int chunk_columns(int T, int H, int B);

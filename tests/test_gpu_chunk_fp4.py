@@ -109,6 +109,56 @@ def test_long_context_and_many_units(layout):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
+def test_chunks_over_expanded_rows(layout):
+    """Calls of 8192 query rows and 1024 a request, whose rows are expanded once: ragged requests, one without new tokens
+    and one without rows, pages of 16 to 256, not causal; what does not fit (smaller pages, bad pages and lengths, too
+    many rows) takes the general form, with the same results."""
+    new, ctx = [70, 0, 130, 64, 200, 120], [500, 9, 0, 129, 1000, 3]
+    for page in (16, 48, 256, 3):
+        check(make(new, ctx, 16, layout, page=page, seed=page, lead=2, tail=3), exact=page == 48)
+    w = make([600], [1], 16, layout, seed=41)
+    w["causal"] = False
+    check(w)
+    w = make([520, 8], [40, 3], 16, layout, seed=42)
+    w["kv"][1] = 0                                         # tokens that see no key
+    check(w, exact=False)
+    w = make([600, 30], [40, 300], 16, layout, page=16, seed=43)
+    w["table"][1, 5], w["table"][0, 7] = -3, 1 << 22
+    check(w, err_want=binding.DSA_DEV_ERR_PAGE_RANGE, exact=False)
+    w = make([300, 300], [40, 300], 16, layout, page=16, seed=44)
+    w["kv"][1] = 10 ** 6
+    o, lse, err = run(w, w["pool"], layout)
+    assert err & binding.DSA_DEV_ERR_LENGTH
+    o8, lse8, err8 = run(w, fp4_ref.expand(w["pool"].numpy()), WIDE[layout])
+    assert err == err8 and same(o, o8) and same(lse, lse8)
+    w = make([70, 70, 70], [100, 70, 90], 48, layout, page=64, seed=45)       # three pages each
+    w["table"] = w["table"][:, :3].repeat(1, 500)[:, :1100]      # 70000 keys a request, over the same pages again and again
+    w["kv"][:] = 70000
+    check(w, exact=False)
+
+
+def test_captured_chunk_over_expanded_rows():
+    """A captured chunk serves shorter ones, and lengths that do not fit."""
+    w = make([600], [700], 16, "fp4_416", seed=46)
+    d = {k: v.cuda() for k, v in w.items() if isinstance(v, torch.Tensor)}
+    o, lse = torch.zeros(600, 16, 512, dtype=BF, device="cuda"), torch.zeros(600, 16, device="cuda")
+    ws = binding.chunk_workspace_for(600, 16, 1, "fp4_416")
+    step = (lambda: binding.dsa_chunk_attn(d["q"], d["pool"], "fp4_416", d["table"], 64, d["cu"], d["kv"], SCALE, o, lse, ws))
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for kv in (1300, 5, 640, 0, 1300):
+        d["kv"].fill_(kv)
+        w["kv"][:] = kv
+        o.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        o8, lse8, _ = run(w, fp4_ref.expand(w["pool"].numpy()), "rope656")
+        assert same(o.cpu(), o8) and same(lse.cpu(), lse8)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
 def test_not_causal_and_amplitudes(layout):
     w = make([5, 130, 1], [60, 3, 300], 8, layout, seed=6)
     w["causal"] = False
