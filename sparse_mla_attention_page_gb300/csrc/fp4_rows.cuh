@@ -46,9 +46,9 @@ __device__ __forceinline__ void fp4_expand8(uint32_t w, const Fp4Lut& t, uint32_
   b = prmt(t.lo, t.hi, m >> 16) | ((w << 4) & 0x80808080u);
 }
 
-// The word of eight values (times a power of two), rounded to nearest, ties to
-// even, at most 6 in magnitude; the sign of a value that rounds to zero is kept.
-__device__ __forceinline__ uint32_t fp4_word(const float* v) {
+// The magnitude codes of eight values (times a power of two), rounded to
+// nearest, ties to even, at most 6.
+__device__ __forceinline__ uint32_t fp4_codes(const float* v) {
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -58,8 +58,13 @@ __device__ __forceinline__ uint32_t fp4_word(const float* v) {
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(w)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-  const uint32_t a = prmt(w, 0, 0x1100), b = prmt(w, 0, 0x3322);    // signs in bits 3 and 7 of each pair of bytes
-  return (w & 0x77777777u) | (a << 4 & 0x00800080u) | (a & 0x80008000u) | (b & 0x00080008u) | (b >> 4 & 0x08000800u);
+  return w & 0x77777777u;
+}
+
+// The sign bits of a word, from its eight dims as BF16 pairs: those of values that
+// round to zero are kept.
+__device__ __forceinline__ uint32_t fp4_signs(const uint4& x) {
+  return (prmt(x.x, x.y, 0x7531) & 0x80808080u) | (prmt(x.z, x.w, 0x7531) >> 4 & 0x08080808u);
 }
 
 }  // namespace dsa

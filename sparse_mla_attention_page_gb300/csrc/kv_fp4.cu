@@ -14,17 +14,11 @@
 #include "dsa_common.cuh"
 #include "fp4_rows.cuh"
 #include "kernels.h"
-#include "row_codec.cuh"
 
 namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ uint32_t max_bits(uint32_t v, int lanes) {
-  for (int o = lanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -53,27 +47,32 @@ __device__ __forceinline__ void divide8(float* v, float s) {
     uint64_t q = fma2(x, r, 0ull);
     q = fma2(fma2(n, q, x), r, q);
     q = fma2(fma2(n, q, x), r, q);
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
-    v[k] = copysignf(a, v[k]);         // (a zero keeps its sign)
-    v[k + 1] = copysignf(b, v[k + 1]);
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[k]), "=f"(v[k + 1]) : "l"(q));
   }
 }
 
 // Eight dims of this lane (one of a block's two and a group's sixteen): their
 // word, the block's exponent nibble and the group's scale.
-__device__ __forceinline__ void quantise8(float* v, uint32_t& word, uint32_t& e, float& s) {
-  uint32_t top = 0;                    // as bits: a NaN is the largest
+__device__ __forceinline__ void quantise8(const uint4& x, uint32_t& word, uint32_t& e, float& s) {
+  // the group's largest magnitude, as 16-bit integers: a NaN is the largest
+  const uint32_t p[4] = {x.x, x.y, x.z, x.w};
+  uint32_t top = __vmaxu2(__vmaxu2(p[0] & 0x7FFF7FFFu, p[1] & 0x7FFF7FFFu), __vmaxu2(p[2] & 0x7FFF7FFFu, p[3] & 0x7FFF7FFFu));
+  top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-  const uint32_t group = max_bits(top, 16);
-  const bool odd = group >= 0x7F800000u;
-  s = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(__uint_as_float(group), kFp4Top);
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool odd = top >= 0x7F80u;
+  s = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(bf16_bits_to_f32(top), kFp4Top);
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(p[k] << 16);
+    v[2 * k + 1] = __uint_as_float(p[k] & 0xFFFF0000u);
+  }
   if (__all_sync(0xffffffffu, s >= 0x1p-80f && s <= 0x1p100f)) {
     divide8(v, s);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = odd || s == 0.f ? copysignf(0.f, v[k]) : __fdiv_rn(v[k], s);
+    for (int k = 0; k < 8; ++k) v[k] = odd || s == 0.f ? 0.f : __fdiv_rn(v[k], s);
   }
   float y = 0.f;                       // the block's largest quotient
 #pragma unroll
@@ -84,7 +83,7 @@ __device__ __forceinline__ void quantise8(float* v, uint32_t& word, uint32_t& e,
   const float up = __uint_as_float((127u + 5u - e) << 23);               // 2^(5 - e)
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] *= up;
-  word = fp4_word(v);
+  word = fp4_codes(v) | fp4_signs(x);
 }
 
 template <bool kRope>
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_fp4_kernel(const __grid_
   constexpr int kRow = kRope ? kFp4RopeRow : kFp4Row;
   const int lane = threadIdx.x & 31;
   const int64_t n_warps = ((int64_t)gridDim.x * kThreads) >> 5;
-  auto put = [&](int64_t slot, Row16& r, uint32_t rope) {
+  auto put = [&](int64_t slot, const uint4 (&x)[2], uint32_t rope) {
     if (slot < 0) return;
     if (slot >= a.pool_rows) {
       if (lane == 0) set_err(a.err, DSA_DEV_ERR_SLOT_RANGE);
@@ -102,35 +101,40 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_fp4_kernel(const __grid_
     uint32_t w[2], e[2];
     float s[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) quantise8(r.v + 8 * h, w[h], e[h], s[h]);
+    for (int h = 0; h < 2; ++h) quantise8(x[h], w[h], e[h], s[h]);
     uint8_t* row = a.pool + slot * kRow;
     reinterpret_cast<uint32_t*>(row)[lane] = w[0];
     reinterpret_cast<uint32_t*>(row + 128)[lane] = w[1];
     if (kRope) reinterpret_cast<uint32_t*>(row + kFp4Row)[lane] = rope;
     // nibble l / 2 of each half, from both lanes of a block
     const int at = (lane >> 1 & 7) * 4;
-    uint4 x;
-    x.x = __reduce_or_sync(0xffffffffu, lane < 16 ? e[0] << at : 0u);
-    x.y = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : e[0] << at);
-    x.z = __reduce_or_sync(0xffffffffu, lane < 16 ? e[1] << at : 0u);
-    x.w = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : e[1] << at);
+    uint4 n;
+    n.x = __reduce_or_sync(0xffffffffu, lane < 16 ? e[0] << at : 0u);
+    n.y = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : e[0] << at);
+    n.z = __reduce_or_sync(0xffffffffu, lane < 16 ? e[1] << at : 0u);
+    n.w = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : e[1] << at);
     const float s1 = __shfl_sync(0xffffffffu, s[0], 16), s3 = __shfl_sync(0xffffffffu, s[1], 16);
     if (lane == 0) {
       *reinterpret_cast<float4*>(row + kFp4Scales) = make_float4(s[0], s1, s[1], s3);
-      *reinterpret_cast<uint4*>(row + kFp4Exps) = x;
+      *reinterpret_cast<uint4*>(row + kFp4Exps) = n;
     }
   };
   auto rope_of = [&](int64_t i) {
     return kRope ? __ldcs(reinterpret_cast<const uint32_t*>(a.k_pe + i * a.k_pe_stride) + lane) : 0u;
+  };
+  auto load = [&](int64_t i, uint4 (&x)[2]) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.kv_c + i * a.kv_stride) + lane;
+    x[0] = __ldcs(p);
+    x[1] = __ldcs(p + 32);
   };
   // two rows per warp and pass, all loads issued before any is used
   for (int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i0 < a.n_rows; i0 += 2 * n_warps) {
     const int64_t i1 = i0 + n_warps;
     const bool two = i1 < a.n_rows;
     const int64_t s0 = __ldg(a.slots + i0), s1 = two ? __ldg(a.slots + i1) : -1;
-    Row16 r0, r1;
-    load_row16(a.kv_c + i0 * a.kv_stride, lane, r0);
-    if (two) load_row16(a.kv_c + i1 * a.kv_stride, lane, r1);
+    uint4 r0[2], r1[2];
+    load(i0, r0);
+    if (two) load(i1, r1);
     const uint32_t p0 = rope_of(i0), p1 = two ? rope_of(i1) : 0u;
     put(s0, r0, p0);
     if (two) put(s1, r1, p1);
