@@ -1,5 +1,5 @@
 // Work list of the dense attention of new tokens, shared by the attention
-// kernel, its plan and the merge of split units (chunk_attn.cu,
+// kernel, its plan and the merge of split units (chunk_kernel.cuh,
 // chunk_plan.cuh, chunk_merge.cu).
 //
 // A unit is a group of up to NC consecutive query rows of one request (row =

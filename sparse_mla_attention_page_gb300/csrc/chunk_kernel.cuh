@@ -548,13 +548,19 @@ __device__ void producer_role(const ChunkWork& w, uint8_t* sm, Misc<kShared>& ms
 // expanding warps turn them into the E4M3 bytes of a 528-byte row (fp4_rows.cuh)
 // in a slot of the ring.  So what is on its way from memory takes half the room,
 // and a ring block the shorter way through expansion, scores, softmax and values.
-// us, 1024 tokens of 32 heads over 8192 (288 / 416 bytes) and 64 single tokens of
-// 16 heads over up to 8192 (288): 1280 / 1670 and 64.6 (528-byte rows one by one
-// 968 and 60.5, by TMA 853 and 58.5).  Tried before: six warps that load codes
-// into registers two blocks ahead and expand those 1990 / 2110 and 95; codes of two
-// blocks copied into the ring and expanded in place 1671 / 2255 and 75.  Staging
-// buffers 2 / 3 / 4 / 5, at 288 bytes: 1275 / 1296 / 1279 / 1345, 74.9 / 68.7 / 64.6
-// / 64.6.  Without the expansion's arithmetic: 1138 / 1609 and 61.6.
+// us, 1024 tokens of 32 heads over 8192 (288 / 416 bytes; with every unit expanding
+// for itself, see fp4_flat.cu) and 64 single tokens of 16 heads over up to 8192
+// (288): 1267 / 1661 and 64.6; 528- and 656-byte rows one by one 963 / 1205 and
+// 60.5, by TMA 849 / 1036 and 58.5, with seven and five ring blocks as here one by
+// one 1171 / 1393.  What is left over those is about 650 instructions of each
+// expanding warp a tile beside the softmax.  Tried: six warps that load codes into
+// registers two blocks ahead and expand those, 1990 / 2110 and 95; codes of two
+// blocks copied into the ring and expanded there, 1671 / 2255 and 75, or of one in
+// a longer ring, 1287 / 1846 and 65.7; TMA for the copies, 1416 / 1687 and 66.7 (its
+// writes need a proxy fence behind the reads of a buffer, too); four copying and
+// two expanding warps, 1510 / 1836 and 79; 2 / 3 / 5 staging buffers, at 288 bytes
+// 1275 / 1296 / 1345 and 74.9 / 68.7 / 64.6.  Without the expansion's arithmetic:
+// 1138 / 1609 and 61.6.
 template <int NC, int kLayout, bool kShared>
 __device__ void fp4_copy_role(const ChunkWork& w, uint8_t* sm, Misc<kShared>& ms, const Range& rg) {
   using C = Cfg<NC, kLayout, false, kShared>;

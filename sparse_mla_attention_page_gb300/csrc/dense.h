@@ -1,6 +1,6 @@
 // Internal launch interface of the dense serving operators: page tables and
 // slot maps (pages.cu), rotary positions (rope.cu) and the attention of new
-// tokens over everything in the paged pool (chunk_attn.cu).
+// tokens over everything in the paged pool (chunk_attn.cu, prefix_attn.cu).
 #pragma once
 #include <cstddef>
 #include <cstdint>

@@ -5,7 +5,9 @@
 //   out[cu_b + i][d] = bf16(fp32(value of the code of dim d) * s_g),
 // then the 64 RoPE dims as stored, where the layout has them.
 //
-// HBM-bound: R bytes read and 1024 (1152) written a row.  A warp takes a run of
+// HBM-bound: R bytes read and 1024 (1152) written a row: 113000 rows of 416 bytes
+// take 33.6 us, 5.3 TB/s of mixed reads and writes, 79 % of the copy rate.  (With six
+// blocks an SM in place of four the registers spilled: 39 us.)  A warp takes a run of
 // up to 32 rows: each lane finds one row's request (a search in the offsets,
 // which lie in shared memory) and page, then four rows at a time are
 // loaded before any is used, lane l converting dims [8 l, 8 l + 8) and 256 + the
