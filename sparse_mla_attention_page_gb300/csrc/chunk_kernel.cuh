@@ -149,7 +149,6 @@ struct Cfg {
   static constexpr bool kFp4 = kLayout == DSA_KV_FP4_288 || kLayout == DSA_KV_FP4_416;
   static constexpr bool kRope = kLayout == DSA_KV_ROPE656 || kLayout == DSA_KV_FP4_416;
   static constexpr int R = row_bytes(kLayout);
-  static constexpr int ROPE_AT = kFp4 ? kFp4Row : kScaledRow;    // byte of a row
   static_assert(!(kFp4 && kTma), "4-bit rows are expanded by threads");
   static constexpr int CPT = NC / 4;                 // query columns of a softmax thread
   // Registers: the launch gives every thread LAUNCH_REGS; the softmax warps

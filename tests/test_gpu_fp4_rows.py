@@ -307,6 +307,34 @@ def test_written_and_read_back_in_a_graph():
         assert np.array_equal(bits(out[:n]), bits(expected(rows, "fp4_416"))) and (out[n:] == 3.0).all()
 
 
+def test_rows_behind_32_bits():
+    """A pool of more than 2^31 bytes: rows written, read and attended at its end as in a small one."""
+    n, page, kv = 5_400_000, 64, 300
+    big = torch.empty(n, 416, dtype=torch.uint8, device="cuda")
+    small = torch.zeros(8 * page, 416, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x, pe = torch.randn(kv, 512, generator=g, device="cuda").to(BF), torch.randn(kv, 64, generator=g, device="cuda").to(BF)
+    q = torch.randn(2, 16, 576, generator=g, device="cuda").to(BF)
+    cu, lens = torch.tensor([0, 2], **I32), torch.tensor([kv], **I32)
+    outs = []
+    for pool, first in ((big, n // page - 8), (small, 0)):
+        table = (first + torch.arange(7, -1, -1, **I32))[None].contiguous()
+        j = torch.arange(kv, device="cuda")
+        slots = table[0].long()[j // page] * page + j % page
+        binding.dsa_kv_write_fp4(x, slots, pool, k_pe=pe)
+        out = torch.zeros(kv, 576, dtype=BF, device="cuda")
+        binding.dsa_kv_read(pool, "fp4_416", table, page, torch.tensor([0, kv], **I32), out)
+        o, lse = torch.zeros(2, 16, 512, dtype=BF, device="cuda"), torch.zeros(2, 16, device="cuda")
+        binding.dsa_chunk_attn(q, pool, "fp4_416", table, page, cu, lens, 0.04, o, lse, binding.chunk_workspace_for(2, 16, 1, "fp4_416"))
+        big_call = torch.zeros(600, 16, 512, dtype=BF, device="cuda")          # (whose rows are expanded first)
+        binding.dsa_chunk_attn(q[:1].expand(600, 16, 576).contiguous(), pool, "fp4_416", table, page, torch.tensor([0, 600], **I32),
+                               lens, 0.04, big_call, torch.zeros(600, 16, device="cuda"),
+                               binding.chunk_workspace_for(600, 16, 1, "fp4_416"), causal=False)
+        outs.append((out, o, lse, big_call))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and (a != 0).any()
+
+
 def test_binding_refusals():
     x, pool = torch.zeros(4, 512, dtype=BF, device="cuda"), torch.zeros(8, 288, dtype=torch.uint8, device="cuda")
     slots, out = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, 512, dtype=BF, device="cuda")

@@ -314,6 +314,22 @@ def test_nan_rows(layout):
     assert err == 0 and lse[2].isnan().all() and torch.isfinite(lse[rest]).all() and torch.isfinite(o[rest].float()).all()
 
 
+@pytest.mark.parametrize("layout", ["raw512", "rope656"])
+def test_nan_and_zero_queries(layout):
+    """A query row with a NaN or an infinity scores NaN and leaves the rows that it is packed with alone; zero rows average."""
+    p = common(8)
+    w = make([(p, ONE)], 8, layout, seed=28)
+    w["q"][3, 2, 17], w["q"][5, 0, 300], w["q"][6] = math.nan, -math.inf, 0.0
+    o, lse, err = run(w, table=hide_shared(w, [p]))
+    assert err == 0
+    bad = torch.zeros(len(ONE), 8, dtype=torch.bool)
+    bad[3, 2] = bad[5, 0] = True
+    assert lse[bad].isnan().all() and o[bad].isnan().all()
+    w["q"][3, 2, 17] = w["q"][5, 0, 300] = 0.0
+    ro, rl, otol, ltol, _ = ref.chunk_attn(w["q"], w["pool"], layout, w["table"], 64, w["cu"], w["kv"], SCALE)
+    assert ((o.double() - ro).abs() <= otol)[~bad].all() and ((lse.double() - rl).abs() <= ltol)[~bad].all()
+
+
 def test_captured_steps():
     """A captured call serves other lengths, groups and prefixes, with a workspace that eager calls use as well."""
     p, B = common(8), len(ONE)
