@@ -99,12 +99,12 @@ struct ChunkWork {
 // Sharing is for batches of few query rows a request; at most so many on average
 // (eight units each: packing rows could save one of them at most).
 constexpr int kSharedRows = 256;
-// What all groups together have to save, a CTA: about four tiles, for the join.
-// us with / without sharing, 16 heads over raw rows, by the tiles saved: 64 single
+// What all groups together could save, a CTA, for a call to go to the shared
+// kernel and the join: about four tiles.  us there / on the dense path, 16 heads over raw rows, by the tiles saved: 64 single
 // tokens behind 2048 (2.9) 31.0 / 28.7, 4096 (6.2) 33.2 / 35.2, 8192 (13) 43.4 /
 // 51.5, 32768 (54) 90.6 / 144.9; four behind 32768 (3.4) 26.9 / 25.0.
 constexpr int kJoinCost = 4 * kTileCost;
-// Whether the groups could: packing rows saves less than a unit a request, of
+// Whether they could: packing rows saves less than a unit a request, of
 // the tiles that the page table has room for.
 inline bool sharing_possible(const ChunkArgs& a, int ctas) {
   return (int64_t)a.T * a.H <= (int64_t)a.B * kSharedRows &&

@@ -89,10 +89,16 @@ struct Groups {
 // A group shares a whole number of tiles of its prefix, at most what its first
 // tokens all see, and only where packing its rows takes less than each request
 // reading those tiles for itself (the cost of a unit counted as the ranges do).
-// All groups together have to save what joining the rows takes (kJoinCost).  Requests with lengths out of range end the sharing of their group, offsets out
+// However little that is: with a call in this kernel the rows are joined anyway,
+// and not sharing (each request's keys in units of 32 rows) only takes longer.
+// us with sharing / without, 64 single tokens of 16 heads behind 512 keys: raw
+// 24.6 / 26.7, 656-byte rows 30.8 / 31.9, 416-byte rows 36.9 / 36.9; behind 2048:
+// 28.8 / 32.7, 39.0 / 43.0, 47.2 / 53.7.  (At 256 keys of 416-byte rows and 8
+// heads 32.8 / 30.8, the one of 36 such cases that loses more than the noise.)
+// Requests with lengths out of range end the sharing of their group, offsets out
 // of order that of all.
 template <int THREADS>
-__device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch, int64_t* sums) {
+__device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scratch) {
   const ChunkArgs& a = w.a;
   const int tid = threadIdx.x, G = a.G;
   int32_t* cu = scratch;
@@ -127,7 +133,6 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
     }
     __syncthreads();
   }
-  int64_t saved = 0;
   for (int i = tid; i < G; i += THREADS) {
     const int tiles = g.first[i] == INT32_MAX ? 0 : min(g.keys[i], __ldg(a.prefix_lens + i)) / kChunkTile;
     int keys = 0;
@@ -135,17 +140,10 @@ __device__ __forceinline__ Groups find_groups(const ChunkWork& w, int32_t* scrat
       const int n = __ldg(a.cu_q + cu[i + 1]) - __ldg(a.cu_q + cu[i]);
       const int64_t apart = (int64_t)g.units[i] * tiles * kTileCost;
       const int64_t packed = (int64_t)unit_count(a, n, w.nc) * (tiles * kTileCost + w.unit_cost);
-      if (packed < apart) {
-        keys = tiles * kChunkTile;
-        saved += apart - packed;
-      }
+      if (packed < apart) keys = tiles * kChunkTile;
     }
     g.keys[i] = keys;
   }
-  int64_t all;
-  block_scan<THREADS>(saved, &all, sums);
-  if (all < (int64_t)w.grid * kJoinCost)
-    for (int i = tid; i < G; i += THREADS) g.keys[i] = 0;
   __syncthreads();
   return g;
 }
@@ -180,7 +178,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkWork& w, uint8_t* scratch,
   Unit<kShared>* units = units_of<kShared>(w);
   const int N = kShared ? a.B + a.G : a.B;         // parts: the requests, then the groups' prefixes
   Groups groups{};
-  if constexpr (kShared) groups = find_groups<THREADS>(w, first_unit + N, sums);
+  if constexpr (kShared) groups = find_groups<THREADS>(w, first_unit + N);
   int err = 0;
   auto part = [&](int p) -> Part {
     Part x{};

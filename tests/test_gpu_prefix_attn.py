@@ -62,7 +62,7 @@ def make(groups, H, layout, page=64, seed=0, alone=((), ()), lead=0, tail=0, qam
 
 def enough(H, news, sms=152):
     """Keys of a prefix that pays for news[b] new tokens of the group's requests: packing their rows saves a unit's tiles
-    as often as units get fewer, and has to save four tiles a CTA, beside what a packed unit costs (below three tiles)."""
+    as often as units get fewer, and is more than enough at four tiles a CTA, beside what a packed unit costs (below three tiles)."""
     units, packed = sum(-(-n * H // 32) for n in news), -(-sum(news) * H // 32)
     return 128 * -(-(4 * sms + 3 * packed) // (units - packed))
 
@@ -155,6 +155,16 @@ def test_prefix_lengths(layout, more):
     p = common(8, MIXED) + more
     check(make([(p, MIXED)], 8, layout, seed=p), hidden=[p // 128 * 128] if more >= 0 else None)
     check(make([(1 + more // 2, MIXED[:5])], 8, layout, seed=p) if more > 0 else make([(500, MIXED[:5])], 8, layout, seed=p))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("p", [100, 130, 256, 400, 1000])
+def test_short_prefixes_in_a_wide_table(layout, p):
+    """The page table has room for a prefix that pays: a short one is shared too, from two tiles on (16 units' tiles against
+    four packed units' and their cost, below three tiles each)."""
+    w = make([(p, ONE)], 8, layout, seed=p)
+    w["table"] = torch.cat([w["table"], torch.full((len(ONE), common(8) // w["page"]), -1, dtype=torch.int32)], 1)
+    check(w, hidden=[p // 128 * 128] if p >= 256 else None)
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
