@@ -582,16 +582,18 @@ size_t dsa_prefix_attn_workspace_bytes(int T, int H, int B, int layout);
  * A prefix is used as far as it holds for the whole group: rounded down to 128
  * keys, at most what the first new token of each of its requests sees; and where
  * it pays: query rows (tokens x heads) are worked on 32 at a time, so that there is
- * something to save where requests have few of them (single or drafted tokens of a
- * few heads).  Otherwise, and for requests outside every group or in a group of
- * one, this is dsa_chunk_attn.  A call that could gain little by its sizes (more than
- * 256 query rows a request on average, or a page table without room for common keys
- * that save four passes over 128 keys a multiprocessor) does not look at the groups;
- * one that could, but whose groups share nothing, takes a fifth to a third longer
+ * something to save where requests' rows fill part of that (single or drafted tokens
+ * of a few heads; nothing where the heads are a multiple of 32).  Otherwise, and for
+ * requests outside every group or in a group of one, this is dsa_chunk_attn.  Most
+ * calls that could gain little by their sizes alone (T, H, B and the width of the page
+ * table: less than three passes over 128 keys a multiprocessor, or more than 256 query
+ * rows a request) are dsa_chunk_attn throughout and do not look at the groups;
+ * one that looks, but whose groups share nothing, takes a fifth to a third longer
  * than dsa_chunk_attn (8 to 14 us at 64 single tokens of 16 heads behind 2048 keys).
  *   group_cu_dev     [G + 1] int32 ascending within [0, B], prefix_lens_dev [G]
- *                    int32, at least 0, read on the GPU; otherwise
- *                    (DSA_DEV_ERR_LENGTH) the call's requests attend alone.
+ *                    int32, at least 0, read on the GPU; otherwise the call's
+ *                    requests attend alone (DSA_DEV_ERR_LENGTH where the call
+ *                    looks at the groups).
  *   G                0 (pointers may be NULL) to B;  B <= DSA_MAX_PREFIX_REQUESTS.
  *   workspace_dev    ws_bytes >= dsa_prefix_attn_workspace_bytes(T, H, B, layout).
  * Everything else as dsa_chunk_attn. */

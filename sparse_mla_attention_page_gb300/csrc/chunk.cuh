@@ -76,6 +76,7 @@ struct __align__(16) ChunkSplit {
   int32_t pad[2];
 };
 constexpr int kFewParts = 8;         // split units of up to so many parts are merged a thread for each 4 dims
+constexpr int kLoopParts = 24;       // rows of up to so many parts over prefix and own keys are joined so, kFewParts at a time
 constexpr int kMaxCtas = 1024;       // of the attention grid (one per SM); parts of a unit
 
 // Everything a call needs; the pointers from hdr on lie in the workspace.
@@ -100,15 +101,31 @@ struct ChunkWork {
 // (eight units each: packing rows could save one of them at most).
 constexpr int kSharedRows = 256;
 // What all groups together could save, a CTA, for a call to go to the shared
-// kernel and the join: about four tiles.  us there / on the dense path, 16 heads over raw rows, by the tiles saved: 64 single
-// tokens behind 2048 (2.9) 31.0 / 28.7, 4096 (6.2) 33.2 / 35.2, 8192 (13) 43.4 /
-// 51.5, 32768 (54) 90.6 / 144.9; four behind 32768 (3.4) 26.9 / 25.0.
-constexpr int kJoinCost = 4 * kTileCost;
-// Whether they could: packing rows saves less than a unit a request, of
-// the tiles that the page table has room for.
+// kernel and the join: three tiles.  us there / on the dense path of single tokens,
+// by the tiles that they save a CTA, about 2 / 3 / 4 / 6:
+//   64 of 4 heads    raw 18.7 / 15.8  19.3 / 18.1  19.5 / 19.3  20.6 / 21.6   656 bytes 23.4 / 19.6  23.2 / 22.2  22.1 / 22.9  25.0 / 27.0
+//   64 of 16 heads   raw 23.6 / 19.8  24.9 / 22.0  26.3 / 24.4  28.8 / 28.9   416 bytes 34.0 / 32.4  38.3 / 38.5  42.0 / 44.7  50.1 / 57.0
+//   16 of 8 heads    raw 19.4 / 20.9  23.5 / 22.1  23.7 / 23.3  24.9 / 26.7   656 bytes 23.1 / 23.7  27.3 / 25.8  27.3 / 27.5  29.6 / 32.8
+//   16 of 40 heads   raw 23.8 / 24.5  26.3 / 27.1  29.5 / 30.5  33.8 / 36.7   656 bytes 31.4 / 32.2  35.4 / 38.2  41.9 / 43.6  48.8 / 57.9
+//   64 of 48 heads   raw 37.9 / 24.3  41.6 / 30.2  44.2 / 40.0  52.3 / 50.0   416 bytes 62.3 / 52.4  75.2 / 71.6  86.9 / 86.6  109 / 116
+// (the last have a unit a CTA on the dense path, nothing spread).
+constexpr int kJoinCost = 3 * kTileCost;
+// Whether they could, by the sizes alone.  A request's rows are a multiple of
+// gcd(H, 32), so its last unit has at most 32 less that many columns to spare, and
+// packing saves no more than the units that the spare columns of all make up: none
+// where the heads are a multiple of 32.  Beside that: where the dense path spreads a
+// unit over so many CTAs that its merge goes by slices, but the join takes the
+// parts in a loop, the join alone makes up for the rest.  us there / on the dense path, raw rows:
+// 16 tokens of 32 heads behind 4096 22.0 / 33.7, 8192 27.2 / 38.6, 16 of 16 heads
+// behind 4864 22.1 / 26.5.  (64 of 32 heads, of two parts each: 38.9 / 36.6, 54.7 / 52.1.)
 inline bool sharing_possible(const ChunkArgs& a, int ctas) {
-  return (int64_t)a.T * a.H <= (int64_t)a.B * kSharedRows &&
-         (int64_t)(a.B - 1) * ((int64_t)a.max_pages * a.page_size / kChunkTile) * kTileCost >= (int64_t)ctas * kJoinCost;
+  const int64_t rows = (int64_t)a.T * a.H, tiles = (int64_t)a.max_pages * a.page_size / kChunkTile;
+  if (rows > (int64_t)a.B * kSharedRows) return false;
+  const int spare = 32 - (a.H % 32 == 0 ? 32 : a.H & -a.H);
+  if ((int64_t)a.B * spare / 32 * tiles * kTileCost >= (int64_t)ctas * kJoinCost) return true;
+  const int nc = chunk_columns(a.T, a.H, a.B);
+  const int64_t units = a.B * (((rows + a.B - 1) / a.B + nc - 1) / nc);
+  return units * kFewParts < ctas && units * kLoopParts >= ctas && (a.B - 1) * tiles >= 4 * (int64_t)ctas;
 }
 
 template <bool kShared>

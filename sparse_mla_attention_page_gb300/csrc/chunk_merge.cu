@@ -185,9 +185,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) chunk_merge_kernel(const __g
 
 // ---- rows that share a prefix
 
-// Rows of up to so many parts are joined by a thread for each 4 dims, kFewParts
+// Rows of up to kLoopParts parts are joined by a thread for each 4 dims, kFewParts
 // parts at a time; with more, which only few rows have, by slices.
-constexpr int kLoopParts = 24;
 
 // A unit of a request, and where its rows' parts over the prefix lie: those of
 // its first rows, and from column brk on those of the prefix's next unit.
