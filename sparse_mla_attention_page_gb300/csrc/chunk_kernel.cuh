@@ -205,9 +205,10 @@ struct Cfg {
   static_assert(MISC_OFF >= plan_scratch(kShared), "the plan's scratch lies in front");
   // a tile's rows are replaced kMeta tiles later, when its blocks are gone from the ring
   static_assert((NS - 1) / 4 + 1 < kMeta, "rows of a tile in use");
-  // (4-bit rows: when tile t's first codes are requested, block 4 t - NST is expanded, the last of tile t - 2 or
-  // a later one, so that 4 t - NST - NS is gone)
-  static_assert(NST + NS <= 4 * kMeta - 3 && NST <= kMaxStage, "rows of a tile in use");
+  // (4-bit rows: tile t's are written once the codes of block 4 t - NST are read, which a warp does before it waits
+  // for that block's slot: it has had the slot of the block before, so that 4 t - NST - 1 - NS is gone, which has to
+  // be the last block of tile t - kMeta or a later one)
+  static_assert(NST + NS <= 4 * kMeta - 4 && NST <= kMaxStage, "rows of a tile in use");
   static_assert(SMEM <= kSmemLimit && TMEM_USED <= 512 && P_GROUP % 1024 == 0 && QR_BYTES % 1024 == 0, "budgets");
 };
 
