@@ -20,8 +20,9 @@
  *  - Arguments are validated on the host before anything is launched.  On a
  *    non-zero status other than DSA_ERR_CUDA nothing was launched and no
  *    output was touched.  DSA_ERR_CUDA means a launch itself failed
- *    (cudaGetLastError); of a call that makes two, the first may run: its
- *    outputs are then undefined (after dsa_pages_extend and dsa_pages_release
+ *    (cudaGetLastError); of a call that makes several (up to five: a chunk over
+ *    4-bit rows), those before it may run: the call's outputs are then undefined
+ *    (after dsa_pages_extend, dsa_pages_release and dsa_pages_release_own
  *    also the page table and the stack, whose count was not moved), and the
  *    call is not to be repeated on them.
  *  - Data-dependent faults (a top-k index outside the pool or the page table,
@@ -90,7 +91,7 @@ enum {
   DSA_ERR_LAYOUT = 3,    /* unknown layout, or a layout this entry point refuses */
   DSA_ERR_ROW_WIDTH = 4, /* query width or KV row width is not 512 [P1 Modifications] */
   DSA_ERR_TOPK_PAD = 5,  /* top-k width is not a positive multiple of 128 [P3 Modifications] */
-  DSA_ERR_HEADS = 6,     /* head count not in {8, 16, 32, 64, 128} (dsa_chunk_attn: not in 1 to 1024) */
+  DSA_ERR_HEADS = 6,     /* head count not in {8, 16, 32, 64, 128} (dsa_chunk_attn, dsa_prefix_attn: not in 1 to 1024) */
   DSA_ERR_WORKSPACE = 7, /* workspace missing or smaller than dsa_sparse_attn_workspace_bytes */
   DSA_ERR_DEVICE = 8,    /* no current CUDA device of compute capability 10.3 */
   DSA_ERR_CUDA = 9,      /* a kernel launch failed; the call's outputs are undefined */
@@ -588,8 +589,9 @@ size_t dsa_prefix_attn_workspace_bytes(int T, int H, int B, int layout);
  * calls that could gain little by their sizes alone (T, H, B and the width of the page
  * table: less than three passes over 128 keys a multiprocessor, or more than 256 query
  * rows a request) are dsa_chunk_attn throughout and do not look at the groups;
- * one that looks, but whose groups share nothing, takes a fifth to a third longer
- * than dsa_chunk_attn (8 to 14 us at 64 single tokens of 16 heads behind 2048 keys).
+ * one that looks, but whose groups share nothing, takes a tenth to two fifths longer
+ * than dsa_chunk_attn (5 to 7 us at 64 single tokens of 16 heads over up to 2048 keys
+ * of their own).
  *   group_cu_dev     [G + 1] int32 ascending within [0, B], prefix_lens_dev [G]
  *                    int32, at least 0, read on the GPU; otherwise the call's
  *                    requests attend alone (DSA_DEV_ERR_LENGTH where the call

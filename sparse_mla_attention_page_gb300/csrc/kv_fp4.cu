@@ -7,9 +7,11 @@
 // at most 1 as the code 6 of the smaller exponent and by as much under the
 // larger one, which would cost the block's other dims a bit.
 //
-// 1024 (1152) bytes read and 288 (416) written a row; bound by the instructions
-// of the quantisation (some 270 a warp and row, issue 60 % busy): 131072 rows with
-// RoPE dims take 49 us, 4.2 TB/s, against 31 at the copy rate.  Dividing each value by
+// 1024 (1152) bytes read and 288 (416) written a row: 131072 rows with RoPE dims
+// take 49 us, 4.2 TB/s, against 31 at the copy rate.  Neither the issue slots (62 % busy,
+// some 270 instructions a warp and row) nor DRAM is full: a warp loads two rows,
+// quantises and stores them, and only then loads the next two, and 32 warps an SM do
+// not cover all of the wait.  Dividing each value by
 // itself and comparing it with every border took 1.5 times as long.  A warp per row, lane l
 // dims [8 l, 8 l + 8) and 256 + the same, so that each load instruction reads 512
 // contiguous bytes and each store writes 128 or more.  Two lanes hold a block,

@@ -12,7 +12,7 @@
 // 42 / 50, behind 32768 90 / 145, of 8 heads behind 8192 33 / 50; 96 requests of 2
 // tokens and 8 heads behind four prefixes of up to 6000 rows of 656 bytes 61 / 69;
 // 128 single tokens of 8 heads behind 32768 rows of 656 bytes 162 / 376, of 416
-// 233 / 692.  (32 and more heads fill the tiles by themselves: nothing is shared.)
+// 233 / 692.  (Multiples of 32 heads fill the units by themselves: nothing is shared.)
 #include "chunk_kernel.cuh"
 
 namespace dsa {
