@@ -113,11 +113,16 @@ constexpr int kJoinCost = 3 * kTileCost;
 // Whether they could, by the sizes alone.  A request's rows are a multiple of
 // gcd(H, 32), so its last unit has at most 32 less that many columns to spare, and
 // packing saves no more than the units that the spare columns of all make up: none
-// where the heads are a multiple of 32.  Beside that: where the dense path spreads a
-// unit over so many CTAs that its merge goes by slices, but the join takes the
-// parts in a loop, the join alone makes up for the rest.  us there / on the dense path, raw rows:
-// 16 tokens of 32 heads behind 4096 22.0 / 33.7, 8192 27.2 / 38.6, 16 of 16 heads
-// behind 4864 22.1 / 26.5.  (64 of 32 heads, of two parts each: 38.9 / 36.6, 54.7 / 52.1.)
+// where the heads are a multiple of 32.  Beside that: where the dense path spreads
+// long units over so many CTAs that its merge goes by slices, but the join takes the
+// parts in a loop, the join alone makes up for the rest, whatever is shared.  us there /
+// on the dense path, behind 12 / 24 / 80 tiles:
+//   16 of 32 heads   raw 18.3 / 19.2  20.4 / 32.8  28.2 / 40.4   656 bytes 22.8 / 31.2  25.8 / 37.6  42.0 / 53.0
+//   4 of 64 heads    raw 18.7 / 23.7  20.8 / 24.0  24.8 / 27.6   416 bytes 25.1 / 30.0  27.2 / 30.3  38.5 / 40.7
+//   16 of 16 heads   raw 18.7 / 15.5  19.8 / 24.8  24.9 / 31.6   656 bytes 22.4 / 22.9  23.6 / 27.7  33.1 / 37.9
+//   16 of 8 heads    raw 17.2 / 14.1  19.3 / 20.4  24.8 / 27.2   656 bytes 21.3 / 19.5  23.0 / 23.2  29.8 / 33.3
+//   10 of 16 heads   raw 17.9 / 19.7  19.8 / 20.8  24.4 / 25.1   656 bytes 21.4 / 21.9  23.9 / 23.3  29.6 / 29.9
+// (64 of 32 heads, of two parts each, behind 32 and 64 raw tiles 38.9 / 36.6, 54.7 / 52.1.)
 inline bool sharing_possible(const ChunkArgs& a, int ctas) {
   const int64_t rows = (int64_t)a.T * a.H, tiles = (int64_t)a.max_pages * a.page_size / kChunkTile;
   if (rows > (int64_t)a.B * kSharedRows) return false;
@@ -125,7 +130,7 @@ inline bool sharing_possible(const ChunkArgs& a, int ctas) {
   if ((int64_t)a.B * spare / 32 * tiles * kTileCost >= (int64_t)ctas * kJoinCost) return true;
   const int nc = chunk_columns(a.T, a.H, a.B);
   const int64_t units = a.B * (((rows + a.B - 1) / a.B + nc - 1) / nc);
-  return units * kFewParts < ctas && units * kLoopParts >= ctas && (a.B - 1) * tiles >= 4 * (int64_t)ctas;
+  return units * kFewParts < ctas && units * kLoopParts >= ctas && tiles >= kLoopParts;
 }
 
 template <bool kShared>

@@ -69,3 +69,13 @@ def test_bound_of_the_saving():
         w = make([], 48, "raw512", seed=1, alone=([(1, 20 + b) for b in range(64)], []))
         w["table"] = torch.cat([w["table"], torch.full((64, tiles * 2), -1, dtype=torch.int32)], 1)[:, :tiles * 2].contiguous()
         check(tangle(w), err_want=binding.DSA_DEV_ERR_LENGTH if looked else 0, only=[0, 31, 63])
+
+
+@pytest.mark.parametrize("B,H,layout", [(16, 32, "raw512"), (4, 64, "fp4_416"), (16, 16, "rope656"), (2, 128, "scaled528")])
+def test_few_long_units(B, H, layout):
+    """Units that would be spread over 9 to 24 SMs (of 152) go to the shared kernel from 24 tiles of the page table on."""
+    for tiles, looked in ((23, False), (24, True)):
+        w = make([], H, layout, seed=2, alone=([(1, tiles * 128 - 1 - 130 * b) for b in range(B)], []))
+        w["table"] = w["table"][:, :tiles * 2].contiguous()
+        w["gcu"], w["plens"] = torch.tensor([0, B + 1], dtype=torch.int32), torch.tensor([640], dtype=torch.int32)
+        check(w, err_want=binding.DSA_DEV_ERR_LENGTH if looked else 0, only=[0, B // 2, B - 1])
